@@ -16,13 +16,25 @@ Entry points (same names as the C ABI):
   ep_layout_dispatch_noalloc(prob, topk_idx, layout, x, recv_x, recv_scales=None,
                              stream=None)   (workspace: the library's device array)
   ep_combine(prob, expert_out, layout, topk_weights, y, stream=None)
+  ep_route(rt, logits, topk_idx, topk_weights, expert_bias=None, valid=None, stream=None)
+  ep_balance_workspace_bytes(rt)             -> bytes
+  ep_balance_loss(rt, logits, topk_idx, coef, counts, mean_prob, num_valid, loss,
+                  workspace, valid=None, stream=None)
+  ep_route_backward(rt, logits, topk_idx, d_logits, d_weights=None, coef=0.0,
+                    counts=None, num_valid=None, d_loss=None, valid=None, stream=None)
+  ep_expert_w4(prob, mm, rows, layout, codes, scales, out, row_scales=None, stream=None)
   ep_e4m3_encode(inp, out, stream=None)
   ep_strerror(code)
 
 Helpers that allocate with torch (plumbing, outside the computation):
-  Problem(...), Layout.empty(prob, device), alloc_workspace, alloc_recv.
+  Problem(...), Layout.empty(prob, device), alloc_workspace, alloc_recv,
+  Routing(...), ExpertW4(...).
 
-Prepared calls (prepare_layout / prepare_dispatch / prepare_combine) check
+The routing calls and ep_expert_w4 run on the GPU that holds their tensors,
+by default on that GPU's current stream; tensors on several devices are
+refused.
+
+Prepared calls (prepare_layout / prepare_dispatch / prepare_combine / ...) check
 and marshal the arguments once and return a callable that only issues the C
 call, for loops that launch the same problem many times.
 """
@@ -35,6 +47,9 @@ __all__ = [
     "alloc_workspace", "alloc_recv", "library_path", "load_library",
     "prepare_layout", "prepare_dispatch", "prepare_combine", "ep_layout_dispatch",
     "prepare_layout_dispatch", "ep_layout_dispatch_noalloc",
+    "Routing", "ExpertW4", "ep_route", "ep_balance_workspace_bytes", "ep_balance_loss",
+    "ep_route_backward", "ep_expert_w4", "prepare_route", "prepare_balance_loss",
+    "prepare_route_backward", "prepare_expert_w4",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -63,6 +78,46 @@ class Problem(ctypes.Structure):
     def __repr__(self):
         return (f"Problem(T={self.num_tokens}, H={self.hidden}, k={self.num_topk}, "
                 f"E={self.num_experts}, cap={self.capacity}, fp8={self.use_fp8})")
+
+
+class Routing(ctypes.Structure):
+    """ep_routing: T, E, k, groups and how many of them a token may use, the
+    score ("softmax" / 0 or "sigmoid" / 1), whether a token's weights are
+    normalised, sequences of the balance loss, factor of the weights."""
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_experts", ctypes.c_int32),
+                ("num_topk", ctypes.c_int32), ("num_groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("normalize", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+                ("weight_scale", ctypes.c_float)]
+
+    def __init__(self, num_tokens, num_experts, num_topk, num_groups=1, topk_groups=1,
+                 score="softmax", normalize=True, num_seqs=1, weight_scale=1.0):
+        if isinstance(score, str):
+            if score not in ("softmax", "sigmoid"):
+                raise ValueError(f"score is {score!r}, expected 'softmax' or 'sigmoid'")
+            score = int(score == "sigmoid")
+        super().__init__(num_tokens, num_experts, num_topk, num_groups, topk_groups, score,
+                         int(normalize), num_seqs, weight_scale)
+
+    def __repr__(self):
+        return (f"Routing(T={self.num_tokens}, E={self.num_experts}, k={self.num_topk}, "
+                f"groups={self.topk_groups}/{self.num_groups}, "
+                f"score={'sigmoid' if self.score else 'softmax'}, normalize={self.normalize}, "
+                f"seqs={self.num_seqs}, scale={self.weight_scale})")
+
+
+class ExpertW4(ctypes.Structure):
+    """ep_expert_w4_t: K inputs, N outputs, format of the rows (0 bf16, 1 and 2
+    E4M3FN as Problem.use_fp8) and activation (0 none, 1 silu(gate) * up)."""
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
+                ("in_format", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+    def __init__(self, in_features, out_features, in_format=0, activation=0):
+        super().__init__(in_features, out_features, int(in_format), int(activation))
+
+    def __repr__(self):
+        return (f"ExpertW4(K={self.in_features}, N={self.out_features}, "
+                f"format={self.in_format}, activation={self.activation})")
 
 
 class _LayoutPtrs(ctypes.Structure):
@@ -104,6 +159,18 @@ def load_library():
     lib.ep_layout_dispatch_noalloc.argtypes = [P, vp, L, vp, vp, vp, vp]
     lib.ep_combine.restype = ctypes.c_int
     lib.ep_combine.argtypes = [P, vp, L, vp, vp, vp]
+    RT, i32, f32 = ctypes.POINTER(Routing), ctypes.c_int, ctypes.c_float
+    lib.ep_route.restype = ctypes.c_int
+    lib.ep_route.argtypes = [RT, vp, i32, i64, vp, vp, vp, vp, vp]
+    lib.ep_balance_workspace_bytes.restype = i64
+    lib.ep_balance_workspace_bytes.argtypes = [RT]
+    lib.ep_balance_loss.restype = ctypes.c_int
+    lib.ep_balance_loss.argtypes = [RT, vp, i32, i64, vp, vp, f32, vp, vp, vp, vp, vp,
+                                    ctypes.c_size_t, vp]
+    lib.ep_route_backward.restype = ctypes.c_int
+    lib.ep_route_backward.argtypes = [RT, vp, i32, i64, vp, vp, vp, f32, vp, vp, vp, vp, vp]
+    lib.ep_expert_w4.restype = ctypes.c_int
+    lib.ep_expert_w4.argtypes = [P, ctypes.POINTER(ExpertW4), vp, vp, L, vp, vp, vp, vp]
     lib.ep_e4m3_encode.restype = ctypes.c_int
     lib.ep_e4m3_encode.argtypes = [vp, vp, i64, vp]
     lib.ep_strerror.restype = ctypes.c_char_p
@@ -365,3 +432,225 @@ def prepare_layout_dispatch(prob, topk_idx, layout, workspace, x, recv_x, recv_s
     s, args = _layout_dispatch_args(prob, topk_idx, layout, workspace, x, recv_x, recv_scales)
     return _Prepared("ep_layout_dispatch", lib.ep_layout_dispatch, args,
                      (prob, s, topk_idx, layout, workspace, x, recv_x, recv_scales))
+
+
+# ------------------------------------------------- routing and expert products
+
+def _device_of(t, name):
+    """Index of the GPU that holds `t`."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be in GPU memory")
+    return dev
+
+
+def _arg(t, name, dtype, numel, dev, allow_none=False):
+    """Pointer of a contiguous tensor of `numel` elements on device `dev`."""
+    if t is None and allow_none:
+        return None
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.numel() != numel:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be in GPU memory, on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _issue(name, fn, args, dev, stream):
+    """The C call on device `dev`, on its current stream by default."""
+    torch = _torch()
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        code = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, handle)
+    if code != EP_OK:
+        raise EpError(name, code)
+
+
+class _PreparedOn(_Prepared):
+    """A prepared call that runs on the device of its tensors."""
+
+    def __init__(self, name, fn, args, dev, keep):
+        super().__init__(name, fn, args, keep)
+        self._dev = dev
+
+    def __call__(self, stream=None):
+        _issue(self.name, self._fn, self._args, self._dev, stream)
+
+
+def _logits_args(rt, logits):
+    """Device, element type and row pitch of [T, E] logits, rows of any pitch."""
+    torch = _torch()
+    dev = _device_of(logits, "logits")
+    if logits.dtype is torch.bfloat16:
+        bf16 = 1
+    elif logits.dtype is torch.float32:
+        bf16 = 0
+    else:
+        raise TypeError(f"logits has dtype {logits.dtype}, expected float32 or bfloat16")
+    T, E = rt.num_tokens, rt.num_experts
+    if logits.dim() != 2 or logits.shape[0] != T or logits.shape[1] != E:
+        raise ValueError(f"logits has shape {tuple(logits.shape)}, expected {(T, E)}")
+    stride, inner = logits.stride()
+    if inner != 1 and E > 1:
+        raise ValueError("logits must be contiguous along the experts")
+    if T <= 1:
+        stride = max(stride, E)
+    if stride < E:
+        raise ValueError(f"logits rows overlap: row pitch {stride} below {E}")
+    return dev, logits.data_ptr(), bf16, stride
+
+
+def _valid_arg(rt, valid, dev):
+    torch = _torch()
+    return _arg(valid, "valid", (torch.uint8, torch.bool), rt.num_tokens, dev, allow_none=True)
+
+
+def _route_args(rt, logits, topk_idx, topk_weights, expert_bias, valid):
+    torch = _torch()
+    dev, lp, bf16, stride = _logits_args(rt, logits)
+    n = rt.num_tokens * rt.num_topk
+    bp = _arg(expert_bias, "expert_bias", torch.float32, rt.num_experts, dev, allow_none=True)
+    vp = _valid_arg(rt, valid, dev)
+    ip = _arg(topk_idx, "topk_idx", torch.int32, n, dev)
+    wp = _arg(topk_weights, "topk_weights", torch.float32, n, dev)
+    return dev, (ctypes.byref(rt), lp, bf16, stride, bp, vp, ip, wp)
+
+
+def ep_route(rt, logits, topk_idx, topk_weights, expert_bias=None, valid=None, stream=None):
+    lib = _lib or load_library()
+    dev, args = _route_args(rt, logits, topk_idx, topk_weights, expert_bias, valid)
+    _issue("ep_route", lib.ep_route, args, dev, stream)
+
+
+def prepare_route(rt, logits, topk_idx, topk_weights, expert_bias=None, valid=None):
+    lib = load_library()
+    dev, args = _route_args(rt, logits, topk_idx, topk_weights, expert_bias, valid)
+    return _PreparedOn("ep_route", lib.ep_route, args, dev,
+                       (rt, logits, topk_idx, topk_weights, expert_bias, valid))
+
+
+def ep_balance_workspace_bytes(rt):
+    return int(load_library().ep_balance_workspace_bytes(ctypes.byref(rt)))
+
+
+def _balance_args(rt, logits, topk_idx, coef, counts, mean_prob, num_valid, loss, workspace,
+                  valid):
+    torch = _torch()
+    dev, lp, bf16, stride = _logits_args(rt, logits)
+    T, E, B = rt.num_tokens, rt.num_experts, rt.num_seqs
+    ip = _arg(topk_idx, "topk_idx", torch.int32, T * rt.num_topk, dev)
+    vp = _valid_arg(rt, valid, dev)
+    cp = _arg(counts, "counts", torch.int32, B * E, dev)
+    mp = _arg(mean_prob, "mean_prob", torch.float32, B * E, dev)
+    np_ = _arg(num_valid, "num_valid", torch.int32, B, dev)
+    op = _arg(loss, "loss", torch.float32, 1, dev)
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    wp = _arg(workspace, "workspace", workspace.dtype, workspace.numel(), dev)
+    nbytes = workspace.numel() * workspace.element_size()
+    return dev, (ctypes.byref(rt), lp, bf16, stride, ip, vp, coef, cp, mp, np_, op, wp, nbytes)
+
+
+def ep_balance_loss(rt, logits, topk_idx, coef, counts, mean_prob, num_valid, loss, workspace,
+                    valid=None, stream=None):
+    lib = _lib or load_library()
+    dev, args = _balance_args(rt, logits, topk_idx, coef, counts, mean_prob, num_valid, loss,
+                              workspace, valid)
+    _issue("ep_balance_loss", lib.ep_balance_loss, args, dev, stream)
+
+
+def prepare_balance_loss(rt, logits, topk_idx, coef, counts, mean_prob, num_valid, loss, workspace,
+                         valid=None):
+    lib = load_library()
+    dev, args = _balance_args(rt, logits, topk_idx, coef, counts, mean_prob, num_valid, loss,
+                              workspace, valid)
+    return _PreparedOn("ep_balance_loss", lib.ep_balance_loss, args, dev,
+                       (rt, logits, topk_idx, counts, mean_prob, num_valid, loss, workspace, valid))
+
+
+def _route_backward_args(rt, logits, topk_idx, d_logits, d_weights, coef, counts, num_valid,
+                         d_loss, valid):
+    torch = _torch()
+    dev, lp, bf16, stride = _logits_args(rt, logits)
+    T, E, B = rt.num_tokens, rt.num_experts, rt.num_seqs
+    n = T * rt.num_topk
+    if d_weights is None and d_loss is None:
+        raise ValueError("d_weights or d_loss is required")
+    if d_weights is not None and topk_idx is None:
+        raise ValueError("topk_idx is required with d_weights")
+    if d_loss is not None and (counts is None or num_valid is None):
+        raise ValueError("counts and num_valid are required with d_loss")
+    ip = _arg(topk_idx, "topk_idx", torch.int32, n, dev, allow_none=True)
+    gp = _arg(d_weights, "d_weights", torch.float32, n, dev, allow_none=True)
+    vp = _valid_arg(rt, valid, dev)
+    cp = _arg(counts, "counts", torch.int32, B * E, dev, allow_none=True)
+    np_ = _arg(num_valid, "num_valid", torch.int32, B, dev, allow_none=True)
+    sp = _arg(d_loss, "d_loss", torch.float32, 1, dev, allow_none=True)
+    dp = _arg(d_logits, "d_logits", logits.dtype, T * E, dev)
+    return dev, (ctypes.byref(rt), lp, bf16, stride, ip, gp, vp, coef, cp, np_, sp, dp)
+
+
+def ep_route_backward(rt, logits, topk_idx, d_logits, d_weights=None, coef=0.0, counts=None,
+                      num_valid=None, d_loss=None, valid=None, stream=None):
+    lib = _lib or load_library()
+    dev, args = _route_backward_args(rt, logits, topk_idx, d_logits, d_weights, coef, counts,
+                                     num_valid, d_loss, valid)
+    _issue("ep_route_backward", lib.ep_route_backward, args, dev, stream)
+
+
+def prepare_route_backward(rt, logits, topk_idx, d_logits, d_weights=None, coef=0.0, counts=None,
+                           num_valid=None, d_loss=None, valid=None):
+    lib = load_library()
+    dev, args = _route_backward_args(rt, logits, topk_idx, d_logits, d_weights, coef, counts,
+                                     num_valid, d_loss, valid)
+    return _PreparedOn("ep_route_backward", lib.ep_route_backward, args, dev,
+                       (rt, logits, topk_idx, d_logits, d_weights, counts, num_valid, d_loss, valid))
+
+
+def _expert_w4_args(prob, mm, rows, layout, codes, scales, out, row_scales):
+    torch = _torch()
+    dev = _device_of(rows, "rows")
+    R = ep_num_recv_rows(prob)
+    K, N, E, fmt = mm.in_features, mm.out_features, prob.num_experts, mm.in_format
+    n2 = 2 * N if mm.activation == 1 else N
+    u8 = torch.uint8
+    s = _LayoutPtrs()
+    s.count = _arg(layout.count, "count", torch.int32, E, dev)
+    s.offset = _arg(layout.offset, "offset", torch.int32, E + 1, dev)
+    if fmt == 0:
+        rp = _arg(rows, "rows", torch.bfloat16, R * K, dev)
+        sp = None
+    else:
+        rp = _arg(rows, "rows", (u8, torch.float8_e4m3fn), R * K, dev)
+        sp = _arg(row_scales, "row_scales", u8 if fmt == 2 else torch.float32, R * (K // 128), dev)
+    cp = _arg(codes, "codes", u8, E * n2 * (K // 2), dev)
+    wp = _arg(scales, "scales", u8, E * n2 * (K // 32), dev)
+    op = _arg(out, "out", torch.bfloat16, R * N, dev)
+    return dev, s, (ctypes.byref(prob), ctypes.byref(mm), rp, sp, ctypes.byref(s), cp, wp, op)
+
+
+def ep_expert_w4(prob, mm, rows, layout, codes, scales, out, row_scales=None, stream=None):
+    lib = _lib or load_library()
+    dev, _s, args = _expert_w4_args(prob, mm, rows, layout, codes, scales, out, row_scales)
+    _issue("ep_expert_w4", lib.ep_expert_w4, args, dev, stream)
+
+
+def prepare_expert_w4(prob, mm, rows, layout, codes, scales, out, row_scales=None):
+    lib = load_library()
+    dev, s, args = _expert_w4_args(prob, mm, rows, layout, codes, scales, out, row_scales)
+    return _PreparedOn("ep_expert_w4", lib.ep_expert_w4, args, dev,
+                       (prob, mm, s, rows, layout, codes, scales, out, row_scales))

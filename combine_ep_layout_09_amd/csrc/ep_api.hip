@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
 #include <mutex>
 
 #include "ep.h"
@@ -102,6 +103,61 @@ int check_layout_dispatch_args(const ep_problem* prob, const int32_t* topk_idx,
     if (!aligned16(x) || !aligned16(recv_x) || (prob->use_fp8 && !aligned16(recv_scales)))
         return EP_ERR_ALIGN;
     return EP_OK;
+}
+
+// Shape and row pitch of a routing problem.
+int check_routing(const ep_routing* rt) {
+    if (rt == nullptr) return EP_ERR_ARG;
+    if (rt->num_tokens < 0 || rt->num_experts < 1 || rt->num_topk < 1 || rt->num_groups < 1 ||
+        rt->topk_groups < 1 || rt->num_seqs < 1 || rt->score < 0 || rt->score > 1 ||
+        rt->normalize < 0 || rt->normalize > 1 || !std::isfinite(rt->weight_scale))
+        return EP_ERR_ARG;
+    if (rt->num_experts > ep::kMaxExperts || rt->num_topk > ep::kMaxTopk ||
+        rt->num_groups > ep::kMaxGroups || rt->num_seqs > ep::kMaxSeqs)
+        return EP_ERR_UNSUPPORTED;
+    if (rt->num_experts % rt->num_groups != 0 || rt->topk_groups > rt->num_groups ||
+        rt->num_topk > rt->topk_groups * (rt->num_experts / rt->num_groups) ||
+        rt->num_tokens % rt->num_seqs != 0)
+        return EP_ERR_ARG;
+    if (static_cast<int64_t>(rt->num_tokens) * rt->num_topk >= (int64_t{1} << 31))
+        return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+int check_logits(const ep_routing& rt, const void* logits, int bf16, int64_t stride) {
+    if (bf16 < 0 || bf16 > 1 || stride < rt.num_experts) return EP_ERR_ARG;
+    if (stride > (int64_t{1} << 31)) return EP_ERR_UNSUPPORTED;
+    if (rt.num_tokens > 0 && logits == nullptr) return EP_ERR_ARG;
+    if (reinterpret_cast<uintptr_t>(logits) % (bf16 ? 2 : 4) != 0) return EP_ERR_ALIGN;
+    return EP_OK;
+}
+
+ep::RouteArgs route_args(const ep_routing& rt, const void* logits, int bf16, int64_t stride,
+                         const void* d_logits) {
+    ep::RouteArgs a;
+    a.logits = logits;
+    a.stride = stride;
+    a.num_tokens = rt.num_tokens;
+    a.num_experts = rt.num_experts;
+    a.num_topk = rt.num_topk;
+    a.num_groups = rt.num_groups;
+    a.topk_groups = rt.topk_groups;
+    a.num_seqs = rt.num_seqs;
+    a.seq_len = rt.num_tokens / rt.num_seqs;
+    a.scale = rt.weight_scale;
+    a.bf16 = bf16 != 0;
+    a.sigmoid = rt.score == 1;
+    a.normalize = rt.normalize == 1;
+    const int el = bf16 ? 2 : 4;
+    const int vpl = ep::token_shape(rt.num_experts).vpl;
+    const int piece = vpl * el < 16 ? vpl : 16 / el;  // elements per access
+    const auto fits = [&](const void* p, int64_t pitch) {
+        return rt.num_experts % piece == 0 && pitch % piece == 0 &&
+               reinterpret_cast<uintptr_t>(p) % (piece * el) == 0;
+    };
+    a.pieces = fits(logits, stride);
+    a.out_pieces = fits(d_logits, rt.num_experts);
+    return a;
 }
 
 }  // namespace
@@ -203,6 +259,103 @@ int ep_e4m3_encode(const float* in, uint8_t* out, int64_t n, void* stream) {
     if (n > 0 && (in == nullptr || out == nullptr)) return EP_ERR_ARG;
     if (!aligned4(in)) return EP_ERR_ALIGN;
     return from_hip(ep::launch_e4m3_encode(in, out, n, static_cast<hipStream_t>(stream)));
+}
+
+int ep_route(const ep_routing* rt, const void* logits, int logits_bf16, int64_t logits_stride,
+             const float* expert_bias, const uint8_t* valid, int32_t* topk_idx,
+             float* topk_weights, void* stream) {
+    int rc = check_routing(rt);
+    if (rc != EP_OK) return rc;
+    rc = check_logits(*rt, logits, logits_bf16, logits_stride);
+    if (rc != EP_OK) return rc;
+    if (rt->num_tokens > 0 && (topk_idx == nullptr || topk_weights == nullptr)) return EP_ERR_ARG;
+    if (!aligned4(expert_bias) || !aligned4(topk_idx) || !aligned4(topk_weights))
+        return EP_ERR_ALIGN;
+    const ep::RouteForward f = {expert_bias, valid, topk_idx, topk_weights};
+    return from_hip(ep::launch_route(route_args(*rt, logits, logits_bf16, logits_stride, nullptr),
+                                     f, static_cast<hipStream_t>(stream)));
+}
+
+int64_t ep_balance_workspace_bytes(const ep_routing* rt) {
+    if (check_routing(rt) != EP_OK) return -1;
+    return ep::balance_workspace_bytes(rt->num_tokens, rt->num_experts, rt->num_seqs);
+}
+
+int ep_balance_loss(const ep_routing* rt, const void* logits, int logits_bf16,
+                    int64_t logits_stride, const int32_t* topk_idx, const uint8_t* valid,
+                    float coef, int32_t* counts, float* mean_prob, int32_t* num_valid,
+                    float* loss, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_routing(rt);
+    if (rc != EP_OK) return rc;
+    rc = check_logits(*rt, logits, logits_bf16, logits_stride);
+    if (rc != EP_OK) return rc;
+    if (!std::isfinite(coef)) return EP_ERR_ARG;
+    if (rt->num_tokens > 0 && topk_idx == nullptr) return EP_ERR_ARG;
+    if (counts == nullptr || mean_prob == nullptr || num_valid == nullptr || loss == nullptr)
+        return EP_ERR_ARG;
+    if (workspace == nullptr ||
+        static_cast<int64_t>(workspace_bytes) <
+            ep::balance_workspace_bytes(rt->num_tokens, rt->num_experts, rt->num_seqs))
+        return EP_ERR_ARG;
+    if (!aligned4(topk_idx) || !aligned4(counts) || !aligned4(mean_prob) || !aligned4(num_valid) ||
+        !aligned4(loss) || !aligned16(workspace))
+        return EP_ERR_ALIGN;
+    const ep::BalanceArgs b = {topk_idx, valid, coef, counts, mean_prob, num_valid, loss};
+    return from_hip(ep::launch_balance(route_args(*rt, logits, logits_bf16, logits_stride, nullptr),
+                                       b, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int ep_route_backward(const ep_routing* rt, const void* logits, int logits_bf16,
+                      int64_t logits_stride, const int32_t* topk_idx, const float* d_weights,
+                      const uint8_t* valid, float coef, const int32_t* counts,
+                      const int32_t* num_valid, const float* d_loss, void* d_logits,
+                      void* stream) {
+    int rc = check_routing(rt);
+    if (rc != EP_OK) return rc;
+    rc = check_logits(*rt, logits, logits_bf16, logits_stride);
+    if (rc != EP_OK) return rc;
+    if (!std::isfinite(coef)) return EP_ERR_ARG;
+    if (rt->num_tokens > 0) {
+        if (d_logits == nullptr || (d_weights == nullptr && d_loss == nullptr)) return EP_ERR_ARG;
+        if (d_weights != nullptr && topk_idx == nullptr) return EP_ERR_ARG;
+        if (d_loss != nullptr && (counts == nullptr || num_valid == nullptr)) return EP_ERR_ARG;
+    }
+    if (!aligned4(topk_idx) || !aligned4(d_weights) || !aligned4(counts) || !aligned4(num_valid) ||
+        !aligned4(d_loss) ||
+        reinterpret_cast<uintptr_t>(d_logits) % (logits_bf16 ? 2 : 4) != 0)
+        return EP_ERR_ALIGN;
+    const ep::RouteBackward b = {topk_idx, d_weights, valid, coef, counts, num_valid, d_loss,
+                                 d_logits};
+    return from_hip(ep::launch_route_backward(
+        route_args(*rt, logits, logits_bf16, logits_stride, d_logits), b,
+        static_cast<hipStream_t>(stream)));
+}
+
+int ep_expert_w4(const ep_problem* prob, const ep_expert_w4_t* mm, const void* rows,
+                 const void* row_scales, const ep_layout_t* layout, const uint8_t* codes,
+                 const uint8_t* scales, void* out, void* stream) {
+    int rc = check_problem(prob);
+    if (rc != EP_OK) return rc;
+    if (mm == nullptr || layout == nullptr) return EP_ERR_ARG;
+    if (mm->in_features < 1 || mm->out_features < 1 || mm->in_format < 0 || mm->in_format > 2 ||
+        mm->activation < 0 || mm->activation > 1)
+        return EP_ERR_ARG;
+    if (mm->in_features > ep::kMaxHidden || mm->out_features > ep::kMaxHidden ||
+        mm->in_features % (mm->in_format ? 128 : 32) != 0)
+        return EP_ERR_UNSUPPORTED;
+    if (layout->count == nullptr || (prob->capacity == 0 && layout->offset == nullptr))
+        return EP_ERR_ARG;
+    if (!aligned4(layout->count) || !aligned4(layout->offset)) return EP_ERR_ALIGN;
+    if (prob->num_tokens > 0) {
+        if (rows == nullptr || codes == nullptr || scales == nullptr || out == nullptr)
+            return EP_ERR_ARG;
+        if (mm->in_format && row_scales == nullptr) return EP_ERR_ARG;
+    }
+    if (!aligned16(rows) || !aligned16(codes) || !aligned16(scales) || !aligned16(out) ||
+        (mm->in_format && !aligned16(row_scales)))
+        return EP_ERR_ALIGN;
+    return from_hip(ep::launch_expert_w4(*prob, *mm, rows, row_scales, *layout, codes, scales, out,
+                                         static_cast<hipStream_t>(stream)));
 }
 
 const char* ep_strerror(int code) {

@@ -1,0 +1,213 @@
+// ep_balance.hip -- the balance loss of a routing with its per-expert counts.
+//
+//   p[t, e]   probability of expert e for token t (softmax, or sigmoid scores
+//             over their sum)
+//   c[s, e]   entries of sequence s's tokens that name expert e
+//   P[s, e]   mean of p[t, e] over the n_s tokens of the sequence
+//   loss = coef / B * sum_s sum_e E / (k n_s) c[s, e] P[s, e]
+//
+// First kernel: a workgroup per run of consecutive tokens of one sequence
+// adds its tokens' probabilities per expert in registers, its entries in an
+// LDS histogram, and writes both as one row of partial sums.  Second kernel: a
+// thread per (sequence, expert) adds the rows in order, in fp64.  Third: one
+// wave adds the per-workgroup parts of the loss.  No sum depends on the order
+// in which workgroups run.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ep_internal.h"
+#include "ep_route_dev.h"
+
+namespace ep {
+namespace {
+
+using namespace route;
+
+constexpr int kFinish = 256;
+
+struct Geometry {
+    int runs;        // runs of tokens per sequence
+    int run_tokens;  // tokens per run
+    int tiles;       // workgroups per sequence in the second kernel
+    int64_t probs, hist, live, part, bytes;  // workspace offsets and size
+};
+
+Geometry geometry(int T, int E, int B) {
+    Geometry g;
+    const int64_t len = T / B;
+    // About two workgroups per CU over all sequences, of 32 tokens at least.
+    int64_t runs = (512 + B - 1) / B;
+    const int64_t most = (len + 31) / 32;
+    if (runs > most) runs = most;
+    if (runs < 1) runs = 1;
+    g.run_tokens = static_cast<int>((len + runs - 1) / runs);
+    g.runs = g.run_tokens ? static_cast<int>((len + g.run_tokens - 1) / g.run_tokens) : 1;
+    g.tiles = (E + kFinish - 1) / kFinish;
+    const auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
+    const int64_t rows = static_cast<int64_t>(B) * g.runs;
+    g.probs = 0;
+    g.hist = up(g.probs + rows * E * 4);
+    g.live = up(g.hist + rows * E * 4);
+    g.part = up(g.live + rows * 4);
+    g.bytes = up(g.part + static_cast<int64_t>(B) * g.tiles * 8);
+    return g;
+}
+
+template <int LPT, int VPL, bool BF16>
+__global__ __launch_bounds__(kThreads) void balance_sum_kernel(RouteArgs a, const int32_t* topk_idx,
+                                                               const uint8_t* valid, int runs,
+                                                               int run_tokens, float* probs,
+                                                               int32_t* hist, int32_t* live_rows) {
+    constexpr int kTokens = kThreads / LPT;
+    constexpr int kWidth = LPT * VPL;
+    __shared__ float sums[kTokens][kWidth];
+    __shared__ int32_t counts[kWidth];
+    __shared__ int32_t live_count;
+    const int lane = threadIdx.x % LPT;
+    const int slot = threadIdx.x / LPT;
+    const int E = a.num_experts, k = a.num_topk;
+    const int64_t seq = blockIdx.x / runs;
+    const int run = blockIdx.x % runs;
+    const int begin = run * run_tokens;
+    const int end = min(begin + run_tokens, a.seq_len);
+    const int64_t t0 = seq * a.seq_len;
+    for (int e = threadIdx.x; e < kWidth; e += kThreads) counts[e] = 0;
+    if (threadIdx.x == 0) live_count = 0;
+    __syncthreads();
+
+    float acc[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
+    int mine = 0;
+    for (int base = begin; base < end; base += kTokens) {  // the same count for every wave
+        const int at = base + slot;
+        const int64_t t = t0 + at;
+        const bool live = at < end && (valid == nullptr || valid[t] != 0);
+        float x[VPL], z[VPL], slope[VPL], total;
+        load_logits<VPL, BF16>(a.logits, (live ? t : t0) * a.stride, live ? E : 0, lane * VPL,
+                               a.pieces, x);
+        scores<LPT, VPL>(x, a.sigmoid, z, slope, total);
+        const float r = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) acc[i] += z[i] * r;
+        if (live) {
+            if (lane == 0) ++mine;
+            for (int j = lane; j < k; j += LPT) {
+                const int id = topk_idx[t * k + j];
+                if (id >= 0 && id < E) atomicAdd(&counts[id], 1);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) sums[slot][lane * VPL + i] = acc[i];
+    if (mine) atomicAdd(&live_count, mine);
+    __syncthreads();
+    const int64_t out = static_cast<int64_t>(blockIdx.x) * E;
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+        float s = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kTokens; ++q) s += sums[q][e];
+        probs[out + e] = s;
+        hist[out + e] = counts[e];
+    }
+    if (threadIdx.x == 0) live_rows[blockIdx.x] = live_count;
+}
+
+__global__ __launch_bounds__(kFinish) void balance_mean_kernel(
+    int E, int tiles, int runs, const float* probs, const int32_t* hist, const int32_t* live_rows,
+    int32_t* counts, float* mean_prob, int32_t* num_valid, double* part) {
+    __shared__ double red[kFinish];
+    const int64_t seq = blockIdx.x / tiles;
+    const int tile = blockIdx.x % tiles;
+    const int e = tile * kFinish + threadIdx.x;
+    int n = 0;
+    for (int r = 0; r < runs; ++r) n += live_rows[seq * runs + r];
+    double term = 0.0;
+    if (e < E) {
+        double s = 0.0;
+        int c = 0;
+        for (int r = 0; r < runs; ++r) {
+            s += static_cast<double>(probs[(seq * runs + r) * E + e]);
+            c += hist[(seq * runs + r) * E + e];
+        }
+        const double mean = n ? s / n : 0.0;
+        counts[seq * E + e] = c;
+        mean_prob[seq * E + e] = static_cast<float>(mean);
+        if (n) term = mean * c / n;
+    }
+    if (tile == 0 && threadIdx.x == 0) num_valid[seq] = n;
+    red[threadIdx.x] = term;
+    __syncthreads();
+    for (int w = kFinish / 2; w > 0; w /= 2) {
+        if (static_cast<int>(threadIdx.x) < w) red[threadIdx.x] += red[threadIdx.x + w];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) part[blockIdx.x] = red[0];
+}
+
+__global__ __launch_bounds__(kFinish) void balance_loss_kernel(int64_t parts, const double* part,
+                                                               double factor, float* loss) {
+    __shared__ double red[kFinish];
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < parts; i += kFinish) s += part[i];
+    red[threadIdx.x] = s;
+    __syncthreads();
+    for (int w = kFinish / 2; w > 0; w /= 2) {
+        if (static_cast<int>(threadIdx.x) < w) red[threadIdx.x] += red[threadIdx.x + w];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) loss[0] = static_cast<float>(red[0] * factor);
+}
+
+template <int LPT, int VPL>
+void launch_sum(const RouteArgs& a, const BalanceArgs& b, const Geometry& g, char* ws,
+                hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(a.num_seqs) * g.runs);
+    float* probs = reinterpret_cast<float*>(ws + g.probs);
+    int32_t* hist = reinterpret_cast<int32_t*>(ws + g.hist);
+    int32_t* live = reinterpret_cast<int32_t*>(ws + g.live);
+    if (a.bf16)
+        hipLaunchKernelGGL((balance_sum_kernel<LPT, VPL, true>), grid, dim3(kThreads), 0, stream, a,
+                           b.topk_idx, b.valid, g.runs, g.run_tokens, probs, hist, live);
+    else
+        hipLaunchKernelGGL((balance_sum_kernel<LPT, VPL, false>), grid, dim3(kThreads), 0, stream,
+                           a, b.topk_idx, b.valid, g.runs, g.run_tokens, probs, hist, live);
+}
+
+}  // namespace
+
+int64_t balance_workspace_bytes(int num_tokens, int num_experts, int num_seqs) {
+    return geometry(num_tokens, num_experts, num_seqs).bytes;
+}
+
+hipError_t launch_balance(const RouteArgs& a, const BalanceArgs& b, void* workspace,
+                          hipStream_t stream) {
+    const Geometry g = geometry(a.num_tokens, a.num_experts, a.num_seqs);
+    char* ws = static_cast<char*>(workspace);
+    const TokenShape s = token_shape(a.num_experts);
+    if (s.lpt == 16) {
+        switch (s.vpl) {
+            case 1: launch_sum<16, 1>(a, b, g, ws, stream); break;
+            case 2: launch_sum<16, 2>(a, b, g, ws, stream); break;
+            case 4: launch_sum<16, 4>(a, b, g, ws, stream); break;
+            case 8: launch_sum<16, 8>(a, b, g, ws, stream); break;
+            default: launch_sum<16, 16>(a, b, g, ws, stream); break;
+        }
+    } else if (s.vpl == 8) {
+        launch_sum<64, 8>(a, b, g, ws, stream);
+    } else {
+        launch_sum<64, 16>(a, b, g, ws, stream);
+    }
+    double* part = reinterpret_cast<double*>(ws + g.part);
+    hipLaunchKernelGGL(balance_mean_kernel, dim3(static_cast<unsigned>(a.num_seqs) * g.tiles),
+                       dim3(kFinish), 0, stream, a.num_experts, g.tiles, g.runs, reinterpret_cast<float*>(ws + g.probs),
+                       reinterpret_cast<int32_t*>(ws + g.hist),
+                       reinterpret_cast<int32_t*>(ws + g.live), b.counts, b.mean_prob, b.num_valid,
+                       part);
+    const double factor = static_cast<double>(b.coef) / a.num_seqs * a.num_experts / a.num_topk;
+    hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(kFinish), 0, stream,
+                       static_cast<int64_t>(a.num_seqs) * g.tiles, part, factor, b.loss);
+    return hipGetLastError();
+}
+
+}  // namespace ep

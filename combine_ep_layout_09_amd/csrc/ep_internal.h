@@ -11,6 +11,8 @@ namespace ep {
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopk = 32;
 constexpr int kMaxHidden = 65536;
+constexpr int kMaxGroups = 64;
+constexpr int kMaxSeqs = 1 << 20;
 
 // Workgroup width (a multiple of 64, at most 1024) and number of column tiles
 // that cover a row of nvec 16-byte pieces with vpl pieces per lane.
@@ -78,6 +80,59 @@ hipError_t launch_layout_dispatch_persistent(const ep_problem& p, const int32_t*
                                              void* recv_scales, int ncu, hipStream_t stream);
 hipError_t launch_combine(const ep_problem& p, const void* expert_out, const int32_t* slot_of,
                           const float* topk_weights, void* y, hipStream_t stream);
+
+// Routing (gate logits): the problem as the kernels take it.  `pieces` /
+// `out_pieces`: rows of the logits / of the dense gradient can be accessed in
+// aligned pieces of min(experts per lane, 16 bytes' worth) elements.
+struct RouteArgs {
+    const void* logits;
+    int64_t stride;  // elements between rows of the logits
+    int32_t num_tokens, num_experts, num_topk, num_groups, topk_groups;
+    int32_t num_seqs, seq_len;
+    float scale;
+    bool bf16, sigmoid, normalize, pieces, out_pieces;
+};
+// Lanes per token and experts per lane of the routing kernels.
+struct TokenShape {
+    int lpt, vpl;
+};
+TokenShape token_shape(int num_experts);
+struct RouteForward {
+    const float* bias;
+    const uint8_t* valid;
+    int32_t* topk_idx;
+    float* topk_weights;
+};
+struct RouteBackward {
+    const int32_t* topk_idx;
+    const float* d_weights;
+    const uint8_t* valid;
+    float coef;
+    const int32_t* counts;
+    const int32_t* num_valid;
+    const float* d_loss;
+    void* d_logits;
+};
+hipError_t launch_route(const RouteArgs& a, const RouteForward& f, hipStream_t stream);
+hipError_t launch_route_backward(const RouteArgs& a, const RouteBackward& b, hipStream_t stream);
+
+struct BalanceArgs {
+    const int32_t* topk_idx;
+    const uint8_t* valid;
+    float coef;
+    int32_t* counts;
+    float* mean_prob;
+    int32_t* num_valid;
+    float* loss;
+};
+int64_t balance_workspace_bytes(int num_tokens, int num_experts, int num_seqs);
+hipError_t launch_balance(const RouteArgs& a, const BalanceArgs& b, void* workspace,
+                          hipStream_t stream);
+
+hipError_t launch_expert_w4(const ep_problem& p, const ep_expert_w4_t& mm, const void* rows,
+                            const void* row_scales, const ep_layout_t& layout,
+                            const uint8_t* codes, const uint8_t* scales, void* out,
+                            hipStream_t stream);
 hipError_t launch_e4m3_encode(const float* in, uint8_t* out, int64_t n, hipStream_t stream);
 
 }  // namespace ep

@@ -1,0 +1,332 @@
+// ep_route.hip -- the choice of experts from gate logits, and the gradient of
+// the logits from the routing weights and the balance loss.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ep_internal.h"
+#include "ep_route_dev.h"
+
+namespace ep {
+namespace {
+
+using namespace route;
+
+// ---------------------------------------------------------------- the choice
+
+// Keys of experts outside the token's best topk_groups groups become 0 (off).
+// The token's keys pass through LDS; lane g scores groups g, g + LPT, ...: the
+// sum (fp64, so exact order of the fp32 keys' sums) of the group's two largest
+// keys, an expert that is off counting as -FLT_MAX.  A group is kept if fewer
+// than topk_groups groups are better; equal scores go to the lower index.
+template <int LPT, int VPL>
+__device__ __forceinline__ void limit_groups(uint32_t (&key)[VPL], uint32_t* keys, double* score,
+                                             int lane, const RouteArgs& a) {
+    const int gs = a.num_experts / a.num_groups;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        if (lane * VPL + i < a.num_experts) keys[lane * VPL + i] = key[i];
+    __syncthreads();
+    for (int g = lane; g < a.num_groups; g += LPT) {
+        uint32_t m1 = 0, m2 = 0;
+        for (int i = 0; i < gs; ++i) {
+            const uint32_t k = keys[g * gs + i];
+            m2 = max(m2, min(m1, k));
+            m1 = max(m1, k);
+        }
+        const double low = -3.4028234663852886e38;
+        double s = m1 ? static_cast<double>(order_value(m1)) : low;
+        if (gs > 1) s += m2 ? static_cast<double>(order_value(m2)) : low;
+        score[g] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int e = lane * VPL + i;
+        if (e < a.num_experts) {
+            const int g = e / gs;
+            const double s = score[g];
+            int better = 0;
+            for (int h = 0; h < a.num_groups; ++h) {
+                const double o = score[h];
+                better += (o > s || (o == s && h < g)) ? 1 : 0;
+            }
+            if (better >= a.topk_groups) key[i] = 0;
+        }
+    }
+}
+
+// One launch, a token per LPT lanes.  The k best keys are taken one after the
+// other: every lane keeps the best of its own keys, a reduction over the
+// token's lanes finds the best of all, and the lowest lane that holds it gives
+// it up.  Entry j ends in lane j % LPT; the weights are then computed with one
+// lane per entry from the logits themselves (the bias only steers the choice).
+template <int LPT, int VPL, bool BF16>
+__global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const float* bias,
+                                                         const uint8_t* valid, int32_t* topk_idx,
+                                                         float* topk_weights) {
+    constexpr int kTokens = kThreads / LPT;
+    constexpr int kSel = kMaxTopk > LPT ? kMaxTopk / LPT : 1;
+    __shared__ uint32_t lds_keys[kTokens][LPT * VPL];
+    __shared__ double lds_score[kTokens][kMaxGroups];
+    const int lane = threadIdx.x % LPT;
+    const int slot = threadIdx.x / LPT;
+    const int wave_lane = threadIdx.x % kWave;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + slot;
+    const bool inside = t < a.num_tokens;
+    const bool live = inside && (valid == nullptr || valid[t] != 0);
+    const int E = a.num_experts;
+    const int64_t row = (inside ? t : 0) * a.stride;
+
+    float x[VPL];
+    load_logits<VPL, BF16>(a.logits, row, live ? E : 0, lane * VPL, a.pieces, x);
+    float m = 0.0f, total = 1.0f;
+    if (!a.sigmoid && !a.normalize) {
+        float z[VPL], slope[VPL];
+        scores<LPT, VPL>(x, false, z, slope, total);
+        m = -3.402823466e38f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (finite(x[i])) m = fmaxf(m, x[i]);
+        m = token_fmax<LPT>(m);
+    }
+    uint32_t key[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        float v = x[i];
+        if (bias != nullptr && lane * VPL + i < E) v += bias[lane * VPL + i];
+        key[i] = finite(x[i]) && finite(v) ? order_key(v) : 0u;
+    }
+    if (a.num_groups > 1) limit_groups<LPT, VPL>(key, lds_keys[slot], lds_score[slot], lane, a);
+
+    int sel[kSel];
+#pragma unroll
+    for (int q = 0; q < kSel; ++q) sel[q] = -1;
+    uint32_t best = 0;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        if (key[i] > best) best = key[i], at = i;
+    for (int j = 0; j < a.num_topk; ++j) {
+        const uint32_t top = token_max<LPT>(best);
+        const int winner = token_first<LPT>(best == top, wave_lane);
+        const int e = top ? winner * VPL + static_cast<int>(token_bcast<LPT>(at, winner)) : -1;
+#pragma unroll
+        for (int q = 0; q < kSel; ++q)
+            if (j == q * LPT + lane) sel[q] = e;
+        if (lane == winner) {
+            const int gone = at;
+            best = 0;
+            at = 0;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                if (i == gone) key[i] = 0;
+                if (key[i] > best) best = key[i], at = i;
+            }
+        }
+    }
+
+    float xe[kSel], w[kSel];
+#pragma unroll
+    for (int q = 0; q < kSel; ++q) xe[q] = logit_at<BF16>(a.logits, row, sel[q], sel[q] >= 0);
+    entry_weights<LPT, kSel>(xe, a, m, total, w);
+    if (inside) {
+#pragma unroll
+        for (int q = 0; q < kSel; ++q) {
+            const int j = q * LPT + lane;
+            if (j < a.num_topk) {
+                topk_idx[t * a.num_topk + j] = sel[q];
+                topk_weights[t * a.num_topk + j] = a.scale * w[q];
+            }
+        }
+    }
+}
+
+// -------------------------------------------------------------- the gradient
+
+// d_logits of a token = the balance loss's part, dense, plus the weights'
+// part, which is dense only for weights that were not normalised over the
+// chosen experts of a softmax.
+//   p = probabilities, A_e = coef d_loss E / (B k n^2) count_e:
+//     p_e (A_e - sum_i A_i p_i) slope_e
+// Counts enter as their (exact) distance from the first expert's: adding a
+// constant to A changes nothing, and the difference keeps the digits that
+// A_e - sum A p would cancel.  Entries that name one expert twice are added
+// up in their order by the first of them, so no order of atomics matters.
+template <int LPT, int VPL, bool BF16>
+__global__ __launch_bounds__(kThreads) void route_backward_kernel(
+    RouteArgs a, const int32_t* topk_idx, const float* d_weights, const uint8_t* valid, float coef,
+    const int32_t* counts, const int32_t* num_valid, const float* d_loss, void* d_logits) {
+    constexpr int kTokens = kThreads / LPT;
+    constexpr int kSel = kMaxTopk > LPT ? kMaxTopk / LPT : 1;
+    __shared__ float add[kTokens][LPT * VPL];
+    const int lane = threadIdx.x % LPT;
+    const int slot = threadIdx.x / LPT;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + slot;
+    const bool inside = t < a.num_tokens;
+    const bool live = inside && (valid == nullptr || valid[t] != 0);
+    const int E = a.num_experts, k = a.num_topk;
+    const int first = lane * VPL;
+    const int64_t row = (inside ? t : 0) * a.stride;
+
+    float x[VPL], dx[VPL];
+    load_logits<VPL, BF16>(a.logits, row, live ? E : 0, first, a.pieces, x);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        dx[i] = 0.0f;
+        add[slot][first + i] = 0.0f;
+    }
+    const bool loss = d_loss != nullptr;
+    const bool spread = d_weights != nullptr && !a.sigmoid && !a.normalize;
+    float m = 0.0f, total = 1.0f;
+    float p[VPL], slope[VPL];
+    if (loss || spread) {
+        scores<LPT, VPL>(x, a.sigmoid, p, slope, total);
+        const float r = total > 0.0f ? 1.0f / total : 0.0f;
+        m = -3.402823466e38f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            if (finite(x[i])) m = fmaxf(m, x[i]);
+            p[i] *= r;
+        }
+        m = token_fmax<LPT>(m);
+    }
+    if (loss) {
+        const int64_t seq = (inside ? t : 0) / a.seq_len;
+        const int32_t* c = counts + seq * E;
+        const float n = static_cast<float>(max(num_valid[seq], 1));
+        const float f = coef * static_cast<float>(E) /
+                        (static_cast<float>(a.num_seqs) * static_cast<float>(k)) * d_loss[0] / n / n;
+        const int32_t c0 = c[0];
+        float d[VPL], dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            d[i] = first + i < E ? static_cast<float>(c[first + i] - c0) : 0.0f;
+            dot += d[i] * p[i];
+        }
+        dot = token_sum<LPT>(dot);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) dx[i] = f * (p[i] * (d[i] - dot) * slope[i]);
+    }
+    if (d_weights != nullptr) {
+        int e[kSel];
+        float xe[kSel], g[kSel], w[kSel], part[kSel];
+        float gw = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kSel; ++q) {
+            const int j = q * LPT + lane;
+            e[q] = -1;
+            g[q] = 0.0f;
+            if (live && j < k) {
+                const int id = topk_idx[t * k + j];
+                if (id >= 0 && id < E) e[q] = id;
+            }
+            xe[q] = logit_at<BF16>(a.logits, row, e[q], e[q] >= 0);
+            if (!finite(xe[q])) e[q] = -1;
+            if (e[q] >= 0) g[q] = a.scale * d_weights[t * k + j];
+        }
+        entry_weights<LPT, kSel>(xe, a, m, total, w);
+#pragma unroll
+        for (int q = 0; q < kSel; ++q) gw += g[q] * w[q];
+        gw = token_sum<LPT>(gw);
+#pragma unroll
+        for (int q = 0; q < kSel; ++q) {
+            const float neg = a.sigmoid && e[q] >= 0 ? sigmoids(xe[q]).neg : 1.0f;
+            part[q] = e[q] < 0 ? 0.0f : w[q] * (a.normalize ? g[q] - gw : g[q]) * neg;
+        }
+        if (spread) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) dx[i] -= p[i] * gw;
+        }
+        __syncthreads();
+        float sum[kSel] = {};
+        bool mine[kSel];
+#pragma unroll
+        for (int q = 0; q < kSel; ++q) mine[q] = e[q] >= 0;
+        for (int j = 0; j < k; ++j) {
+#pragma unroll
+            for (int s = 0; s < kSel; ++s) {
+                if (j / LPT != s) continue;
+                const int ej = static_cast<int>(token_bcast<LPT>(e[s], j % LPT));
+                const float pj =
+                    __uint_as_float(token_bcast<LPT>(__float_as_uint(part[s]), j % LPT));
+#pragma unroll
+                for (int q = 0; q < kSel; ++q) {
+                    if (ej == e[q]) {
+                        sum[q] += pj;
+                        if (j < q * LPT + lane) mine[q] = false;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kSel; ++q)
+            if (mine[q]) add[slot][e[q]] = sum[q];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) dx[i] += add[slot][first + i];
+    }
+    if (inside) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (!finite(x[i])) dx[i] = 0.0f;
+        store_logits<VPL, BF16>(d_logits, t * E, E, first, a.out_pieces, dx);
+    }
+}
+
+template <int LPT, int VPL, bool BF16>
+void launch_one(const RouteArgs& a, const RouteForward* f, const RouteBackward* b,
+                hipStream_t stream) {
+    constexpr int kTokens = kThreads / LPT;
+    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(a.num_tokens) + kTokens - 1) /
+                                                kTokens);
+    if (f != nullptr)
+        hipLaunchKernelGGL((route_kernel<LPT, VPL, BF16>), dim3(grid), dim3(kThreads), 0, stream, a,
+                           f->bias, f->valid, f->topk_idx, f->topk_weights);
+    else
+        hipLaunchKernelGGL((route_backward_kernel<LPT, VPL, BF16>), dim3(grid), dim3(kThreads), 0,
+                           stream, a, b->topk_idx, b->d_weights, b->valid, b->coef, b->counts,
+                           b->num_valid, b->d_loss, b->d_logits);
+}
+
+template <bool BF16>
+hipError_t launch(const RouteArgs& a, const RouteForward* f, const RouteBackward* b,
+                  hipStream_t stream) {
+    if (a.num_tokens == 0) return hipSuccess;
+    const TokenShape s = token_shape(a.num_experts);
+    if (s.lpt == 16) {
+        switch (s.vpl) {
+            case 1: launch_one<16, 1, BF16>(a, f, b, stream); break;
+            case 2: launch_one<16, 2, BF16>(a, f, b, stream); break;
+            case 4: launch_one<16, 4, BF16>(a, f, b, stream); break;
+            case 8: launch_one<16, 8, BF16>(a, f, b, stream); break;
+            default: launch_one<16, 16, BF16>(a, f, b, stream); break;
+        }
+    } else {
+        if (s.vpl == 8)
+            launch_one<64, 8, BF16>(a, f, b, stream);
+        else
+            launch_one<64, 16, BF16>(a, f, b, stream);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// 16 lanes a token up to 256 experts, so that four tokens share each of a
+// wave's reductions; 64 lanes above.
+TokenShape token_shape(int num_experts) {
+    const int lpt = num_experts <= 256 ? 16 : 64;
+    int vpl = 1;
+    while (lpt * vpl < num_experts) vpl *= 2;
+    return {lpt, vpl};
+}
+
+hipError_t launch_route(const RouteArgs& a, const RouteForward& f, hipStream_t stream) {
+    return a.bf16 ? launch<true>(a, &f, nullptr, stream) : launch<false>(a, &f, nullptr, stream);
+}
+
+hipError_t launch_route_backward(const RouteArgs& a, const RouteBackward& b, hipStream_t stream) {
+    return a.bf16 ? launch<true>(a, nullptr, &b, stream) : launch<false>(a, nullptr, &b, stream);
+}
+
+}  // namespace ep

@@ -1,0 +1,321 @@
+// ep_route_dev.h -- device helpers of the routing kernels (gfx950, wave64).
+//
+// A token is handled by LPT consecutive lanes of one wave (16 or 64), each
+// holding VPL consecutive experts, so LPT * VPL >= E and the lowest lane with
+// a value also holds the lowest expert index.  Reductions leave their result
+// in every lane of the token and combine in a fixed order.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ep_device.h"
+#include "ep_internal.h"
+
+namespace ep {
+namespace route {
+
+constexpr int kThreads = 256;
+
+// Lane permutations: rotate by N inside each row of 16 lanes.
+template <int N>
+__device__ __forceinline__ uint32_t row_ror(uint32_t v) {
+    return static_cast<uint32_t>(
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x120 + N, 0xf, 0xf, false));
+}
+
+// The two halves of a pairwise exchange: {rows 0, 0, 2, 2} and {1, 1, 3, 3}
+// for 16, {lanes 0-31 twice} and {lanes 32-63 twice} for 32.
+__device__ __forceinline__ uint2 swap16(uint32_t v) {
+    auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return make_uint2(r[0], r[1]);
+}
+__device__ __forceinline__ uint2 swap32(uint32_t v) {
+    auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return make_uint2(r[0], r[1]);
+}
+
+template <int LPT>
+__device__ __forceinline__ uint32_t token_max(uint32_t v) {
+    v = max(v, row_ror<8>(v));
+    v = max(v, row_ror<4>(v));
+    v = max(v, row_ror<2>(v));
+    v = max(v, row_ror<1>(v));
+    if constexpr (LPT == 64) {
+        uint2 p = swap16(v);
+        v = max(p.x, p.y);
+        p = swap32(v);
+        v = max(p.x, p.y);
+    }
+    return v;
+}
+
+// Sum and maximum of floats.  Every lane adds the same pairs: x + y == y + x.
+template <int LPT>
+__device__ __forceinline__ float token_sum(float f) {
+    f += __uint_as_float(row_ror<8>(__float_as_uint(f)));
+    f += __uint_as_float(row_ror<4>(__float_as_uint(f)));
+    f += __uint_as_float(row_ror<2>(__float_as_uint(f)));
+    f += __uint_as_float(row_ror<1>(__float_as_uint(f)));
+    if constexpr (LPT == 64) {
+        uint2 p = swap16(__float_as_uint(f));
+        f = __uint_as_float(p.x) + __uint_as_float(p.y);
+        p = swap32(__float_as_uint(f));
+        f = __uint_as_float(p.x) + __uint_as_float(p.y);
+    }
+    return f;
+}
+
+template <int LPT>
+__device__ __forceinline__ float token_fmax(float f) {
+    f = fmaxf(f, __uint_as_float(row_ror<8>(__float_as_uint(f))));
+    f = fmaxf(f, __uint_as_float(row_ror<4>(__float_as_uint(f))));
+    f = fmaxf(f, __uint_as_float(row_ror<2>(__float_as_uint(f))));
+    f = fmaxf(f, __uint_as_float(row_ror<1>(__float_as_uint(f))));
+    if constexpr (LPT == 64) {
+        uint2 p = swap16(__float_as_uint(f));
+        f = fmaxf(__uint_as_float(p.x), __uint_as_float(p.y));
+        p = swap32(__float_as_uint(f));
+        f = fmaxf(__uint_as_float(p.x), __uint_as_float(p.y));
+    }
+    return f;
+}
+
+// Value held by lane `src` (0 .. LPT-1) of this lane's token.
+template <int LPT>
+__device__ __forceinline__ uint32_t token_bcast(uint32_t v, int src) {
+    return static_cast<uint32_t>(__shfl(static_cast<int>(v), src, LPT));
+}
+
+// Lowest lane of this lane's token for which `p` holds (p holds for one at
+// least).
+template <int LPT>
+__device__ __forceinline__ int token_first(bool p, int wave_lane) {
+    const uint64_t b = __ballot(p);
+    if constexpr (LPT == 64) return __ffsll(static_cast<unsigned long long>(b)) - 1;
+    const uint32_t mine = static_cast<uint32_t>(b >> (wave_lane & ~15)) & 0xffffu;
+    return __ffs(static_cast<int>(mine)) - 1;
+}
+
+__device__ __forceinline__ bool finite(float x) {
+    return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u;
+}
+
+// Order-preserving map of a finite float to an integer > 0; -0 and +0 agree.
+__device__ __forceinline__ uint32_t order_key(float x) {
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t k) {
+    return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
+}
+
+// sigma(x) and sigma(-x), both to full relative precision: with
+// t = exp(-|x|), the larger of the two is 1 / (1 + t), the smaller t times it.
+struct Sigmoids {
+    float pos, neg;
+};
+__device__ __forceinline__ Sigmoids sigmoids(float x) {
+    const float t = expf(-fabsf(x));
+    const float r = 1.0f / (1.0f + t);
+    const float s = t * r;
+    return x >= 0.0f ? Sigmoids{r, s} : Sigmoids{s, r};
+}
+__device__ __forceinline__ float log_sigmoid(float x) {
+    return fminf(x, 0.0f) - log1pf(expf(-fabsf(x)));
+}
+
+// Row of `n` logits: VPL of them from index lane * VPL on, NaN (an expert
+// that is off) past the end.  `piece` is the host's word that rows may be
+// read in aligned pieces of min(VPL, 16 bytes' worth) elements that do not
+// straddle the row's end.
+template <int VPL, bool BF16>
+__device__ __forceinline__ void load_logits(const void* base, int64_t row_start, int n, int first,
+                                            bool piece, float (&x)[VPL]) {
+    const float nan = __uint_as_float(0x7fc00000u);
+    if constexpr (BF16) {
+        const uint16_t* p = static_cast<const uint16_t*>(base) + row_start + first;
+        constexpr int W = VPL < 8 ? VPL : 8;
+        if (W > 1 && piece) {
+#pragma unroll
+            for (int i = 0; i < VPL; i += W) {
+                const bool in = first + i < n;
+                uint32_t w[W > 1 ? W / 2 : 1];
+#pragma unroll
+                for (int q = 0; q < W / 2; ++q) w[q] = 0x7fc07fc0u;
+                if (in) {
+                    if constexpr (W == 8) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(p + i);
+                        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                    } else if constexpr (W == 4) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(p + i);
+                        w[0] = v.x, w[1] = v.y;
+                    } else if constexpr (W == 2) {
+                        w[0] = *reinterpret_cast<const uint32_t*>(p + i);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < W / 2; ++q) {
+                    x[i + 2 * q] = bf16_lo(w[q]);
+                    x[i + 2 * q + 1] = bf16_hi(w[q]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                x[i] = first + i < n ? __uint_as_float(static_cast<uint32_t>(p[i]) << 16) : nan;
+        }
+    } else {
+        const float* p = static_cast<const float*>(base) + row_start + first;
+        constexpr int W = VPL < 4 ? VPL : 4;
+        if (W > 1 && piece) {
+#pragma unroll
+            for (int i = 0; i < VPL; i += W) {
+                const bool in = first + i < n;
+#pragma unroll
+                for (int q = 0; q < W; ++q) x[i + q] = nan;
+                if (in) {
+                    if constexpr (W == 4) {
+                        const float4 v = *reinterpret_cast<const float4*>(p + i);
+                        x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+                    } else if constexpr (W == 2) {
+                        const float2 v = *reinterpret_cast<const float2*>(p + i);
+                        x[i] = v.x, x[i + 1] = v.y;
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) x[i] = first + i < n ? p[i] : nan;
+        }
+    }
+}
+
+// Unnormalised scores of a token's experts: z[i] / (sum of z over the token)
+// are its probabilities; 0 for experts that are off.  Softmax: exp(x - max).
+// Sigmoid: sigma(x); where even the largest logit is below -20, sigma(x) is
+// exp(x) to 2e-9, and exp(x - max) keeps a row of tiny scores from vanishing.
+// slope[i] is d log z / dx of the score: 1, or sigma(-x).
+template <int LPT, int VPL>
+__device__ __forceinline__ void scores(const float (&x)[VPL], bool sigmoid, float (&z)[VPL],
+                                       float (&slope)[VPL], float& total) {
+    float m = -3.402823466e38f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        if (finite(x[i])) m = fmaxf(m, x[i]);
+    m = token_fmax<LPT>(m);
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        z[i] = 0.0f;
+        slope[i] = 1.0f;
+        if (finite(x[i])) {
+            if (sigmoid && m > -20.0f) {
+                const Sigmoids g = sigmoids(x[i]);
+                z[i] = g.pos;
+                slope[i] = g.neg;
+            } else {
+                z[i] = expf(x[i] - m);
+                // below -20 sigma(-x) rounds to 1
+            }
+        }
+        s += z[i];
+    }
+    total = token_sum<LPT>(s);
+}
+
+// One logit, or NaN where the entry is absent.
+template <bool BF16>
+__device__ __forceinline__ float logit_at(const void* base, int64_t row_start, int e, bool there) {
+    if (!there) return __uint_as_float(0x7fc00000u);
+    if constexpr (BF16)
+        return __uint_as_float(
+            static_cast<uint32_t>(static_cast<const uint16_t*>(base)[row_start + e]) << 16);
+    else
+        return static_cast<const float*>(base)[row_start + e];
+}
+
+// Weights of a token's entries before the scale: entry q * LPT + lane has the
+// logit xe[q] (NaN: absent, weight 0).  m and total are the maximum and the
+// exp sum of the whole row, for softmax weights that are not normalised over
+// the entries.
+template <int LPT, int SEL>
+__device__ __forceinline__ void entry_weights(const float (&xe)[SEL], const RouteArgs& a, float m,
+                                              float total, float (&w)[SEL]) {
+    if (a.normalize) {
+        float l[SEL], top = -3.402823466e38f, s = 0.0f;
+#pragma unroll
+        for (int q = 0; q < SEL; ++q) {
+            l[q] = a.sigmoid ? log_sigmoid(xe[q]) : xe[q];
+            if (finite(xe[q])) top = fmaxf(top, l[q]);
+        }
+        top = token_fmax<LPT>(top);
+#pragma unroll
+        for (int q = 0; q < SEL; ++q) {
+            w[q] = finite(xe[q]) ? expf(l[q] - top) : 0.0f;
+            s += w[q];
+        }
+        s = token_sum<LPT>(s);
+#pragma unroll
+        for (int q = 0; q < SEL; ++q) w[q] = s > 0.0f ? w[q] / s : 0.0f;
+    } else {
+#pragma unroll
+        for (int q = 0; q < SEL; ++q) {
+            w[q] = 0.0f;
+            if (finite(xe[q])) w[q] = a.sigmoid ? sigmoids(xe[q]).pos : expf(xe[q] - m) / total;
+        }
+    }
+}
+
+// Dense row of n gradients in the logits' type, rounded to nearest even.
+template <int VPL, bool BF16>
+__device__ __forceinline__ void store_logits(void* base, int64_t row_start, int n, int first,
+                                             bool piece, const float (&v)[VPL]) {
+    if constexpr (BF16) {
+        uint16_t* p = static_cast<uint16_t*>(base) + row_start + first;
+        constexpr int W = VPL < 8 ? VPL : 8;
+        uint32_t h[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) h[i] = f32_to_bf16_rne(v[i]);
+        if (W > 1 && piece) {
+#pragma unroll
+            for (int i = 0; i < VPL; i += W) {
+                if (first + i >= n) continue;
+                if constexpr (W == 8)
+                    *reinterpret_cast<uint4*>(p + i) =
+                        make_uint4(h[i] | h[i + 1] << 16, h[i + 2] | h[i + 3] << 16,
+                                   h[i + 4] | h[i + 5] << 16, h[i + 6] | h[i + 7] << 16);
+                else if constexpr (W == 4)
+                    *reinterpret_cast<uint2*>(p + i) =
+                        make_uint2(h[i] | h[i + 1] << 16, h[i + 2] | h[i + 3] << 16);
+                else if constexpr (W == 2)
+                    *reinterpret_cast<uint32_t*>(p + i) = h[i] | h[i + 1] << 16;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (first + i < n) p[i] = static_cast<uint16_t>(h[i]);
+        }
+    } else {
+        float* p = static_cast<float*>(base) + row_start + first;
+        constexpr int W = VPL < 4 ? VPL : 4;
+        if (W > 1 && piece) {
+#pragma unroll
+            for (int i = 0; i < VPL; i += W) {
+                if (first + i >= n) continue;
+                if constexpr (W == 4)
+                    *reinterpret_cast<float4*>(p + i) =
+                        make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                else if constexpr (W == 2)
+                    *reinterpret_cast<float2*>(p + i) = make_float2(v[i], v[i + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (first + i < n) p[i] = v[i];
+        }
+    }
+}
+
+}  // namespace route
+}  // namespace ep

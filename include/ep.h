@@ -1,13 +1,16 @@
 /* ep.h -- C ABI of libep: MoE token dispatch and combine on one AMD MI355X
  * (gfx950), every expert resident on this GPU.
  *
- * Three operations, each one or more launches of hand-written HIP kernels,
+ * Operations, each one or more launches of hand-written HIP kernels,
  * asynchronously on the caller's stream:
  *
+ *   ep_route    gate logits -> each token's experts and weights; with
+ *               ep_balance_loss and ep_route_backward for training
  *   ep_layout   routing table -> per-expert counts, expert-major offsets and a
  *               stable slot for every (token, k) routing entry
  *   ep_dispatch token rows -> per-expert receive rows (bf16 copy, or E4M3FN
  *               bytes plus one fp32 scale per 128 channels)
+ *   ep_expert_w4  receive rows -> the experts' products with 4-bit weights
  *   ep_combine  the k expert outputs of each token -> their routing-weighted
  *               sum in fp32, rounded to bf16
  *
@@ -225,6 +228,126 @@ int ep_combine(const ep_problem* prob, const void* expert_out, const ep_layout_t
  *   out  uint8 [n], device.
  * n = 0 is valid and launches nothing. */
 int ep_e4m3_encode(const float* in, uint8_t* out, int64_t n, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Routing: the choice of experts in front of ep_layout, the balance loss of a
+ * routing, and the gradient of the gate logits from both.
+ *
+ * A logit that is not finite (NaN, -inf, +inf) switches its expert off for
+ * that token: it has no probability, is never chosen, and gets gradient 0.
+ * A token whose `valid` byte is 0 (padding) has every expert off and its
+ * logits are not read.
+ *
+ * Scores of token t: softmax (score = 0): z_e = exp(x_e); sigmoid (1):
+ * z_e = 1 / (1 + exp(-x_e)).  Probabilities p_e = z_e / sum_i z_i over the
+ * token's experts.  Sums, maxima and gradients are held in fp32 or fp64. */
+typedef struct ep_routing {
+    int32_t num_tokens;   /* T >= 0 */
+    int32_t num_experts;  /* E, 1 .. 1024 */
+    int32_t num_topk;     /* k, 1 .. 32, at most topk_groups * (E / num_groups) */
+    int32_t num_groups;   /* G, 1 .. 64, divides E; groups are runs of E / G experts */
+    int32_t topk_groups;  /* groups a token may choose from, 1 .. G */
+    int32_t score;        /* 0 softmax, 1 sigmoid */
+    int32_t normalize;    /* 1: a token's weights are divided by their sum */
+    int32_t num_seqs;     /* B, 1 .. 2^20, divides T: the balance loss is taken per sequence of
+                             T / B consecutive tokens */
+    float weight_scale;   /* factor of every weight, finite */
+} ep_routing;
+
+/* Experts and weights of each token.
+ *   logits        [T, E] gate logits, fp32 (logits_bf16 = 0) or bf16 (1), device, at their
+ *                 own alignment (4 / 2 bytes); row t starts logits_stride >= E elements after
+ *                 row t - 1.
+ *   expert_bias   fp32 [E], device, or NULL.  Added to the logits for the choice only.
+ *   valid         uint8 [T], device, or NULL (every token is valid).
+ *   topk_idx      int32 [T, k], written: the experts with the k largest keys
+ *                 fp32(logit + bias), largest first, equal keys by the lower index; -1
+ *                 where fewer than k experts are on (ep_layout skips those entries).  A key
+ *                 that is not finite is off.
+ *                 G > 1: only experts of the topk_groups best groups; a group's score is
+ *                 the fp64 sum of its two largest keys (one, if it has one expert), an
+ *                 expert that is off counting as -FLT_MAX; equal scores by the lower index.
+ *   topk_weights  fp32 [T, k], written: weight_scale times z_e (sigmoid) or p_e (softmax)
+ *                 of the chosen experts, or with normalize their z_e over the sum of the
+ *                 token's k; 0 where topk_idx is -1.
+ * T = 0 is valid and launches nothing. */
+int ep_route(const ep_routing* rt, const void* logits, int logits_bf16, int64_t logits_stride,
+             const float* expert_bias, const uint8_t* valid, int32_t* topk_idx,
+             float* topk_weights, void* stream);
+
+/* Bytes of device workspace ep_balance_loss needs, or -1 if the problem is
+ * invalid.  Needs no initialisation; scratch after the call. */
+int64_t ep_balance_workspace_bytes(const ep_routing* rt);
+
+/* Balance loss of a routing:
+ *   c[s, e]  entries of valid tokens of sequence s that name expert e
+ *   n[s]     valid tokens of sequence s
+ *   P[s, e]  mean of p_e over those tokens (0 if there are none)
+ *   loss     coef / B * sum_s sum_e E / (k n[s]) * c[s, e] * P[s, e]
+ * Sequences without a valid token add nothing.
+ *   topk_idx   int32 [T, k], device; ids outside [0, E) are not counted.
+ *   counts     int32 [B, E], mean_prob fp32 [B, E], num_valid int32 [B], loss fp32 [1]:
+ *              device, written.
+ *   coef       finite.
+ *   workspace  device scratch of at least ep_balance_workspace_bytes bytes, 16-byte aligned.
+ * The sums have a fixed order: equal calls give equal bits. */
+int ep_balance_loss(const ep_routing* rt, const void* logits, int logits_bf16,
+                    int64_t logits_stride, const int32_t* topk_idx, const uint8_t* valid,
+                    float coef, int32_t* counts, float* mean_prob, int32_t* num_valid,
+                    float* loss, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of the logits from the routing weights (d_weights), from the
+ * balance loss (d_loss), or their sum; at least one is given.
+ *   topk_idx   int32 [T, k], as chosen (read with d_weights); entries whose id is outside
+ *              [0, E) or names an expert that is off add nothing, an id may repeat.
+ *   d_weights  fp32 [T, k], device, or NULL.
+ *   coef, counts, num_valid   as given to and written by ep_balance_loss (read with d_loss;
+ *              counts are constants of the loss).
+ *   d_loss     fp32 [1], device, or NULL: gradient of the loss.
+ *   d_logits   [T, E] in the logits' type, dense, device, every element written (0 for tokens
+ *              that are not valid and experts that are off), rounded once from fp32. */
+int ep_route_backward(const ep_routing* rt, const void* logits, int logits_bf16,
+                      int64_t logits_stride, const int32_t* topk_idx, const float* d_weights,
+                      const uint8_t* valid, float coef, const int32_t* counts,
+                      const int32_t* num_valid, const float* d_loss, void* d_logits,
+                      void* stream);
+
+/* ------------------------------------------------------------------------
+ * The experts' products on the receive rows, with 4-bit weights (the OCP
+ * microscaling format: E2M1 codes, values 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a
+ * sign; one UE8M0 scale byte per 32 input channels). */
+typedef struct ep_expert_w4_t {
+    int32_t in_features;   /* K, a multiple of 32 (of 128 for FP8 rows), 32 .. 65536 */
+    int32_t out_features;  /* N, 1 .. 65536 */
+    int32_t in_format;     /* rows: 0 bf16; 1, 2 E4M3FN with the block scales that
+                              ep_problem.use_fp8 = 1, 2 names */
+    int32_t activation;    /* 0: out = y, weights [E, N, K].
+                              1: out = silu(gate) * up with silu(v) = v / (1 + exp(-v));
+                              weights [E, 2N, K], rows n and N + n of an expert giving gate
+                              and up of output n */
+} ep_expert_w4_t;
+
+/* out[r, n] = sum_k rows[r, k] * weight[e, n, k] for every receive row r that
+ * an entry of expert e fills (activation 0; see above for 1).  Products are
+ * exact, sums fp32 in a fixed order, one rounding to bf16.  Rows that no
+ * entry fills are neither read nor written.
+ *   prob        T, k, E and capacity of the layout; hidden and use_fp8 are not read beyond
+ *               the common checks.
+ *   rows        [R, K], bf16 or E4M3FN bytes, in the receive-row layout (ep_dispatch's
+ *               recv_x, or another ep_expert_w4's out).
+ *   row_scales  [R, K / 128] fp32 (in_format 1) or UE8M0 bytes (2); ignored for 0.
+ *   layout      as written by ep_layout for the same problem (count and offset are read).
+ *   codes       uint8 [E, N or 2N, K / 2]: channel 2i in the low, 2i + 1 in the high four
+ *               bits of byte i; bit 3 the sign.
+ *   scales      uint8 [E, N or 2N, K / 32]: value 2^(byte - 127); 255 is NaN.  A weight of
+ *               magnitude 2^128 or more (byte 254 with a code of 2 or more, 253 with 4 or
+ *               more) is infinite.
+ *   out         bf16 [R, N]; must not overlap rows.
+ * The weights of an expert that no entry names are not read.  Data pointers
+ * are 16-byte aligned. */
+int ep_expert_w4(const ep_problem* prob, const ep_expert_w4_t* mm, const void* rows,
+                 const void* row_scales, const ep_layout_t* layout, const uint8_t* codes,
+                 const uint8_t* scales, void* out, void* stream);
 
 /* Static text for a status code. */
 const char* ep_strerror(int code);
