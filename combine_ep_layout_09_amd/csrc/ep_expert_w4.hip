@@ -47,11 +47,9 @@ struct Args {
     const uint8_t* rows;      // bf16 or E4M3FN [R, K]
     const void* row_scales;   // fp32 or UE8M0 [R, K / 128]
     const int32_t* count;
-    const int32_t* offset;
     const uint8_t* codes;     // [E, n2, K / 2]
     const uint8_t* scales;    // [E, n2, K / 32]
     uint16_t* out;            // bf16 [R, N]
-    int64_t tiles;            // row tiles at most
     int64_t num_rows;         // R
     int32_t num_experts, capacity, K, N;
 };
@@ -99,62 +97,65 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t at, u
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, step, 0));
 }
 
-// Rows of expert e: their number, and the first one in *start.
-__device__ __forceinline__ int expert_rows(const Args& a, int e, int64_t* start) {
-    int64_t s, n = a.count[e];
-    if (a.capacity > 0) {
-        s = static_cast<int64_t>(e) * a.capacity;
-        n = n < a.capacity ? n : a.capacity;
-    } else {
-        // a layout of another problem must not lead outside the rows
-        s = a.offset[e];
-        s = s < 0 ? 0 : s;
-        n = n < a.num_rows - s ? n : a.num_rows - s;
-    }
-    *start = s;
-    return n > 0 ? static_cast<int>(n) : 0;
-}
-
-// The expert and row tile number `want` names: experts with rows, in order,
-// each with one tile per MC rows.
-template <int THREADS, int MC>
-struct Finder {
-    int first[THREADS / kWave];   // tiles of each wave's experts
-    int expert, tile;
-
-    __device__ __forceinline__ void find(const Args& a, int64_t want) {
-        const int per = (a.num_experts + THREADS - 1) / THREADS;
-        const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-        const int e0 = threadIdx.x * per;
-        int tiles = 0;
-        int64_t s;
-        for (int i = 0; i < per; ++i)
-            if (e0 + i < a.num_experts) tiles += (expert_rows(a, e0 + i, &s) + MC - 1) / MC;
-        int before = tiles;
-#pragma unroll
-        for (int d = 1; d < kWave; d *= 2) {
-            const int v = __shfl_up(before, d, kWave);
-            if (lane >= d) before += v;
-        }
-        if (lane == kWave - 1) first[wave] = before;
-        if (threadIdx.x == 0) expert = -1;
-        __syncthreads();
-        int64_t at = before - tiles;
-        for (int w = 0; w < wave; ++w) at += first[w];
-        if (want >= at && want < at + tiles) {
-            for (int i = 0; i < per; ++i) {
-                const int n = (expert_rows(a, e0 + i, &s) + MC - 1) / MC;
-                if (want < at + n) {
-                    expert = e0 + i;
-                    tile = static_cast<int>(want - at);
-                    break;
-                }
-                at += n;
-            }
-        }
-        __syncthreads();
-    }
+// The expert, rows and row tile that number `want` names: experts with rows,
+// in order, each with one tile per MC rows; expert -1 if there are fewer.
+// Every wave finds it by itself, a lane per run of experts, so no wave waits
+// for another; contiguous rows start where the counts before them end.
+struct Found {
+    int expert, count, tile;
+    int64_t start;
 };
+template <int MC>
+__device__ __forceinline__ Found find_tile(const Args& a, uint32_t want) {
+    const int lane = threadIdx.x % kWave;
+    const int per = (a.num_experts + kWave - 1) / kWave;
+    // Counts of another problem's layout must not lead outside the rows: all
+    // sums stop at the number of rows (and of tiles).
+    const uint32_t most = static_cast<uint32_t>(a.capacity > 0 ? a.capacity : a.num_rows);
+    const uint32_t top_rows = static_cast<uint32_t>(a.num_rows), top_tiles = 0x40000000u;
+    const auto count_of = [&](int e) {
+        const int n = e < a.num_experts ? a.count[e] : 0;
+        return n < 0 ? 0u : min(static_cast<uint32_t>(n), most);
+    };
+    const auto tiles_of = [](uint32_t n) { return (n + MC - 1) / MC; };
+    uint32_t rows = 0, tiles = 0;
+    for (int i = 0; i < per; ++i) {
+        const uint32_t n = count_of(lane * per + i);
+        rows = min(rows + n, top_rows);
+        tiles = min(tiles + tiles_of(n), top_tiles);
+    }
+    uint32_t rows_to = rows, tiles_to = tiles;  // sums up to and with this lane
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+        const uint32_t r = __shfl_up(rows_to, d, kWave), q = __shfl_up(tiles_to, d, kWave);
+        if (lane >= d) {
+            rows_to = min(rows_to + r, top_rows);
+            tiles_to = min(tiles_to + q, top_tiles);
+        }
+    }
+    const uint64_t beyond = __ballot(tiles_to > want);
+    Found f{-1, 0, 0, 0};
+    if (beyond == 0) return f;
+    const int owner = __ffsll(static_cast<unsigned long long>(beyond)) - 1;
+    uint32_t at = 0, row = 0;
+    if (owner > 0) {
+        at = __builtin_amdgcn_readlane(tiles_to, owner - 1);
+        row = __builtin_amdgcn_readlane(rows_to, owner - 1);
+    }
+    for (int i = 0; i < per; ++i) {
+        const uint32_t n = __builtin_amdgcn_readfirstlane(count_of(owner * per + i));
+        if (want - at < tiles_of(n)) {
+            f.expert = owner * per + i;
+            f.tile = static_cast<int>(want - at);
+            f.start = a.capacity > 0 ? static_cast<int64_t>(f.expert) * a.capacity : row;
+            f.count = static_cast<int>(a.capacity > 0 ? n : min(n, top_rows - row));
+            break;
+        }
+        at += tiles_of(n);
+        row = min(row + n, top_rows);
+    }
+    return f;
+}
 
 // One step's operands of a wave.
 template <int MT, bool FP8>
@@ -165,12 +166,13 @@ struct Stage {
 
 // Few rows per expert.  FP8: rows are E4M3FN with one scale per 128 channels
 // (UE8: a UE8M0 byte, else fp32), which multiplies the step's sum.  GATED:
-// tiles 0, 1 are rows n of the gate half and tiles 2, 3 rows N + n.
+// tiles 0, 1 are rows n of the gate half and tiles 2, 3 rows N + n.  WORDS:
+// K % 128 == 0, so rows of scales are whole words.
 //
 // WAVES waves take the steps of a segment in turns.  Each keeps the loads of
 // its next step in flight while it multiplies the present one.  The scales,
 // scattered bytes in memory, are read once, whole rows at a time, into LDS.
-template <int WAVES, int MT, bool FP8, bool UE8, bool GATED>
+template <int WAVES, int MT, bool FP8, bool UE8, bool GATED, bool WORDS>
 __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void expert_w4_kernel(Args a) {
     constexpr int kThreads = WAVES * kWave;
     constexpr int MC = 16 * MT;
@@ -180,7 +182,6 @@ __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void e
     constexpr int kRedBytes = WAVES * MC * kRedRow * 4;
     constexpr int kBytes =
         kScaleBytes + kRowScaleBytes > kRedBytes ? kScaleBytes + kRowScaleBytes : kRedBytes;
-    __shared__ Finder<kThreads, MC> finder;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kBytes];
     uint8_t(*lds_scale)[kScaleRow] = reinterpret_cast<uint8_t(*)[kScaleRow]>(lds);
     float(*lds_row)[kRowScaleRow] =
@@ -195,195 +196,211 @@ __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void e
     const int n0 = blockIdx.x * kOut;
     const int here = N - n0 < kOut ? N - n0 : kOut;  // outputs of this workgroup
 
-    for (int64_t tile = blockIdx.y; tile < a.tiles; tile += gridDim.y) {
-        finder.find(a, tile);
-        const int e = __builtin_amdgcn_readfirstlane(finder.expert);
-        if (e < 0) break;  // tiles are in order: no later one has rows either
-        int64_t start;
-        const int count = expert_rows(a, e, &start);
-        const int m0 = __builtin_amdgcn_readfirstlane(finder.tile) * MC;
-        const int rows_here = count - m0 < MC ? count - m0 : MC;
+    const Found f = find_tile<MC>(a, blockIdx.z * gridDim.y + blockIdx.y);
+    const int e = f.expert;
+    if (e < 0) return;
+    const int64_t start = f.start;
+    const int m0 = f.tile * MC;
+    const int rows_here = f.count - m0 < MC ? f.count - m0 : MC;
+    if (rows_here <= 0) return;
 
-        const int64_t w_row = static_cast<int64_t>(e) * (GATED ? 2 * N : N) + n0;
-        const uint32_t w_pitch = K / 2;
-        const uint32_t x_pitch = K * (FP8 ? 1 : 2);
-        const auto w_view = view(a.codes + w_row * w_pitch, here * w_pitch);
-        const auto up_view = view(a.codes + (w_row + (GATED ? N : 0)) * w_pitch, here * w_pitch);
-        const auto x_view = view(a.rows + (start + m0) * x_pitch, rows_here * x_pitch);
-        uint32_t w_at[kOut / 16], x_at[MT];
+    const int64_t w_row = static_cast<int64_t>(e) * (GATED ? 2 * N : N) + n0;
+    const uint32_t w_pitch = K / 2;
+    const uint32_t x_pitch = K * (FP8 ? 1 : 2);
+    const auto w_view = view(a.codes + w_row * w_pitch, here * w_pitch);
+    const auto up_view = view(a.codes + (w_row + (GATED ? N : 0)) * w_pitch, here * w_pitch);
+    const auto s_view = view(a.scales + w_row * blocks, here * blocks);
+    const auto up_s_view = view(a.scales + (w_row + (GATED ? N : 0)) * blocks, here * blocks);
+    const auto x_view = view(a.rows + (start + m0) * x_pitch, rows_here * x_pitch);
+    uint32_t w_at[kOut / 16], x_at[MT];
 #pragma unroll
-        for (int t = 0; t < kOut / 16; ++t)
-            w_at[t] = t * 16 + r16 < here ? (t * 16 + r16) * w_pitch + group * 16 : kNowhere;
+    for (int t = 0; t < kOut / 16; ++t)
+        w_at[t] = t * 16 + r16 < here ? (t * 16 + r16) * w_pitch + group * 16 : kNowhere;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+        x_at[m] = m * 16 + r16 < rows_here
+                      ? (m * 16 + r16) * x_pitch + group * (FP8 ? 32 : 64)
+                      : kNowhere;
+
+    f32x4 acc[kTiles][MT];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[t][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const auto load = [&](int c, Stage<MT, FP8>& s) {
+        const bool has = c * 4 + group < blocks;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            const uint32_t at = w_at[t % (kOut / 16)];
+            s.w[t] = load16(GATED && t >= 2 ? up_view : w_view, has ? at : kNowhere, c * 64);
+        }
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-            x_at[m] = m * 16 + r16 < rows_here
-                          ? (m * 16 + r16) * x_pitch + group * (FP8 ? 32 : 64)
-                          : kNowhere;
-
-        f32x4 acc[kTiles][MT];
+#pragma unroll
+            for (int i = 0; i < (FP8 ? 2 : 4); ++i)
+                s.x[m][i] = load16(x_view, has ? x_at[m] : kNowhere,
+                                   c * (FP8 ? 128 : 256) + i * 16);
+    };
+    const auto multiply = [&](int c, const Stage<MT, FP8>& s) {  // c within the segment
+        float sf[kTiles];
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+            sf[t] = __uint_as_float(
+                static_cast<uint32_t>(lds_scale[t * 16 + r16][c * 4 + group]) << 23);
+        f32x4 part[kTiles][MT];
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) acc[t][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-        const auto load = [&](int c, Stage<MT, FP8>& s) {
-            const bool has = c * 4 + group < blocks;
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                const uint32_t at = w_at[t % (kOut / 16)];
-                s.w[t] = load16(GATED && t >= 2 ? up_view : w_view, has ? at : kNowhere, c * 64);
-            }
-#pragma unroll
             for (int m = 0; m < MT; ++m)
+                part[t][m] = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[t][m];
 #pragma unroll
-                for (int i = 0; i < (FP8 ? 2 : 4); ++i)
-                    s.x[m][i] = load16(x_view, has ? x_at[m] : kNowhere,
-                                       c * (FP8 ? 128 : 256) + i * 16);
-        };
-        const auto multiply = [&](int c, const Stage<MT, FP8>& s) {  // c within the segment
-            float sf[kTiles];
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-                sf[t] = __uint_as_float(
-                    static_cast<uint32_t>(lds_scale[t * 16 + r16][c * 4 + group]) << 23);
-            f32x4 part[kTiles][MT];
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    part[t][m] = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[t][m];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                __builtin_amdgcn_sched_barrier(0);  // or every operand is made at once
-                bf16x8 xf[MT];
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    if constexpr (FP8) {
-                        const u32x4 v = s.x[m][i / 2];
-                        xf[m] = i % 2 == 0 ? rows8(v.x, v.y) : rows8(v.z, v.w);
-                    } else {
-                        Frag f;
-                        f.w = s.x[m][i];
-                        xf[m] = f.v;
-                    }
-                }
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t) {
-                    const bf16x8 wf = weights8(s.w[t][i], sf[t]);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-                        part[t][m] =
-                            __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[m], part[t][m], 0, 0, 0);
-                }
-            }
+        for (int i = 0; i < 4; ++i) {
+            __builtin_amdgcn_sched_barrier(0);  // or every operand is made at once
+            bf16x8 xf[MT];
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const float xs = FP8 ? lds_row[m * 16 + r16][c] : 1.0f;
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t) {
-                    if constexpr (FP8) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[t][m][i] = fmaf(xs, part[t][m][i], acc[t][m][i]);
-                    } else {
-                        acc[t][m] = part[t][m];
-                    }
+                if constexpr (FP8) {
+                    const u32x4 v = s.x[m][i / 2];
+                    xf[m] = i % 2 == 0 ? rows8(v.x, v.y) : rows8(v.z, v.w);
+                } else {
+                    Frag f;
+                    f.w = s.x[m][i];
+                    xf[m] = f.v;
                 }
             }
-        };
-
-        for (int seg = 0; seg * kSegment < K; ++seg) {
-            const int c0 = seg * kSegSteps;
-            int steps = (K - seg * kSegment + kStep - 1) / kStep;
-            steps = steps < kSegSteps ? steps : kSegSteps;
-            Stage<MT, FP8> s0, s1;
-            int c = wave;
-            load(c0 + c, s0);
-            if (seg > 0) __syncthreads();  // the scales before are done with
-            // weight scales: 16 bytes of four rows, or one word of one row, per lane
-            const int seg_blocks = blocks - c0 * 4 < kSegment / 32 ? blocks - c0 * 4 : kSegment / 32;
-            const auto scale_row = [&](int r) {
-                const int half = GATED ? r / kOut : 0;
-                int n = GATED ? r % kOut : r;
-                n = n < here ? n : here - 1;
-                return a.scales + (w_row + n + static_cast<int64_t>(half) * N) * blocks + c0 * 4;
-            };
-            if (K % 512 == 0) {
-                for (int r = wave * 4 + group; r < kRows; r += WAVES * 4)
-                    if (r16 * 16 < seg_blocks) {
-                        const u32x4 v = *reinterpret_cast<const u32x4*>(scale_row(r) + r16 * 16);
-                        uint32_t* to = reinterpret_cast<uint32_t*>(&lds_scale[r][r16 * 16]);
-                        to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
-                    }
-            } else {
-                for (int r = wave; r < kRows; r += WAVES)
-                    for (int b = lane; b < (seg_blocks + 3) / 4 * 4; b += kWave)
-                        lds_scale[r][b] = b < seg_blocks ? scale_row(r)[b] : 0;
-            }
-            if constexpr (FP8) {
-                for (int i = threadIdx.x; i < MC * kSegSteps; i += kThreads) {
-                    const int m = i / kSegSteps, q = i % kSegSteps;
-                    float v = 0.0f;
-                    if (m < rows_here && q < steps) {
-                        const int64_t at = (start + m0 + m) * (K / 128) + c0 + q;
-                        v = UE8 ? exponent_value(static_cast<const uint8_t*>(a.row_scales)[at])
-                                : static_cast<const float*>(a.row_scales)[at];
-                    }
-                    lds_row[m][q] = v;
-                }
-            }
-            __syncthreads();
-            // Steps past the end load nothing, but the loads are issued all the
-            // same: a branch around them would make the wait for the present
-            // step's operands one for the next step's too.
-            for (; c < steps; c += 2 * WAVES) {
-                load(c0 + c + WAVES, s1);
-                multiply(c, s0);
-                load(c0 + c + 2 * WAVES, s0);
-                if (c + WAVES < steps) multiply(c + WAVES, s1);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                const bf16x8 wf = weights8(s.w[t][i], sf[t]);
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    part[t][m] =
+                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[m], part[t][m], 0, 0, 0);
             }
         }
-        __syncthreads();  // the scales are done with: their LDS takes the sums
-
-        // lane l holds weight rows 4 * (l / 16) .. + 3 of a tile against row l % 16
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
+        for (int m = 0; m < MT; ++m) {
+            const float xs = FP8 ? lds_row[m * 16 + r16][c] : 1.0f;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-                *reinterpret_cast<f32x4*>(&red[wave][m * 16 + r16][t * 16 + group * 4]) = acc[t][m];
-        __syncthreads();
-        for (int i = threadIdx.x; i < rows_here * kOut; i += kThreads) {
-            const int m = i / kOut, n = i % kOut;
-            if (n < here) {
-                float y = 0.0f, up = 0.0f;
+            for (int t = 0; t < kTiles; ++t) {
+                if constexpr (FP8) {
 #pragma unroll
-                for (int v = 0; v < WAVES; ++v) {
-                    y += red[v][m][n];
-                    if constexpr (GATED) up += red[v][m][kRows / 2 + n];
+                    for (int i = 0; i < 4; ++i)
+                        acc[t][m][i] = fmaf(xs, part[t][m][i], acc[t][m][i]);
+                } else {
+                    acc[t][m] = part[t][m];
                 }
-                if constexpr (GATED) y = y / (1.0f + expf(-y)) * up;
-                a.out[(start + m0 + m) * N + n0 + n] = static_cast<uint16_t>(f32_to_bf16_rne(y));
             }
         }
+    };
+
+    for (int seg = 0; seg * kSegment < K; ++seg) {
+        const int c0 = seg * kSegSteps;
+        int steps = (K - seg * kSegment + kStep - 1) / kStep;
+        steps = steps < kSegSteps ? steps : kSegSteps;
+        // The segment's scales: a word of one row per lane where rows are
+        // whole words.  Their loads go first, so that waiting for them does
+        // not wait for the first step's operands.
+        constexpr int kMine = kRows / WAVES;
+        const int seg_blocks = blocks - c0 * 4 < kSegment / 32 ? blocks - c0 * 4 : kSegment / 32;
+        uint32_t scale[kMine];
+        if constexpr (WORDS) {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int r = wave * kMine + i;
+                scale[i] = __builtin_amdgcn_raw_buffer_load_b32(
+                    r < kOut ? s_view : up_s_view, lane * 4 < seg_blocks && r % kOut < here ? lane * 4 : kNowhere,
+                    (r % kOut) * blocks + c0 * 4, 0);
+            }
+        }
+        constexpr int kRowMine = FP8 ? MC * kSegSteps / kThreads : 1;
+        float row_scale[kRowMine];
+        if constexpr (FP8) {
+#pragma unroll
+            for (int i = 0; i < kRowMine; ++i) {
+                const int m = wave + i * WAVES;  // lane: the step
+                const int64_t at = (start + m0 + m) * (K / 128) + c0 + lane;
+                row_scale[i] = 0.0f;
+                if (m < rows_here && lane < steps)
+                    row_scale[i] =
+                        UE8 ? exponent_value(static_cast<const uint8_t*>(a.row_scales)[at])
+                            : static_cast<const float*>(a.row_scales)[at];
+            }
+        }
+        Stage<MT, FP8> s0, s1;
+        int c = wave;
+        load(c0 + c, s0);
+        if (seg > 0) __syncthreads();  // the scales before are done with
+        if constexpr (WORDS) {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+                *reinterpret_cast<uint32_t*>(&lds_scale[wave * kMine + i][lane * 4]) = scale[i];
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < kMine; ++i) {
+                const int r = wave * kMine + i;
+                for (int q = lane; q < (seg_blocks + 3) / 4 * 4; q += kWave)
+                    lds_scale[r][q] = __builtin_amdgcn_raw_buffer_load_b8(
+                        r < kOut ? s_view : up_s_view, q < seg_blocks && r % kOut < here ? q : kNowhere,
+                        (r % kOut) * blocks + c0 * 4, 0);
+            }
+        }
+        if constexpr (FP8) {
+#pragma unroll
+            for (int i = 0; i < kRowMine; ++i) lds_row[wave + i * WAVES][lane] = row_scale[i];
+        }
         __syncthreads();
+        // Steps past the end load nothing, but the loads are issued all the
+        // same: a branch around them would make the wait for the present
+        // step's operands one for the next step's too.
+        for (; c < steps; c += 2 * WAVES) {
+            load(c0 + c + WAVES, s1);
+            multiply(c, s0);
+            load(c0 + c + 2 * WAVES, s0);
+            if (c + WAVES < steps) multiply(c + WAVES, s1);
+        }
+    }
+    __syncthreads();  // the scales are done with: their LDS takes the sums
+
+    // lane l holds weight rows 4 * (l / 16) .. + 3 of a tile against row l % 16
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            *reinterpret_cast<f32x4*>(&red[wave][m * 16 + r16][t * 16 + group * 4]) = acc[t][m];
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows_here * kOut; i += kThreads) {
+        const int m = i / kOut, n = i % kOut;
+        if (n < here) {
+            float y = 0.0f, up = 0.0f;
+#pragma unroll
+            for (int v = 0; v < WAVES; ++v) {
+                y += red[v][m][n];
+                if constexpr (GATED) up += red[v][m][kRows / 2 + n];
+            }
+            if constexpr (GATED) y = y / (1.0f + expf(-y)) * up;
+            a.out[(start + m0 + m) * N + n0 + n] = static_cast<uint16_t>(f32_to_bf16_rne(y));
+        }
     }
 }
 
 template <int WAVES, int MT>
 void launch_rows(const Args& a, int format, bool gated, dim3 grid, hipStream_t stream) {
-    constexpr int kThreads = WAVES * kWave;
     const auto go = [&](auto* kernel) {
-        hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a);
+        hipLaunchKernelGGL(kernel, grid, dim3(WAVES * kWave), 0, stream, a);
     };
-    if (format == 0)
-        gated ? go(expert_w4_kernel<WAVES, MT, false, false, true>)
-              : go(expert_w4_kernel<WAVES, MT, false, false, false>);
+    if (format == 0 && a.K % kStep != 0)
+        gated ? go(expert_w4_kernel<WAVES, MT, false, false, true, false>)
+              : go(expert_w4_kernel<WAVES, MT, false, false, false, false>);
+    else if (format == 0)
+        gated ? go(expert_w4_kernel<WAVES, MT, false, false, true, true>)
+              : go(expert_w4_kernel<WAVES, MT, false, false, false, true>);
     else if (format == 1)
-        gated ? go(expert_w4_kernel<WAVES, MT, true, false, true>)
-              : go(expert_w4_kernel<WAVES, MT, true, false, false>);
+        gated ? go(expert_w4_kernel<WAVES, MT, true, false, true, true>)
+              : go(expert_w4_kernel<WAVES, MT, true, false, false, true>);
     else
-        gated ? go(expert_w4_kernel<WAVES, MT, true, true, true>)
-              : go(expert_w4_kernel<WAVES, MT, true, true, false>);
+        gated ? go(expert_w4_kernel<WAVES, MT, true, true, true, true>)
+              : go(expert_w4_kernel<WAVES, MT, true, true, false, true>);
 }
 
 }  // namespace
@@ -402,7 +419,6 @@ hipError_t launch_expert_w4(const ep_problem& p, const ep_expert_w4_t& mm, const
     a.rows = static_cast<const uint8_t*>(rows);
     a.row_scales = row_scales;
     a.count = layout.count;
-    a.offset = layout.offset;
     a.codes = codes;
     a.scales = scales;
     a.out = static_cast<uint16_t*>(out);
@@ -416,9 +432,10 @@ hipError_t launch_expert_w4(const ep_problem& p, const ep_expert_w4_t& mm, const
     const int64_t experts = p.num_experts < filled ? p.num_experts : filled;
     const int64_t mean = filled / experts;
     const int mt = mean > 24 ? 4 : mean > 8 ? 2 : 1;
-    a.tiles = experts + filled / (16 * mt);
-    const dim3 grid((mm.out_features + outs - 1) / outs,
-                    static_cast<unsigned>(a.tiles < 32768 ? a.tiles : 32768));
+    const int64_t tiles = experts + filled / (16 * mt);
+    const int64_t y = tiles < 32768 ? tiles : 32768;
+    const dim3 grid((mm.out_features + outs - 1) / outs, static_cast<unsigned>(y),
+                    static_cast<unsigned>((tiles + y - 1) / y));
     switch (mt) {
         case 1: launch_rows<4, 1>(a, mm.in_format, gated, grid, stream); break;
         case 2: launch_rows<4, 2>(a, mm.in_format, gated, grid, stream); break;
