@@ -93,8 +93,23 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t view(const void* p, uint32_t b
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
 }
 constexpr uint32_t kNowhere = 0x7fffff00u;  // past the end of every view
+template <bool ONCE>  // not kept in the caches
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t step) {
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, step, 0));
+    return __builtin_bit_cast(u32x4,
+                              __builtin_amdgcn_raw_buffer_load_b128(r, at, step, ONCE ? 2 : 0));
+}
+
+// a: rows 0-7, b: rows 8-15 of a weight tile, lane l of a row of 16 lanes
+// holding row l % 8 and, below lane 8, the first chunk, from lane 8 on, the
+// second one.  Afterwards a is the first chunk and b the second one, lane l
+// holding row l: lanes 8-15 of a and 0-7 of b change places.
+__device__ __forceinline__ void pair_chunks(u32x4& a, u32x4& b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int x = static_cast<int>(a[i]), y = static_cast<int>(b[i]);
+        a[i] = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(x, y, 0x128, 0xf, 0xc, false));
+        b[i] = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(y, x, 0x128, 0xf, 0x3, false));
+    }
 }
 
 // The expert, rows and row tile that number `want` names: experts with rows,
@@ -157,11 +172,11 @@ __device__ __forceinline__ Found find_tile(const Args& a, uint32_t want) {
     return f;
 }
 
-// One step's operands of a wave.
+// One step's operands of a wave: two chunks of 128 channels.
 template <int MT, bool FP8>
 struct Stage {
-    u32x4 w[kTiles];
-    u32x4 x[MT][FP8 ? 2 : 4];
+    u32x4 w[2][kTiles];
+    u32x4 x[2][MT][FP8 ? 2 : 4];
 };
 
 // Few rows per expert.  FP8: rows are E4M3FN with one scale per 128 channels
@@ -212,15 +227,12 @@ __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void e
     const auto s_view = view(a.scales + w_row * blocks, here * blocks);
     const auto up_s_view = view(a.scales + (w_row + (GATED ? N : 0)) * blocks, here * blocks);
     const auto x_view = view(a.rows + (start + m0) * x_pitch, rows_here * x_pitch);
-    uint32_t w_at[kOut / 16], x_at[MT];
-#pragma unroll
-    for (int t = 0; t < kOut / 16; ++t)
-        w_at[t] = t * 16 + r16 < here ? (t * 16 + r16) * w_pitch + group * 16 : kNowhere;
+    const int half = lane / 8 % 2;
+    const uint32_t w_at = lane % 8 * w_pitch + half * 64 + group * 16;
+    uint32_t x_at[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
-        x_at[m] = m * 16 + r16 < rows_here
-                      ? (m * 16 + r16) * x_pitch + group * (FP8 ? 32 : 64)
-                      : kNowhere;
+        x_at[m] = (m * 16 + r16) * x_pitch + group * (FP8 ? 32 : 64);
 
     f32x4 acc[kTiles][MT];
 #pragma unroll
@@ -228,21 +240,29 @@ __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void e
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[t][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    const auto load = [&](int c, Stage<MT, FP8>& s) {
-        const bool has = c * 4 + group < blocks;
+    const auto load = [&](int p, Stage<MT, FP8>& s) {  // chunks 2p and 2p + 1
+        const uint32_t at = p * 8 + half * 4 + group < blocks ? w_at : kNowhere;
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-            const uint32_t at = w_at[t % (kOut / 16)];
-            s.w[t] = load16(GATED && t >= 2 ? up_view : w_view, has ? at : kNowhere, c * 64);
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                s.w[i][t] = load16<true>(GATED && t >= 2 ? up_view : w_view,
+                                         at + ((GATED ? t % 2 : t) * 16 + i * 8) * w_pitch, p * 128);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool has = p * 8 + h * 4 + group < blocks;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < (FP8 ? 2 : 4); ++i)
+                    s.x[h][m][i] = load16<false>(x_view, has ? x_at[m] : kNowhere,
+                                                 (2 * p + h) * (FP8 ? 128 : 256) + i * 16);
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < (FP8 ? 2 : 4); ++i)
-                s.x[m][i] = load16(x_view, has ? x_at[m] : kNowhere,
-                                   c * (FP8 ? 128 : 256) + i * 16);
+        for (int t = 0; t < kTiles; ++t) pair_chunks(s.w[0][t], s.w[1][t]);
     };
-    const auto multiply = [&](int c, const Stage<MT, FP8>& s) {  // c within the segment
+    const auto multiply = [&](int c, const u32x4(&w)[kTiles],
+                              const u32x4(&x)[MT][FP8 ? 2 : 4]) {  // c within the segment
         float sf[kTiles];
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
@@ -261,17 +281,17 @@ __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void e
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 if constexpr (FP8) {
-                    const u32x4 v = s.x[m][i / 2];
+                    const u32x4 v = x[m][i / 2];
                     xf[m] = i % 2 == 0 ? rows8(v.x, v.y) : rows8(v.z, v.w);
                 } else {
                     Frag f;
-                    f.w = s.x[m][i];
+                    f.w = x[m][i];
                     xf[m] = f.v;
                 }
             }
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
-                const bf16x8 wf = weights8(s.w[t][i], sf[t]);
+                const bf16x8 wf = weights8(w[t][i], sf[t]);
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
                     part[t][m] =
@@ -327,9 +347,6 @@ __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void e
                             : static_cast<const float*>(a.row_scales)[at];
             }
         }
-        Stage<MT, FP8> s0, s1;
-        int c = wave;
-        load(c0 + c, s0);
         if (seg > 0) __syncthreads();  // the scales before are done with
         if constexpr (WORDS) {
 #pragma unroll
@@ -350,14 +367,11 @@ __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void e
             for (int i = 0; i < kRowMine; ++i) lds_row[wave + i * WAVES][lane] = row_scale[i];
         }
         __syncthreads();
-        // Steps past the end load nothing, but the loads are issued all the
-        // same: a branch around them would make the wait for the present
-        // step's operands one for the next step's too.
-        for (; c < steps; c += 2 * WAVES) {
-            load(c0 + c + WAVES, s1);
-            multiply(c, s0);
-            load(c0 + c + 2 * WAVES, s0);
-            if (c + WAVES < steps) multiply(c + WAVES, s1);
+        for (int p = wave; 2 * p < steps; p += WAVES) {
+            Stage<MT, FP8> s;
+            load(c0 / 2 + p, s);
+            multiply(2 * p, s.w[0], s.x[0]);
+            if (2 * p + 1 < steps) multiply(2 * p + 1, s.w[1], s.x[1]);
         }
     }
     __syncthreads();  // the scales are done with: their LDS takes the sums
