@@ -401,23 +401,262 @@ __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void e
     }
 }
 
-template <int WAVES, int MT>
-void launch_rows(const Args& a, int format, bool gated, dim3 grid, hipStream_t stream) {
-    const auto go = [&](auto* kernel) {
-        hipLaunchKernelGGL(kernel, grid, dim3(WAVES * kWave), 0, stream, a);
+// Many rows per expert: a workgroup takes 256 weight rows, 64 per wave, against
+// up to 16 * MT rows.  The rows' operands are the same for the four waves: each
+// chunk of 128 channels passes through LDS, as bf16, once for all of them,
+// while the next chunk is on its way; the weights' next pair of chunks is in
+// flight as in the kernel above.  GATED: a wave's tiles 0, 1 are gate and 2, 3
+// up of the same 32 outputs.
+constexpr int kTileSegment = 4096;                 // channels of weight scales in LDS
+constexpr int kTileScaleRow = kTileSegment / 32 + 4;  // bytes
+constexpr int kTileRow = kStep * 2 + 16;           // bytes of a row's chunk in LDS
+
+template <int MT, bool FP8, bool UE8, bool GATED, bool WORDS>
+__global__ __launch_bounds__(256, 2) void expert_w4_tile_kernel(Args a) {
+    constexpr int MC = 16 * MT;
+    constexpr int kOut = GATED ? kRows / 2 : kRows;  // outputs per wave
+    constexpr int kPieces = FP8 ? 8 : 16;            // 16-byte pieces of a row's chunk
+    constexpr int kMine = MC * kPieces / 256;        // pieces per thread
+    __shared__ __attribute__((aligned(16))) uint8_t lds_x[2][MC][kTileRow];
+    __shared__ float lds_row[2][MC];
+    __shared__ uint32_t lds_scale[4 * kRows][kTileScaleRow / 4];
+
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int r16 = lane % 16, group = lane / 16;
+    const int K = a.K, N = a.N;
+    const int blocks = K / 32;
+    const int steps = (K + kStep - 1) / kStep;
+    const int n0 = (blockIdx.x * 4 + wave) * kOut;
+    const int left = N - n0 < kOut ? N - n0 : kOut;
+    const int here = left > 0 ? left : 0;  // outputs of this wave
+
+    const Found f = find_tile<MC>(a, blockIdx.z * gridDim.y + blockIdx.y);
+    if (f.expert < 0) return;
+    const int m0 = f.tile * MC;
+    const int rows_here = f.count - m0 < MC ? f.count - m0 : MC;
+    if (rows_here <= 0) return;
+    const int64_t row0 = f.start + m0;
+
+    const int64_t w_row = static_cast<int64_t>(f.expert) * (GATED ? 2 * N : N) + (here ? n0 : 0);
+    const uint32_t w_pitch = K / 2;
+    const uint32_t x_pitch = K * (FP8 ? 1 : 2);
+    const auto w_view = view(a.codes + w_row * w_pitch, here * w_pitch);
+    const auto up_view = view(a.codes + (w_row + (GATED ? N : 0)) * w_pitch, here * w_pitch);
+    const auto x_view = view(a.rows + row0 * x_pitch, rows_here * x_pitch);
+    const int half = lane / 8 % 2;
+    const uint32_t w_at = lane % 8 * w_pitch + half * 64 + group * 16;
+
+    f32x4 acc[kTiles][MT];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[t][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    u32x4 next_w[2][kTiles];
+    const auto load_w = [&](int p) {  // chunks 2p and 2p + 1; nothing past the end
+        const uint32_t at = p * 8 + half * 4 + group < blocks ? w_at : kNowhere;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                next_w[i][t] = load16<false>(t * 16 < kOut ? w_view : up_view,
+                                             at + (t * 16 % kOut + i * 8) * w_pitch, p * 128);
     };
-    if (format == 0 && a.K % kStep != 0)
-        gated ? go(expert_w4_kernel<WAVES, MT, false, false, true, false>)
-              : go(expert_w4_kernel<WAVES, MT, false, false, false, false>);
-    else if (format == 0)
-        gated ? go(expert_w4_kernel<WAVES, MT, false, false, true, true>)
-              : go(expert_w4_kernel<WAVES, MT, false, false, false, true>);
-    else if (format == 1)
-        gated ? go(expert_w4_kernel<WAVES, MT, true, false, true, true>)
-              : go(expert_w4_kernel<WAVES, MT, true, false, false, true>);
+    u32x4 next_x[kMine];
+    float next_row;
+    const auto load_x = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int at = threadIdx.x + i * 256;
+            const int m = at / kPieces, q = at % kPieces;
+            const bool has = c * 4 + q / (kPieces / 4) < blocks;
+            next_x[i] = load16<false>(x_view, has ? m * x_pitch + q * 16 : kNowhere, c * kPieces * 16);
+        }
+        if constexpr (FP8) {
+            const int m = threadIdx.x;
+            next_row = 0.0f;
+            if (m < rows_here && c < steps) {
+                const int64_t at = (row0 + m) * (K / kStep) + c;
+                next_row = UE8 ? exponent_value(static_cast<const uint8_t*>(a.row_scales)[at])
+                               : static_cast<const float*>(a.row_scales)[at];
+            }
+        }
+    };
+    const auto store_x = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int at = threadIdx.x + i * 256;
+            const int m = at / kPieces, q = at % kPieces;
+            if constexpr (FP8) {
+                Frag lo, hi;
+                lo.v = rows8(next_x[i].x, next_x[i].y);
+                hi.v = rows8(next_x[i].z, next_x[i].w);
+                *reinterpret_cast<u32x4*>(&lds_x[buf][m][q * 32]) = lo.w;
+                *reinterpret_cast<u32x4*>(&lds_x[buf][m][q * 32 + 16]) = hi.w;
+            } else {
+                *reinterpret_cast<u32x4*>(&lds_x[buf][m][q * 16]) = next_x[i];
+            }
+        }
+        if constexpr (FP8) {
+            if (threadIdx.x < MC) lds_row[buf][threadIdx.x] = next_row;
+        }
+    };
+    // The wave's own rows of weight scales: a word of two rows per lane.
+    const auto stage_scales = [&](int first_block) {
+        const int n_words = kTileSegment / 32 / 4;
+#pragma unroll 8
+        for (int i = 0; i < kRows * n_words / kWave; ++i) {
+            const int r = i * 2 + lane / n_words, q = lane % n_words;
+            const int n = r % kOut, b = first_block + q * 4;
+            const uint32_t at = n * blocks + b;
+            const auto from =
+                view(a.scales + (w_row + (i * 2 < kOut ? 0 : N)) * blocks, here * blocks);
+            uint32_t v = 0;
+            if constexpr (WORDS) {
+                v = __builtin_amdgcn_raw_buffer_load_b32(from, b < blocks ? at : kNowhere, 0, 0);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v |= static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b8(
+                             from, b + k < blocks ? at + k : kNowhere, 0, 0))
+                         << (8 * k);
+            }
+            lds_scale[wave * kRows + r][q] = v;
+        }
+    };
+    const auto multiply = [&](int c, const u32x4(&w)[kTiles], int buf) {
+        float sf[kTiles];
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            const uint32_t word = lds_scale[wave * kRows + t * 16 + r16][c % (kTileSegment / kStep)];
+            sf[t] = __uint_as_float((word >> (8 * group) & 0xffu) << 23);
+        }
+        f32x4 part[kTiles][MT];
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                part[t][m] = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[t][m];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+            bf16x8 xf[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                Frag x;
+                x.w = *reinterpret_cast<const u32x4*>(&lds_x[buf][m * 16 + r16][group * 64 + i * 16]);
+                xf[m] = x.v;
+            }
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                const bf16x8 wf = weights8(w[t][i], sf[t]);
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    part[t][m] =
+                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[m], part[t][m], 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const float xs = FP8 ? lds_row[buf][m * 16 + r16] : 1.0f;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[t][m][i] = fmaf(xs, part[t][m][i], acc[t][m][i]);
+                } else {
+                    acc[t][m] = part[t][m];
+                }
+            }
+        }
+    };
+
+    load_x(0);
+    load_w(0);
+    store_x(0);
+    u32x4 w[2][kTiles];
+    for (int p = 0; 2 * p < steps; ++p) {
+        const int c = 2 * p;
+        // a segment's rows of scales are this wave's own: no barrier
+        if (c % (kTileSegment / kStep) == 0) stage_scales(c * 4);
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            w[0][t] = next_w[0][t];
+            w[1][t] = next_w[1][t];
+            pair_chunks(w[0][t], w[1][t]);
+        }
+        load_x(c + 1);
+        load_w(p + 1);
+        multiply(c, w[0], 0);
+        store_x(1);
+        __syncthreads();
+        load_x(c + 2);
+        if (c + 1 < steps) multiply(c + 1, w[1], 1);
+        store_x(0);
+    }
+
+    // lane l holds outputs 4 * (l / 16) .. + 3 of a tile for row l % 16
+#pragma unroll
+    for (int t = 0; t < kOut / 16; ++t)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int n = t * 16 + group * 4;
+            if (m * 16 + r16 >= rows_here) continue;
+            uint16_t* to = a.out + (row0 + m * 16 + r16) * N + n0 + n;
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v = acc[t][m][i];
+                if constexpr (GATED) v = v / (1.0f + expf(-v)) * acc[t + kOut / 16][m][i];
+                y[i] = f32_to_bf16_rne(v);
+            }
+            if (N % 4 == 0) {
+                if (n < here)
+                    *reinterpret_cast<uint2*>(to) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n + i < here) to[i] = static_cast<uint16_t>(y[i]);
+            }
+        }
+}
+
+// The kernel of WAVES waves for few rows, or (WAVES 0) the one for many.
+template <int WAVES, int MT, bool FP8, bool UE8, bool GATED, bool WORDS>
+void launch_one(const Args& a, dim3 grid, hipStream_t stream) {
+    if constexpr (WAVES == 0)
+        hipLaunchKernelGGL((expert_w4_tile_kernel<MT, FP8, UE8, GATED, WORDS>), grid, dim3(256), 0,
+                           stream, a);
     else
-        gated ? go(expert_w4_kernel<WAVES, MT, true, true, true, true>)
-              : go(expert_w4_kernel<WAVES, MT, true, true, false, true>);
+        hipLaunchKernelGGL((expert_w4_kernel<WAVES, MT, FP8, UE8, GATED, WORDS>), grid,
+                           dim3(WAVES * kWave), 0, stream, a);
+}
+
+template <int WAVES, int MT, bool GATED>
+void launch_format(const Args& a, int format, dim3 grid, hipStream_t stream) {
+    if (format == 1)
+        launch_one<WAVES, MT, true, false, GATED, true>(a, grid, stream);
+    else if (format == 2)
+        launch_one<WAVES, MT, true, true, GATED, true>(a, grid, stream);
+    else if (a.K % kStep == 0)
+        launch_one<WAVES, MT, false, false, GATED, true>(a, grid, stream);
+    else
+        launch_one<WAVES, MT, false, false, GATED, false>(a, grid, stream);
+}
+
+template <int WAVES, int MT>
+void launch_rows(const Args& a, int format, bool gated, int64_t tiles, hipStream_t stream) {
+    const int outs = (gated ? kRows / 2 : kRows) * (WAVES == 0 ? 4 : 1);
+    const int64_t y = tiles < 32768 ? tiles : 32768;
+    const dim3 grid((a.N + outs - 1) / outs, static_cast<unsigned>(y),
+                    static_cast<unsigned>((tiles + y - 1) / y));
+    if (gated)
+        launch_format<WAVES, MT, true>(a, format, grid, stream);
+    else
+        launch_format<WAVES, MT, false>(a, format, grid, stream);
 }
 
 }  // namespace
@@ -431,7 +670,6 @@ hipError_t launch_expert_w4(const ep_problem& p, const ep_expert_w4_t& mm, const
     const int64_t filled = p.capacity > 0 && held < entries ? held : entries;
     if (filled == 0) return hipSuccess;
     const bool gated = mm.activation == 1;
-    const int outs = gated ? kRows / 2 : kRows;
     Args a;
     a.rows = static_cast<const uint8_t*>(rows);
     a.row_scales = row_scales;
@@ -448,23 +686,17 @@ hipError_t launch_expert_w4(const ep_problem& p, const ep_expert_w4_t& mm, const
     // full tile.
     const int64_t experts = p.num_experts < filled ? p.num_experts : filled;
     const int64_t mean = filled / experts;
-    const int mt = mean > 24 ? 4 : mean > 8 ? 2 : 1;
-    const int64_t tiles = experts + filled / (16 * mt);
-    const int64_t y = tiles < 32768 ? tiles : 32768;
-    const dim3 grid((mm.out_features + outs - 1) / outs, static_cast<unsigned>(y),
-                    static_cast<unsigned>((tiles + y - 1) / y));
+    const auto tiles = [&](int mc) { return experts + filled / mc; };
     // Two waves where four would have less than four steps each (K 2048, 256
     // experts: 343 us against 403; K 7168: 589 against 587).
-    switch (mt) {
-        case 1:
-            if (a.K < 4 * 4 * 2 * kStep)
-                launch_rows<2, 1>(a, mm.in_format, gated, grid, stream);
-            else
-                launch_rows<4, 1>(a, mm.in_format, gated, grid, stream);
-            break;
-        case 2: launch_rows<4, 2>(a, mm.in_format, gated, grid, stream); break;
-        default: launch_rows<4, 4>(a, mm.in_format, gated, grid, stream); break;
-    }
+    if (mean > 24)
+        launch_rows<0, 4>(a, mm.in_format, gated, tiles(64), stream);
+    else if (mean > 8)
+        launch_rows<0, 2>(a, mm.in_format, gated, tiles(32), stream);
+    else if (a.K < 4 * 4 * 2 * kStep)
+        launch_rows<2, 1>(a, mm.in_format, gated, tiles(16), stream);
+    else
+        launch_rows<4, 1>(a, mm.in_format, gated, tiles(16), stream);
     return hipGetLastError();
 }
 
