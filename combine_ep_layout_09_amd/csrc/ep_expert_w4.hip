@@ -88,9 +88,14 @@ __device__ __forceinline__ bf16x8 rows8(uint32_t lo, uint32_t hi) {
 }
 
 // Bounded view of `bytes` bytes at p: loads past its end give 0 and touch
-// nothing.  p and bytes are the same in every lane.
+// nothing.  p and bytes are the same in every lane, and said to be: a view in
+// vector registers is loaded through in a loop over its values.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t view(const void* p, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint64_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+    const uint64_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(hi << 32 | (lo & 0xffffffffu)),
+                                             0, __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
 }
 constexpr uint32_t kNowhere = 0x7fffff00u;  // past the end of every view
 template <bool ONCE>  // not kept in the caches
@@ -112,16 +117,17 @@ __device__ __forceinline__ void pair_chunks(u32x4& a, u32x4& b) {
     }
 }
 
-// The expert, rows and row tile that number `want` names: experts with rows,
-// in order, each with one tile per MC rows; expert -1 if there are fewer.
+// The expert, rows and row tile that number pick(number of tiles) names: experts
+// with rows, in order, each with one tile per MC rows; expert -1 if there are
+// fewer.
 // Every wave finds it by itself, a lane per run of experts, so no wave waits
 // for another; contiguous rows start where the counts before them end.
 struct Found {
     int expert, count, tile;
     int64_t start;
 };
-template <int MC>
-__device__ __forceinline__ Found find_tile(const Args& a, uint32_t want) {
+template <int MC, class Pick>
+__device__ __forceinline__ Found find_tile(const Args& a, Pick pick) {
     const int lane = threadIdx.x % kWave;
     const int per = (a.num_experts + kWave - 1) / kWave;
     // Counts of another problem's layout must not lead outside the rows: all
@@ -148,6 +154,7 @@ __device__ __forceinline__ Found find_tile(const Args& a, uint32_t want) {
             tiles_to = min(tiles_to + q, top_tiles);
         }
     }
+    const uint32_t want = pick(__builtin_amdgcn_readlane(tiles_to, kWave - 1));
     const uint64_t beyond = __ballot(tiles_to > want);
     Found f{-1, 0, 0, 0};
     if (beyond == 0) return f;
@@ -211,7 +218,7 @@ __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void e
     const int n0 = blockIdx.x * kOut;
     const int here = N - n0 < kOut ? N - n0 : kOut;  // outputs of this workgroup
 
-    const Found f = find_tile<MC>(a, blockIdx.z * gridDim.y + blockIdx.y);
+    const Found f = find_tile<MC>(a, [](uint32_t) { return blockIdx.z * gridDim.y + blockIdx.y; });
     const int e = f.expert;
     if (e < 0) return;
     const int64_t start = f.start;
@@ -427,12 +434,24 @@ __global__ __launch_bounds__(256, 2) void expert_w4_tile_kernel(Args a) {
     const int K = a.K, N = a.N;
     const int blocks = K / 32;
     const int steps = (K + kStep - 1) / kStep;
-    const int n0 = (blockIdx.x * 4 + wave) * kOut;
+    // Workgroups go round the 8 XCDs in turn.  Each XCD takes a run of items
+    // (row tile, output block), so that its L2 serves one tile's rows to that
+    // tile's blocks, and one expert's weights to that expert's tiles.
+    const uint32_t n_blocks = (N + 4 * kOut - 1) / (4 * kOut);
+    const uint64_t id = static_cast<uint64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+    uint32_t block = 0;
+    const Found f = find_tile<MC>(a, [&](uint32_t tiles) {
+        const uint64_t items = static_cast<uint64_t>(tiles) * n_blocks;
+        const uint64_t run = (items + 7) / 8;
+        const uint64_t item = id % 8 * run + id / 8;
+        if (id / 8 >= run || item >= items) return 0xffffffffu;
+        block = static_cast<uint32_t>(item % n_blocks);
+        return static_cast<uint32_t>(item / n_blocks);
+    });
+    if (f.expert < 0) return;
+    const int n0 = (block * 4 + wave) * kOut;
     const int left = N - n0 < kOut ? N - n0 : kOut;
     const int here = left > 0 ? left : 0;  // outputs of this wave
-
-    const Found f = find_tile<MC>(a, blockIdx.z * gridDim.y + blockIdx.y);
-    if (f.expert < 0) return;
     const int m0 = f.tile * MC;
     const int rows_here = f.count - m0 < MC ? f.count - m0 : MC;
     if (rows_here <= 0) return;
@@ -463,55 +482,76 @@ __global__ __launch_bounds__(256, 2) void expert_w4_tile_kernel(Args a) {
                 next_w[i][t] = load16<false>(t * 16 < kOut ? w_view : up_view,
                                              at + (t * 16 % kOut + i * 8) * w_pitch, p * 128);
     };
-    u32x4 next_x[kMine];
-    float next_row;
-    const auto load_x = [&](int c) {
+    // A chunk's rows on their way to LDS: even and odd chunks have a set each,
+    // loaded two chunks ahead.
+    struct Ahead {
+        u32x4 x[kMine];
+        float row;
+    };
+    const auto load_x = [&](Ahead& s, int c) {
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int at = threadIdx.x + i * 256;
             const int m = at / kPieces, q = at % kPieces;
             const bool has = c * 4 + q / (kPieces / 4) < blocks;
-            next_x[i] = load16<false>(x_view, has ? m * x_pitch + q * 16 : kNowhere, c * kPieces * 16);
+            s.x[i] = load16<false>(x_view, has ? m * x_pitch + q * 16 : kNowhere, c * kPieces * 16);
         }
         if constexpr (FP8) {
             const int m = threadIdx.x;
-            next_row = 0.0f;
+            s.row = 0.0f;
             if (m < rows_here && c < steps) {
                 const int64_t at = (row0 + m) * (K / kStep) + c;
-                next_row = UE8 ? exponent_value(static_cast<const uint8_t*>(a.row_scales)[at])
-                               : static_cast<const float*>(a.row_scales)[at];
+                s.row = UE8 ? exponent_value(static_cast<const uint8_t*>(a.row_scales)[at])
+                            : static_cast<const float*>(a.row_scales)[at];
             }
         }
     };
-    const auto store_x = [&](int buf) {
+    const auto store_x = [&](const Ahead& s, int buf) {
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int at = threadIdx.x + i * 256;
             const int m = at / kPieces, q = at % kPieces;
             if constexpr (FP8) {
                 Frag lo, hi;
-                lo.v = rows8(next_x[i].x, next_x[i].y);
-                hi.v = rows8(next_x[i].z, next_x[i].w);
+                lo.v = rows8(s.x[i].x, s.x[i].y);
+                hi.v = rows8(s.x[i].z, s.x[i].w);
                 *reinterpret_cast<u32x4*>(&lds_x[buf][m][q * 32]) = lo.w;
                 *reinterpret_cast<u32x4*>(&lds_x[buf][m][q * 32 + 16]) = hi.w;
             } else {
-                *reinterpret_cast<u32x4*>(&lds_x[buf][m][q * 16]) = next_x[i];
+                *reinterpret_cast<u32x4*>(&lds_x[buf][m][q * 16]) = s.x[i];
             }
         }
         if constexpr (FP8) {
-            if (threadIdx.x < MC) lds_row[buf][threadIdx.x] = next_row;
+            if (threadIdx.x < MC) lds_row[buf][threadIdx.x] = s.row;
         }
     };
-    // The wave's own rows of weight scales: a word of two rows per lane.
+    // The wave's own rows of weight scales.  16 bytes of eight rows per load
+    // where every piece lies whole in a row, else a word of two rows.
+    const auto scale_view = [&](int r) {
+        return view(a.scales + (w_row + (r < kOut ? 0 : N)) * blocks, here * blocks);
+    };
     const auto stage_scales = [&](int first_block) {
-        const int n_words = kTileSegment / 32 / 4;
-#pragma unroll 8
+        constexpr int n_words = kTileSegment / 32 / 4;
+        if (WORDS && K % (16 * 32) == 0) {
+            u32x4 v[kRows / 8];
+#pragma unroll
+            for (int i = 0; i < kRows / 8; ++i) {
+                const int n = (i * 8 + lane / 8) % kOut, b = first_block + lane % 8 * 16;
+                v[i] = load16<false>(scale_view(i * 8), b < blocks ? n * blocks + b : kNowhere, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < kRows / 8; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    lds_scale[wave * kRows + i * 8 + lane / 8][lane % 8 * 4 + k] = v[i][k];
+            return;
+        }
+#pragma unroll 4
         for (int i = 0; i < kRows * n_words / kWave; ++i) {
             const int r = i * 2 + lane / n_words, q = lane % n_words;
             const int n = r % kOut, b = first_block + q * 4;
             const uint32_t at = n * blocks + b;
-            const auto from =
-                view(a.scales + (w_row + (i * 2 < kOut ? 0 : N)) * blocks, here * blocks);
+            const auto from = scale_view(i * 2);
             uint32_t v = 0;
             if constexpr (WORDS) {
                 v = __builtin_amdgcn_raw_buffer_load_b32(from, b < blocks ? at : kNowhere, 0, 0);
@@ -573,14 +613,18 @@ __global__ __launch_bounds__(256, 2) void expert_w4_tile_kernel(Args a) {
         }
     };
 
-    load_x(0);
+    Ahead even, odd;
+    load_x(even, 0);
+    stage_scales(0);
     load_w(0);
-    store_x(0);
+    load_x(odd, 1);
+    store_x(even, 0);
+    load_x(even, 2);
     u32x4 w[2][kTiles];
     for (int p = 0; 2 * p < steps; ++p) {
         const int c = 2 * p;
         // a segment's rows of scales are this wave's own: no barrier
-        if (c % (kTileSegment / kStep) == 0) stage_scales(c * 4);
+        if (c > 0 && c % (kTileSegment / kStep) == 0) stage_scales(c * 4);
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
@@ -588,14 +632,18 @@ __global__ __launch_bounds__(256, 2) void expert_w4_tile_kernel(Args a) {
             w[1][t] = next_w[1][t];
             pair_chunks(w[0][t], w[1][t]);
         }
-        load_x(c + 1);
         load_w(p + 1);
+        __builtin_amdgcn_s_setprio(1);  // over the workgroup that loads
         multiply(c, w[0], 0);
-        store_x(1);
+        __builtin_amdgcn_s_setprio(0);
+        store_x(odd, 1);
+        load_x(odd, c + 3);
         __syncthreads();
-        load_x(c + 2);
+        __builtin_amdgcn_s_setprio(1);
         if (c + 1 < steps) multiply(c + 1, w[1], 1);
-        store_x(0);
+        __builtin_amdgcn_s_setprio(0);
+        store_x(even, 0);
+        load_x(even, c + 4);
     }
 
     // lane l holds outputs 4 * (l / 16) .. + 3 of a tile for row l % 16
@@ -650,9 +698,17 @@ void launch_format(const Args& a, int format, dim3 grid, hipStream_t stream) {
 template <int WAVES, int MT>
 void launch_rows(const Args& a, int format, bool gated, int64_t tiles, hipStream_t stream) {
     const int outs = (gated ? kRows / 2 : kRows) * (WAVES == 0 ? 4 : 1);
-    const int64_t y = tiles < 32768 ? tiles : 32768;
-    const dim3 grid((a.N + outs - 1) / outs, static_cast<unsigned>(y),
+    const int64_t blocks = (a.N + outs - 1) / outs;
+    dim3 grid;
+    if (WAVES == 0) {  // a row of ids whose length 8 divides
+        const int64_t items = (tiles * blocks + 7) / 8 * 8;
+        const int64_t x = items < (1 << 20) ? items : 1 << 20;
+        grid = dim3(static_cast<unsigned>(x), static_cast<unsigned>((items + x - 1) / x));
+    } else {
+        const int64_t y = tiles < 32768 ? tiles : 32768;
+        grid = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(y),
                     static_cast<unsigned>((tiles + y - 1) / y));
+    }
     if (gated)
         launch_format<WAVES, MT, true>(a, format, grid, stream);
     else
