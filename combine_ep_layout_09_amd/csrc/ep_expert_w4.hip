@@ -685,11 +685,11 @@ void launch_one(const Args& a, dim3 grid, hipStream_t stream) {
 
 template <int WAVES, int MT, bool GATED>
 void launch_format(const Args& a, int format, dim3 grid, hipStream_t stream) {
-    if (format == 1)
-        launch_one<WAVES, MT, true, false, GATED, true>(a, grid, stream);
-    else if (format == 2)
-        launch_one<WAVES, MT, true, true, GATED, true>(a, grid, stream);
-    else if (a.K % kStep == 0)
+    if constexpr (MT < 4) {
+        if (format == 1) return launch_one<WAVES, MT, true, false, GATED, true>(a, grid, stream);
+        if (format == 2) return launch_one<WAVES, MT, true, true, GATED, true>(a, grid, stream);
+    }
+    if (a.K % kStep == 0)
         launch_one<WAVES, MT, false, false, GATED, true>(a, grid, stream);
     else
         launch_one<WAVES, MT, false, false, GATED, false>(a, grid, stream);
@@ -743,11 +743,16 @@ hipError_t launch_expert_w4(const ep_problem& p, const ep_expert_w4_t& mm, const
     const int64_t experts = p.num_experts < filled ? p.num_experts : filled;
     const int64_t mean = filled / experts;
     const auto tiles = [&](int mc) { return experts + filled / mc; };
-    // Two waves where four would have less than four steps each (K 2048, 256
-    // experts: 343 us against 403; K 7168: 589 against 587).
-    if (mean > 24)
+    // By the mean rows of an expert, measured at 64 experts, K 4096, N 1408:
+    // bf16 rows 8: 44 us with the few-row kernel, 47 with 32-row tiles; 12: 51,
+    // 48; 24: 90, 51 and 63 with 64-row tiles; 128: 146 and 126.  FP8 rows, whose
+    // 64-row tile does not fit the registers: 12: 42, 51; 48 (skewed): 234, 155.
+    // Few-row kernel: two waves where four would have less than four steps each
+    // (K 2048, 256 experts: 343 us against 403; K 7168: 589 against 587).
+    const bool fp8 = mm.in_format != 0;
+    if (!fp8 && mean > 48)
         launch_rows<0, 4>(a, mm.in_format, gated, tiles(64), stream);
-    else if (mean > 8)
+    else if (mean > (fp8 ? 16 : 8))
         launch_rows<0, 2>(a, mm.in_format, gated, tiles(32), stream);
     else if (a.K < 4 * 4 * 2 * kStep)
         launch_rows<2, 1>(a, mm.in_format, gated, tiles(16), stream);
