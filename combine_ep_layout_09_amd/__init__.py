@@ -465,12 +465,26 @@ def _arg(t, name, dtype, numel, dev, allow_none=False):
     return t.data_ptr()
 
 
+def _raw_stream(dev):
+    """Handle of the current stream of device `dev`; the raw call costs 0.1 us,
+    a torch.cuda.Stream object for it 1.1."""
+    global _raw_stream
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        def raw(d):
+            return torch.cuda.current_stream(d).cuda_stream
+    _raw_stream = raw
+    return raw(dev)
+
+
 def _issue(name, fn, args, dev, stream):
     """The C call on device `dev`, on its current stream by default."""
     torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    handle = stream if isinstance(stream, int) else stream.cuda_stream
+        handle = _raw_stream(dev)
+    else:
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
     if torch.cuda.current_device() == dev:
         code = fn(*args, handle)
     else:

@@ -133,7 +133,7 @@ int check_logits(const ep_routing& rt, const void* logits, int bf16, int64_t str
 }
 
 ep::RouteArgs route_args(const ep_routing& rt, const void* logits, int bf16, int64_t stride,
-                         const void* d_logits) {
+                         const void* d_logits, const void* counts) {
     ep::RouteArgs a;
     a.logits = logits;
     a.stride = stride;
@@ -149,7 +149,14 @@ ep::RouteArgs route_args(const ep_routing& rt, const void* logits, int bf16, int
     a.sigmoid = rt.score == 1;
     a.normalize = rt.normalize == 1;
     const int el = bf16 ? 2 : 4;
-    const int vpl = ep::token_shape(rt.num_experts).vpl;
+    const ep::TokenShape shape = ep::token_shape(rt.num_experts);
+    const int vpl = shape.vpl;
+    const int group = rt.num_experts / rt.num_groups;
+    const int lanes = group / vpl;
+    a.group_lanes = shape.lpt == 16 && group % vpl == 0 &&
+                            (lanes == 1 || lanes == 2 || lanes == 4 || lanes == 8)
+                        ? lanes
+                        : 0;
     const int piece = vpl * el < 16 ? vpl : 16 / el;  // elements per access
     const auto fits = [&](const void* p, int64_t pitch) {
         return rt.num_experts % piece == 0 && pitch % piece == 0 &&
@@ -157,6 +164,7 @@ ep::RouteArgs route_args(const ep_routing& rt, const void* logits, int bf16, int
     };
     a.pieces = fits(logits, stride);
     a.out_pieces = fits(d_logits, rt.num_experts);
+    a.count_pieces = rt.num_experts % 4 == 0 && aligned16(counts);
     return a;
 }
 
@@ -272,7 +280,7 @@ int ep_route(const ep_routing* rt, const void* logits, int logits_bf16, int64_t 
     if (!aligned4(expert_bias) || !aligned4(topk_idx) || !aligned4(topk_weights))
         return EP_ERR_ALIGN;
     const ep::RouteForward f = {expert_bias, valid, topk_idx, topk_weights};
-    return from_hip(ep::launch_route(route_args(*rt, logits, logits_bf16, logits_stride, nullptr),
+    return from_hip(ep::launch_route(route_args(*rt, logits, logits_bf16, logits_stride, nullptr, nullptr),
                                      f, static_cast<hipStream_t>(stream)));
 }
 
@@ -301,7 +309,7 @@ int ep_balance_loss(const ep_routing* rt, const void* logits, int logits_bf16,
         !aligned4(loss) || !aligned16(workspace))
         return EP_ERR_ALIGN;
     const ep::BalanceArgs b = {topk_idx, valid, coef, counts, mean_prob, num_valid, loss};
-    return from_hip(ep::launch_balance(route_args(*rt, logits, logits_bf16, logits_stride, nullptr),
+    return from_hip(ep::launch_balance(route_args(*rt, logits, logits_bf16, logits_stride, nullptr, nullptr),
                                        b, workspace, static_cast<hipStream_t>(stream)));
 }
 
@@ -327,7 +335,7 @@ int ep_route_backward(const ep_routing* rt, const void* logits, int logits_bf16,
     const ep::RouteBackward b = {topk_idx, d_weights, valid, coef, counts, num_valid, d_loss,
                                  d_logits};
     return from_hip(ep::launch_route_backward(
-        route_args(*rt, logits, logits_bf16, logits_stride, d_logits), b,
+        route_args(*rt, logits, logits_bf16, logits_stride, d_logits, counts), b,
         static_cast<hipStream_t>(stream)));
 }
 

@@ -6,12 +6,14 @@
 //   P[s, e]   mean of p[t, e] over the n_s tokens of the sequence
 //   loss = coef / B * sum_s sum_e E / (k n_s) c[s, e] P[s, e]
 //
-// First kernel: a workgroup per run of consecutive tokens of one sequence
-// adds its tokens' probabilities per expert in registers, its entries in an
-// LDS histogram, and writes both as one row of partial sums.  Second kernel: a
-// thread per (sequence, expert) adds the rows in order, in fp64.  Third: one
-// wave adds the per-workgroup parts of the loss.  No sum depends on the order
-// in which workgroups run.
+// First kernel: a workgroup per run of consecutive tokens of one sequence, one
+// pass of its 16 waves where the batch allows (64 tokens at up to 256 experts:
+// about a workgroup per CU), adds its tokens' probabilities per expert in
+// registers, its entries in an LDS histogram, and writes both as one row of
+// partial sums.  Second kernel: the rows are added in order, in fp64.  Up to
+// kOneGroup values one workgroup does it, and the loss with them; above that a
+// workgroup per sequence and 256 experts, and a third kernel adds their parts
+// of the loss.  No sum depends on the order in which workgroups run.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -23,26 +25,30 @@ namespace {
 
 using namespace route;
 
-constexpr int kFinish = 256;
+constexpr int kSum = 1024;     // threads of the first kernel
+constexpr int kFinish = 1024;  // and of the second: 256 experts x 4 slices of rows
+constexpr int kSlices = kFinish / 256;
+constexpr int kRowsWanted = 256;
+constexpr int64_t kOneGroup = 65536;
 
 struct Geometry {
     int runs;        // runs of tokens per sequence
     int run_tokens;  // tokens per run
-    int tiles;       // workgroups per sequence in the second kernel
+    int tiles;       // of 256 experts
     int64_t probs, hist, live, part, bytes;  // workspace offsets and size
 };
 
 Geometry geometry(int T, int E, int B) {
     Geometry g;
     const int64_t len = T / B;
-    // About two workgroups per CU over all sequences, of 32 tokens at least.
-    int64_t runs = (512 + B - 1) / B;
-    const int64_t most = (len + 31) / 32;
+    const int64_t pass = kSum / token_shape(E).lpt;  // tokens of a workgroup's pass
+    int64_t runs = (kRowsWanted + B - 1) / B;
+    const int64_t most = (len + pass - 1) / pass;
     if (runs > most) runs = most;
     if (runs < 1) runs = 1;
     g.run_tokens = static_cast<int>((len + runs - 1) / runs);
     g.runs = g.run_tokens ? static_cast<int>((len + g.run_tokens - 1) / g.run_tokens) : 1;
-    g.tiles = (E + kFinish - 1) / kFinish;
+    g.tiles = (E + 255) / 256;
     const auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
     const int64_t rows = static_cast<int64_t>(B) * g.runs;
     g.probs = 0;
@@ -54,24 +60,26 @@ Geometry geometry(int T, int E, int B) {
 }
 
 template <int LPT, int VPL, bool BF16>
-__global__ __launch_bounds__(kThreads) void balance_sum_kernel(RouteArgs a, const int32_t* topk_idx,
-                                                               const uint8_t* valid, int runs,
-                                                               int run_tokens, float* probs,
-                                                               int32_t* hist, int32_t* live_rows) {
-    constexpr int kTokens = kThreads / LPT;
+__global__ __launch_bounds__(kSum) void balance_sum_kernel(RouteArgs a, const int32_t* topk_idx,
+                                                           const uint8_t* valid, int runs,
+                                                           int run_tokens, float* probs,
+                                                           int32_t* hist, int32_t* live_rows) {
+    constexpr int kTokens = kSum / LPT;
     constexpr int kWidth = LPT * VPL;
-    __shared__ float sums[kTokens][kWidth];
+    constexpr int kWaves = kSum / kWave;
+    __shared__ float sums[kWaves][kWidth];
     __shared__ int32_t counts[kWidth];
     __shared__ int32_t live_count;
     const int lane = threadIdx.x % LPT;
     const int slot = threadIdx.x / LPT;
+    const int wave = threadIdx.x / kWave;
     const int E = a.num_experts, k = a.num_topk;
     const int64_t seq = blockIdx.x / runs;
     const int run = blockIdx.x % runs;
     const int begin = run * run_tokens;
     const int end = min(begin + run_tokens, a.seq_len);
     const int64_t t0 = seq * a.seq_len;
-    for (int e = threadIdx.x; e < kWidth; e += kThreads) counts[e] = 0;
+    for (int e = threadIdx.x; e < kWidth; e += kSum) counts[e] = 0;
     if (threadIdx.x == 0) live_count = 0;
     __syncthreads();
 
@@ -83,13 +91,9 @@ __global__ __launch_bounds__(kThreads) void balance_sum_kernel(RouteArgs a, cons
         const int at = base + slot;
         const int64_t t = t0 + at;
         const bool live = at < end && (valid == nullptr || valid[t] != 0);
-        float x[VPL], z[VPL], slope[VPL], total;
+        float x[VPL], z[VPL], slope[VPL], total, top;
         load_logits<VPL, BF16>(a.logits, (live ? t : t0) * a.stride, live ? E : 0, lane * VPL,
                                a.pieces, x);
-        scores<LPT, VPL>(x, a.sigmoid, z, slope, total);
-        const float r = total > 0.0f ? 1.0f / total : 0.0f;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) acc[i] += z[i] * r;
         if (live) {
             if (lane == 0) ++mine;
             for (int j = lane; j < k; j += LPT) {
@@ -97,52 +101,106 @@ __global__ __launch_bounds__(kThreads) void balance_sum_kernel(RouteArgs a, cons
                 if (id >= 0 && id < E) atomicAdd(&counts[id], 1);
             }
         }
-    }
+        scores<LPT, VPL>(x, a.sigmoid, z, slope, total, top);
+        const float r = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) sums[slot][lane * VPL + i] = acc[i];
+        for (int i = 0; i < VPL; ++i) acc[i] += z[i] * r;
+    }
+    // the wave's tokens (4 with 16 lanes each), then the waves in order
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        if constexpr (LPT == 16) {
+            uint2 p = swap16(__float_as_uint(acc[i]));
+            acc[i] = __uint_as_float(p.x) + __uint_as_float(p.y);
+            p = swap32(__float_as_uint(acc[i]));
+            acc[i] = __uint_as_float(p.x) + __uint_as_float(p.y);
+        }
+        if (LPT == 64 || threadIdx.x % kWave < 16) sums[wave][lane * VPL + i] = acc[i];
+    }
     if (mine) atomicAdd(&live_count, mine);
     __syncthreads();
     const int64_t out = static_cast<int64_t>(blockIdx.x) * E;
-    for (int e = threadIdx.x; e < E; e += kThreads) {
+    for (int e = threadIdx.x; e < E; e += kSum) {
         float s = 0.0f;
 #pragma unroll
-        for (int q = 0; q < kTokens; ++q) s += sums[q][e];
+        for (int q = 0; q < kWaves; ++q) s += sums[q][e];
         probs[out + e] = s;
         hist[out + e] = counts[e];
     }
     if (threadIdx.x == 0) live_rows[blockIdx.x] = live_count;
 }
 
-__global__ __launch_bounds__(kFinish) void balance_mean_kernel(
-    int E, int tiles, int runs, const float* probs, const int32_t* hist, const int32_t* live_rows,
-    int32_t* counts, float* mean_prob, int32_t* num_valid, double* part) {
-    __shared__ double red[kFinish];
-    const int64_t seq = blockIdx.x / tiles;
-    const int tile = blockIdx.x % tiles;
-    const int e = tile * kFinish + threadIdx.x;
-    int n = 0;
-    for (int r = 0; r < runs; ++r) n += live_rows[seq * runs + r];
-    double term = 0.0;
-    if (e < E) {
-        double s = 0.0;
-        int c = 0;
-        for (int r = 0; r < runs; ++r) {
-            s += static_cast<double>(probs[(seq * runs + r) * E + e]);
-            c += hist[(seq * runs + r) * E + e];
-        }
-        const double mean = n ? s / n : 0.0;
-        counts[seq * E + e] = c;
-        mean_prob[seq * E + e] = static_cast<float>(mean);
-        if (n) term = mean * c / n;
-    }
-    if (tile == 0 && threadIdx.x == 0) num_valid[seq] = n;
-    red[threadIdx.x] = term;
+// Sum over the workgroup of one double per thread, in every thread.
+__device__ __forceinline__ double group_sum(double v, double* lds) {
     __syncthreads();
+    lds[threadIdx.x] = v;
+    __syncthreads();
+#pragma unroll 1
     for (int w = kFinish / 2; w > 0; w /= 2) {
-        if (static_cast<int>(threadIdx.x) < w) red[threadIdx.x] += red[threadIdx.x + w];
+        if (static_cast<int>(threadIdx.x) < w) lds[threadIdx.x] += lds[threadIdx.x + w];
         __syncthreads();
     }
-    if (threadIdx.x == 0) part[blockIdx.x] = red[0];
+    return lds[0];
+}
+
+// One workgroup takes every (sequence, tile of 256 experts) item in order and
+// has the whole loss; more take one each and write its part.
+__global__ __launch_bounds__(kFinish) void balance_mean_kernel(
+    int E, int tiles, int runs, int64_t items, const float* probs, const int32_t* hist,
+    const int32_t* live_rows, int32_t* counts, float* mean_prob, int32_t* num_valid, double* part,
+    double factor, float* loss) {
+    __shared__ double sum_s[kSlices][256];
+    __shared__ int32_t sum_c[kSlices][256];
+    __shared__ double red[kFinish];
+    __shared__ int32_t live;
+    const int col = threadIdx.x % 256, slice = threadIdx.x / 256;
+    double term = 0.0;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int64_t seq = item / tiles;
+        const int tile = static_cast<int>(item % tiles);
+        const int e = tile * 256 + col;
+        if (threadIdx.x == 0) live = 0;
+        __syncthreads();
+        int n = 0;
+        for (int r = threadIdx.x; r < runs; r += kFinish) n += live_rows[seq * runs + r];
+        if (n) atomicAdd(&live, n);
+        double s = 0.0;
+        int c = 0;
+        if (e < E) {
+            const int64_t at = seq * runs * E + e;
+#pragma unroll 8
+            for (int r = slice; r < runs; r += kSlices) {
+                s += static_cast<double>(probs[at + static_cast<int64_t>(r) * E]);
+                c += hist[at + static_cast<int64_t>(r) * E];
+            }
+        }
+        sum_s[slice][col] = s;
+        sum_c[slice][col] = c;
+        __syncthreads();
+        n = live;
+        if (slice == 0 && e < E) {
+#pragma unroll
+            for (int q = 1; q < kSlices; ++q) {
+                s += sum_s[q][col];
+                c += sum_c[q][col];
+            }
+            const double mean = n ? s / n : 0.0;
+            counts[seq * E + e] = c;
+            mean_prob[seq * E + e] = static_cast<float>(mean);
+            if (n) term += mean * c / n;
+        }
+        if (tile == 0 && threadIdx.x == 0) num_valid[seq] = n;
+        if (gridDim.x > 1) {
+            const double p = group_sum(term, red);
+            if (threadIdx.x == 0) part[item] = p;
+            term = 0.0;
+        }
+        __syncthreads();
+    }
+    if (gridDim.x == 1) {
+        const double p = group_sum(term, red);
+        if (threadIdx.x == 0) loss[0] = static_cast<float>(p * factor);
+    }
 }
 
 __global__ __launch_bounds__(kFinish) void balance_loss_kernel(int64_t parts, const double* part,
@@ -150,13 +208,8 @@ __global__ __launch_bounds__(kFinish) void balance_loss_kernel(int64_t parts, co
     __shared__ double red[kFinish];
     double s = 0.0;
     for (int64_t i = threadIdx.x; i < parts; i += kFinish) s += part[i];
-    red[threadIdx.x] = s;
-    __syncthreads();
-    for (int w = kFinish / 2; w > 0; w /= 2) {
-        if (static_cast<int>(threadIdx.x) < w) red[threadIdx.x] += red[threadIdx.x + w];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) loss[0] = static_cast<float>(red[0] * factor);
+    s = group_sum(s, red);
+    if (threadIdx.x == 0) loss[0] = static_cast<float>(s * factor);
 }
 
 template <int LPT, int VPL>
@@ -167,11 +220,11 @@ void launch_sum(const RouteArgs& a, const BalanceArgs& b, const Geometry& g, cha
     int32_t* hist = reinterpret_cast<int32_t*>(ws + g.hist);
     int32_t* live = reinterpret_cast<int32_t*>(ws + g.live);
     if (a.bf16)
-        hipLaunchKernelGGL((balance_sum_kernel<LPT, VPL, true>), grid, dim3(kThreads), 0, stream, a,
+        hipLaunchKernelGGL((balance_sum_kernel<LPT, VPL, true>), grid, dim3(kSum), 0, stream, a,
                            b.topk_idx, b.valid, g.runs, g.run_tokens, probs, hist, live);
     else
-        hipLaunchKernelGGL((balance_sum_kernel<LPT, VPL, false>), grid, dim3(kThreads), 0, stream,
-                           a, b.topk_idx, b.valid, g.runs, g.run_tokens, probs, hist, live);
+        hipLaunchKernelGGL((balance_sum_kernel<LPT, VPL, false>), grid, dim3(kSum), 0, stream, a,
+                           b.topk_idx, b.valid, g.runs, g.run_tokens, probs, hist, live);
 }
 
 }  // namespace
@@ -199,14 +252,18 @@ hipError_t launch_balance(const RouteArgs& a, const BalanceArgs& b, void* worksp
         launch_sum<64, 16>(a, b, g, ws, stream);
     }
     double* part = reinterpret_cast<double*>(ws + g.part);
-    hipLaunchKernelGGL(balance_mean_kernel, dim3(static_cast<unsigned>(a.num_seqs) * g.tiles),
-                       dim3(kFinish), 0, stream, a.num_experts, g.tiles, g.runs, reinterpret_cast<float*>(ws + g.probs),
+    const int64_t items = static_cast<int64_t>(a.num_seqs) * g.tiles;
+    const bool one = static_cast<int64_t>(a.num_seqs) * g.runs * a.num_experts <= kOneGroup;
+    const double factor = static_cast<double>(b.coef) / a.num_seqs * a.num_experts / a.num_topk;
+    hipLaunchKernelGGL(balance_mean_kernel, dim3(one ? 1 : static_cast<unsigned>(items)),
+                       dim3(kFinish), 0, stream, a.num_experts, g.tiles, g.runs, items,
+                       reinterpret_cast<float*>(ws + g.probs),
                        reinterpret_cast<int32_t*>(ws + g.hist),
                        reinterpret_cast<int32_t*>(ws + g.live), b.counts, b.mean_prob, b.num_valid,
-                       part);
-    const double factor = static_cast<double>(b.coef) / a.num_seqs * a.num_experts / a.num_topk;
-    hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(kFinish), 0, stream,
-                       static_cast<int64_t>(a.num_seqs) * g.tiles, part, factor, b.loss);
+                       part, factor, b.loss);
+    if (!one && items > 1)
+        hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(kFinish), 0, stream, items, part,
+                           factor, b.loss);
     return hipGetLastError();
 }
 

@@ -745,12 +745,13 @@ hipError_t launch_expert_w4(const ep_problem& p, const ep_expert_w4_t& mm, const
     const auto tiles = [&](int mc) { return experts + filled / mc; };
     // By the mean rows of an expert, measured at 64 experts, K 4096, N 1408:
     // bf16 rows 8: 44 us with the few-row kernel, 47 with 32-row tiles; 12: 51,
-    // 48; 24: 90, 51 and 63 with 64-row tiles; 128: 146 and 126.  FP8 rows, whose
-    // 64-row tile does not fit the registers: 12: 42, 51; 48 (skewed): 234, 155.
+    // 48; 24: 90, 51 and 63 with 64-row tiles; 48 (skewed): 140 and 134; 128: 146
+    // and 126.  FP8 rows, whose 64-row tile does not fit the registers: 12: 42,
+    // 51; 48 (skewed): 234, 155.
     // Few-row kernel: two waves where four would have less than four steps each
     // (K 2048, 256 experts: 343 us against 403; K 7168: 589 against 587).
     const bool fp8 = mm.in_format != 0;
-    if (!fp8 && mean > 48)
+    if (!fp8 && mean > 40)
         launch_rows<0, 4>(a, mm.in_format, gated, tiles(64), stream);
     else if (mean > (fp8 ? 16 : 8))
         launch_rows<0, 2>(a, mm.in_format, gated, tiles(32), stream);

@@ -83,14 +83,17 @@ hipError_t launch_combine(const ep_problem& p, const void* expert_out, const int
 
 // Routing (gate logits): the problem as the kernels take it.  `pieces` /
 // `out_pieces`: rows of the logits / of the dense gradient can be accessed in
-// aligned pieces of min(experts per lane, 16 bytes' worth) elements.
+// aligned pieces of min(experts per lane, 16 bytes' worth) elements;
+// `count_pieces`: rows of counts in aligned groups of four.  `group_lanes`:
+// lanes of a token that a group of experts fills exactly, 0 if it does not.
 struct RouteArgs {
     const void* logits;
     int64_t stride;  // elements between rows of the logits
     int32_t num_tokens, num_experts, num_topk, num_groups, topk_groups;
     int32_t num_seqs, seq_len;
     float scale;
-    bool bf16, sigmoid, normalize, pieces, out_pieces;
+    int32_t group_lanes;
+    bool bf16, sigmoid, normalize, pieces, out_pieces, count_pieces;
 };
 // Lanes per token and experts per lane of the routing kernels.
 struct TokenShape {

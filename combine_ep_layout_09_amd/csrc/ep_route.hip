@@ -13,19 +13,86 @@ using namespace route;
 
 // ---------------------------------------------------------------- the choice
 
+// The score of a group: the sum of its two largest keys' values, an expert that
+// is off (key 0) counting as -FLT_MAX.  fp64 holds the sum of two fp32 values
+// closely enough that only equal sums of equal terms tie.
+__device__ __forceinline__ double group_score(uint32_t m1, uint32_t m2, bool single) {
+    const double low = -3.4028234663852886e38;
+    double s = m1 ? static_cast<double>(order_value(m1)) : low;
+    if (!single) s += m2 ? static_cast<double>(order_value(m2)) : low;
+    return s;
+}
+
+template <int S>
+__device__ __forceinline__ void merge_half(uint32_t& m1, uint32_t& m2) {
+    const uint32_t o1 = other_half<S>(m1), o2 = other_half<S>(m2);
+    m2 = max(min(m1, o1), max(m2, o2));
+    m1 = max(m1, o1);
+}
+
+// How many lanes of the row of 16 hold a better group than this one, when a
+// group is 2^S lanes (so 2^S times the number of better groups).
+template <int S, int N>
+__device__ __forceinline__ int better_lanes(double s, int lane) {
+    if constexpr (N >= 16) {
+        return 0;
+    } else {
+        const uint64_t u = __builtin_bit_cast(uint64_t, s);
+        const uint64_t lo = row_ror<N>(static_cast<uint32_t>(u));
+        const uint64_t hi = row_ror<N>(static_cast<uint32_t>(u >> 32));
+        const double o = __builtin_bit_cast(double, hi << 32 | lo);
+        const int from = (lane - N) & 15;  // row_ror moves lane i - N to lane i
+        const bool better = o > s || (o == s && from < lane);
+        return (better ? 1 : 0) + better_lanes<S, N + (1 << S)>(s, lane);
+    }
+}
+
+// Groups of 2^S lanes of a 16-lane token: two-largest by pairwise exchanges,
+// then each lane meets one lane of every other group.
+template <int S, int VPL>
+__device__ __forceinline__ bool lane_group_kept(const uint32_t (&key)[VPL], int lane,
+                                                const RouteArgs& a) {
+    uint32_t m1 = 0, m2 = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        m2 = max(m2, min(m1, key[i]));
+        m1 = max(m1, key[i]);
+    }
+    if constexpr (S >= 1) merge_half<1>(m1, m2);
+    if constexpr (S >= 2) merge_half<2>(m1, m2);
+    if constexpr (S >= 3) merge_half<3>(m1, m2);
+    // lanes past the last group are below every score
+    const double s = lane * VPL < a.num_experts ? group_score(m1, m2, VPL << S == 1) : -1.0e300;
+    return better_lanes<S, 1 << S>(s, lane) < a.topk_groups;
+}
+
 // Keys of experts outside the token's best topk_groups groups become 0 (off).
-// The token's keys pass through LDS; lane g scores groups g, g + LPT, ...: the
-// sum (fp64, so exact order of the fp32 keys' sums) of the group's two largest
-// keys, an expert that is off counting as -FLT_MAX.  A group is kept if fewer
-// than topk_groups groups are better; equal scores go to the lower index.
+// A group is kept if fewer than topk_groups groups are better; equal scores go
+// to the lower index.  Groups that are 1, 2, 4 or 8 whole lanes of a 16-lane
+// token are handled in registers; for others the keys pass through LDS, where
+// lane g scores groups g, g + LPT, ....
 template <int LPT, int VPL>
 __device__ __forceinline__ void limit_groups(uint32_t (&key)[VPL], uint32_t* keys, double* score,
                                              int lane, const RouteArgs& a) {
     const int gs = a.num_experts / a.num_groups;
+    if (LPT == 16 && a.group_lanes > 0) {
+        bool kept;
+        if (a.group_lanes == 1)
+            kept = lane_group_kept<0, VPL>(key, lane, a);
+        else if (a.group_lanes == 2)
+            kept = lane_group_kept<1, VPL>(key, lane, a);
+        else if (a.group_lanes == 4)
+            kept = lane_group_kept<2, VPL>(key, lane, a);
+        else
+            kept = lane_group_kept<3, VPL>(key, lane, a);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) key[i] = kept ? key[i] : 0u;
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
         if (lane * VPL + i < a.num_experts) keys[lane * VPL + i] = key[i];
-    __syncthreads();
+    wave_sync();
     for (int g = lane; g < a.num_groups; g += LPT) {
         uint32_t m1 = 0, m2 = 0;
         for (int i = 0; i < gs; ++i) {
@@ -33,12 +100,9 @@ __device__ __forceinline__ void limit_groups(uint32_t (&key)[VPL], uint32_t* key
             m2 = max(m2, min(m1, k));
             m1 = max(m1, k);
         }
-        const double low = -3.4028234663852886e38;
-        double s = m1 ? static_cast<double>(order_value(m1)) : low;
-        if (gs > 1) s += m2 ? static_cast<double>(order_value(m2)) : low;
-        score[g] = s;
+        score[g] = group_score(m1, m2, gs == 1);
     }
-    __syncthreads();
+    wave_sync();
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int e = lane * VPL + i;
@@ -58,7 +122,7 @@ __device__ __forceinline__ void limit_groups(uint32_t (&key)[VPL], uint32_t* key
 // One launch, a token per LPT lanes.  The k best keys are taken one after the
 // other: every lane keeps the best of its own keys, a reduction over the
 // token's lanes finds the best of all, and the lowest lane that holds it gives
-// it up.  Entry j ends in lane j % LPT; the weights are then computed with one
+// it up.  Entry j goes to lane j % LPT through LDS; the weights are then computed with one
 // lane per entry from the logits themselves (the bias only steers the choice).
 template <int LPT, int VPL, bool BF16>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const float* bias,
@@ -68,6 +132,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
     constexpr int kSel = kMaxTopk > LPT ? kMaxTopk / LPT : 1;
     __shared__ uint32_t lds_keys[kTokens][LPT * VPL];
     __shared__ double lds_score[kTokens][kMaxGroups];
+    __shared__ int lds_chosen[kTokens][kMaxTopk];
     const int lane = threadIdx.x % LPT;
     const int slot = threadIdx.x / LPT;
     const int wave_lane = threadIdx.x % kWave;
@@ -82,12 +147,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
     float m = 0.0f, total = 1.0f;
     if (!a.sigmoid && !a.normalize) {
         float z[VPL], slope[VPL];
-        scores<LPT, VPL>(x, false, z, slope, total);
-        m = -3.402823466e38f;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (finite(x[i])) m = fmaxf(m, x[i]);
-        m = token_fmax<LPT>(m);
+        scores<LPT, VPL>(x, false, z, slope, total, m);
     }
     uint32_t key[VPL];
 #pragma unroll
@@ -98,9 +158,6 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
     }
     if (a.num_groups > 1) limit_groups<LPT, VPL>(key, lds_keys[slot], lds_score[slot], lane, a);
 
-    int sel[kSel];
-#pragma unroll
-    for (int q = 0; q < kSel; ++q) sel[q] = -1;
     uint32_t best = 0;
     int at = 0;
 #pragma unroll
@@ -108,12 +165,8 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
         if (key[i] > best) best = key[i], at = i;
     for (int j = 0; j < a.num_topk; ++j) {
         const uint32_t top = token_max<LPT>(best);
-        const int winner = token_first<LPT>(best == top, wave_lane);
-        const int e = top ? winner * VPL + static_cast<int>(token_bcast<LPT>(at, winner)) : -1;
-#pragma unroll
-        for (int q = 0; q < kSel; ++q)
-            if (j == q * LPT + lane) sel[q] = e;
-        if (lane == winner) {
+        if (lane == token_first<LPT>(best == top, wave_lane)) {
+            lds_chosen[slot][j] = top ? lane * VPL + at : -1;
             const int gone = at;
             best = 0;
             at = 0;
@@ -124,6 +177,11 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
             }
         }
     }
+    wave_sync();
+    int sel[kSel];
+#pragma unroll
+    for (int q = 0; q < kSel; ++q)
+        sel[q] = q * LPT + lane < a.num_topk ? lds_chosen[slot][q * LPT + lane] : -1;
 
     float xe[kSel], w[kSel];
 #pragma unroll
@@ -143,6 +201,29 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
 
 // -------------------------------------------------------------- the gradient
 
+// Entry j of the token (lane j % LPT, register j / LPT) to every lane: those of
+// the same expert add it to their sum, in the order of j, and stay responsible
+// for the expert only if no earlier entry names it.
+template <int LPT, int SEL, int J>
+__device__ __forceinline__ void join_entries(const int (&e)[SEL], const float (&part)[SEL], int k,
+                                             int lane, float (&sum)[SEL], bool (&mine)[SEL]) {
+    if constexpr (J < kMaxTopk) {
+        if (J >= k) return;
+        const int ej = static_cast<int>(
+            token_bcast<LPT, J % LPT>(static_cast<uint32_t>(e[J / LPT])));
+        const float pj =
+            __uint_as_float(token_bcast<LPT, J % LPT>(__float_as_uint(part[J / LPT])));
+#pragma unroll
+        for (int q = 0; q < SEL; ++q) {
+            if (ej == e[q]) {
+                sum[q] += pj;
+                if (J < q * LPT + lane) mine[q] = false;
+            }
+        }
+        join_entries<LPT, SEL, J + 1>(e, part, k, lane, sum, mine);
+    }
+}
+
 // d_logits of a token = the balance loss's part, dense, plus the weights'
 // part, which is dense only for weights that were not normalised over the
 // chosen experts of a softmax.
@@ -158,7 +239,9 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     const int32_t* counts, const int32_t* num_valid, const float* d_loss, void* d_logits) {
     constexpr int kTokens = kThreads / LPT;
     constexpr int kSel = kMaxTopk > LPT ? kMaxTopk / LPT : 1;
-    __shared__ float add[kTokens][LPT * VPL];
+    // lane runs of VPL, padded so that 16-byte reads of 8 lanes meet 32 banks
+    constexpr int kRun = VPL >= 8 ? VPL + 4 : VPL;
+    __shared__ __attribute__((aligned(16))) float add[kTokens][LPT * kRun];
     const int lane = threadIdx.x % LPT;
     const int slot = threadIdx.x / LPT;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + slot;
@@ -171,24 +254,16 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     float x[VPL], dx[VPL];
     load_logits<VPL, BF16>(a.logits, row, live ? E : 0, first, a.pieces, x);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        dx[i] = 0.0f;
-        add[slot][first + i] = 0.0f;
-    }
+    for (int i = 0; i < VPL; ++i) dx[i] = 0.0f;
     const bool loss = d_loss != nullptr;
     const bool spread = d_weights != nullptr && !a.sigmoid && !a.normalize;
     float m = 0.0f, total = 1.0f;
     float p[VPL], slope[VPL];
     if (loss || spread) {
-        scores<LPT, VPL>(x, a.sigmoid, p, slope, total);
+        scores<LPT, VPL>(x, a.sigmoid, p, slope, total, m);
         const float r = total > 0.0f ? 1.0f / total : 0.0f;
-        m = -3.402823466e38f;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            if (finite(x[i])) m = fmaxf(m, x[i]);
-            p[i] *= r;
-        }
-        m = token_fmax<LPT>(m);
+        for (int i = 0; i < VPL; ++i) p[i] *= r;
     }
     if (loss) {
         const int64_t seq = (inside ? t : 0) / a.seq_len;
@@ -197,10 +272,22 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
         const float f = coef * static_cast<float>(E) /
                         (static_cast<float>(a.num_seqs) * static_cast<float>(k)) * d_loss[0] / n / n;
         const int32_t c0 = c[0];
+        int32_t ci[VPL];
+        if (VPL >= 4 && a.count_pieces) {
+#pragma unroll
+            for (int i = 0; i + 3 < VPL; i += 4) {
+                const int4 v = first + i < E ? *reinterpret_cast<const int4*>(c + first + i)
+                                             : make_int4(c0, c0, c0, c0);
+                ci[i] = v.x, ci[i + 1] = v.y, ci[i + 2] = v.z, ci[i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) ci[i] = first + i < E ? c[first + i] : c0;
+        }
         float d[VPL], dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            d[i] = first + i < E ? static_cast<float>(c[first + i] - c0) : 0.0f;
+            d[i] = static_cast<float>(ci[i] - c0);
             dot += d[i] * p[i];
         }
         dot = token_sum<LPT>(dot);
@@ -237,33 +324,21 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
 #pragma unroll
             for (int i = 0; i < VPL; ++i) dx[i] -= p[i] * gw;
         }
-        __syncthreads();
         float sum[kSel] = {};
         bool mine[kSel];
 #pragma unroll
         for (int q = 0; q < kSel; ++q) mine[q] = e[q] >= 0;
-        for (int j = 0; j < k; ++j) {
+        join_entries<LPT, kSel, 0>(e, part, k, lane, sum, mine);
+        float* to = add[slot];
 #pragma unroll
-            for (int s = 0; s < kSel; ++s) {
-                if (j / LPT != s) continue;
-                const int ej = static_cast<int>(token_bcast<LPT>(e[s], j % LPT));
-                const float pj =
-                    __uint_as_float(token_bcast<LPT>(__float_as_uint(part[s]), j % LPT));
-#pragma unroll
-                for (int q = 0; q < kSel; ++q) {
-                    if (ej == e[q]) {
-                        sum[q] += pj;
-                        if (j < q * LPT + lane) mine[q] = false;
-                    }
-                }
-            }
-        }
+        for (int i = 0; i < VPL; ++i) to[lane * kRun + i] = 0.0f;
+        wave_sync();
 #pragma unroll
         for (int q = 0; q < kSel; ++q)
-            if (mine[q]) add[slot][e[q]] = sum[q];
-        __syncthreads();
+            if (mine[q]) to[e[q] / VPL * kRun + e[q] % VPL] = sum[q];
+        wave_sync();
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) dx[i] += add[slot][first + i];
+        for (int i = 0; i < VPL; ++i) dx[i] += to[lane * kRun + i];
     }
     if (inside) {
 #pragma unroll

@@ -24,6 +24,32 @@ __device__ __forceinline__ uint32_t row_ror(uint32_t v) {
         __builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x120 + N, 0xf, 0xf, false));
 }
 
+// Value of lane N of each row of 16 lanes, in every lane of it.
+template <int N>
+__device__ __forceinline__ uint32_t row_bcast(uint32_t v) {
+    return static_cast<uint32_t>(
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x150 + N, 0xf, 0xf, false));
+}
+
+// All lanes of an aligned run of 2^S: after S - 1, run it with S.  Lane i meets
+// a lane of the other half of its run.
+template <int S>
+__device__ __forceinline__ uint32_t other_half(uint32_t v) {
+    constexpr int ctrl = S == 1 ? 0xb1      // quad_perm 1, 0, 3, 2
+                         : S == 2 ? 0x4e    // quad_perm 2, 3, 0, 1
+                         : S == 3 ? 0x141   // mirrored in 8 lanes
+                                  : 0x140;  // mirrored in 16 lanes
+    return static_cast<uint32_t>(
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(v), ctrl, 0xf, 0xf, false));
+}
+
+// LDS that one wave writes and reads needs no barrier, but the compiler has to
+// keep the order.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // The two halves of a pairwise exchange: {rows 0, 0, 2, 2} and {1, 1, 3, 3}
 // for 16, {lanes 0-31 twice} and {lanes 32-63 twice} for 32.
 __device__ __forceinline__ uint2 swap16(uint32_t v) {
@@ -81,10 +107,13 @@ __device__ __forceinline__ float token_fmax(float f) {
     return f;
 }
 
-// Value held by lane `src` (0 .. LPT-1) of this lane's token.
-template <int LPT>
-__device__ __forceinline__ uint32_t token_bcast(uint32_t v, int src) {
-    return static_cast<uint32_t>(__shfl(static_cast<int>(v), src, LPT));
+// Value held by lane J (0 .. LPT-1) of this lane's token.
+template <int LPT, int J>
+__device__ __forceinline__ uint32_t token_bcast(uint32_t v) {
+    if constexpr (LPT == 64)
+        return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), J));
+    else
+        return row_bcast<J>(v);
 }
 
 // Lowest lane of this lane's token for which `p` holds (p holds for one at
@@ -195,11 +224,12 @@ __device__ __forceinline__ void load_logits(const void* base, int64_t row_start,
 // are its probabilities; 0 for experts that are off.  Softmax: exp(x - max).
 // Sigmoid: sigma(x); where even the largest logit is below -20, sigma(x) is
 // exp(x) to 2e-9, and exp(x - max) keeps a row of tiny scores from vanishing.
-// slope[i] is d log z / dx of the score: 1, or sigma(-x).
+// slope[i] is d log z / dx of the score: 1, or sigma(-x).  m is the largest
+// logit.
 template <int LPT, int VPL>
 __device__ __forceinline__ void scores(const float (&x)[VPL], bool sigmoid, float (&z)[VPL],
-                                       float (&slope)[VPL], float& total) {
-    float m = -3.402823466e38f;
+                                       float (&slope)[VPL], float& total, float& m) {
+    m = -3.402823466e38f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
         if (finite(x[i])) m = fmaxf(m, x[i]);
