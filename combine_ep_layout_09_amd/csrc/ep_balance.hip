@@ -11,9 +11,9 @@
 // about a workgroup per CU), adds its tokens' probabilities per expert in
 // registers, its entries in an LDS histogram, and writes both as one row of
 // partial sums.  Second kernel: the rows are added in order, in fp64.  Up to
-// kOneGroup values one workgroup does it, and the loss with them; above that a
-// workgroup per sequence and 256 experts, and a third kernel adds their parts
-// of the loss.  No sum depends on the order in which workgroups run.
+// kOneGroup partial sums one workgroup does it, and the loss with them; above
+// that many workgroups, and a third kernel adds their parts of the loss.  No
+// sum depends on the order in which workgroups run.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -26,15 +26,14 @@ namespace {
 using namespace route;
 
 constexpr int kSum = 1024;     // threads of the first kernel
-constexpr int kFinish = 1024;  // and of the second: 256 experts x 4 slices of rows
-constexpr int kSlices = kFinish / 256;
+constexpr int kFinish = 1024;  // and of the others
+constexpr int64_t kMostGroups = 1024;  // of the second
 constexpr int kRowsWanted = 256;
-constexpr int64_t kOneGroup = 65536;
+constexpr int64_t kOneGroup = 16384;
 
 struct Geometry {
     int runs;        // runs of tokens per sequence
     int run_tokens;  // tokens per run
-    int tiles;       // of 256 experts
     int64_t probs, hist, live, part, bytes;  // workspace offsets and size
 };
 
@@ -48,14 +47,13 @@ Geometry geometry(int T, int E, int B) {
     if (runs < 1) runs = 1;
     g.run_tokens = static_cast<int>((len + runs - 1) / runs);
     g.runs = g.run_tokens ? static_cast<int>((len + g.run_tokens - 1) / g.run_tokens) : 1;
-    g.tiles = (E + 255) / 256;
     const auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
     const int64_t rows = static_cast<int64_t>(B) * g.runs;
     g.probs = 0;
     g.hist = up(g.probs + rows * E * 4);
     g.live = up(g.hist + rows * E * 4);
     g.part = up(g.live + rows * 4);
-    g.bytes = up(g.part + static_cast<int64_t>(B) * g.tiles * 8);
+    g.bytes = up(g.part + kMostGroups * 8);
     return g;
 }
 
@@ -130,82 +128,79 @@ __global__ __launch_bounds__(kSum) void balance_sum_kernel(RouteArgs a, const in
     if (threadIdx.x == 0) live_rows[blockIdx.x] = live_count;
 }
 
-// Sum over the workgroup of one double per thread, in every thread.
+// Sum over the workgroup of one double per thread, in thread 0.
 __device__ __forceinline__ double group_sum(double v, double* lds) {
+#pragma unroll
+    for (int d = kWave / 2; d > 0; d /= 2) v += __shfl_down(v, d, kWave);
+    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = v;
     __syncthreads();
-    lds[threadIdx.x] = v;
-    __syncthreads();
-#pragma unroll 1
-    for (int w = kFinish / 2; w > 0; w /= 2) {
-        if (static_cast<int>(threadIdx.x) < w) lds[threadIdx.x] += lds[threadIdx.x + w];
-        __syncthreads();
-    }
-    return lds[0];
+    v = threadIdx.x < kFinish / kWave ? lds[threadIdx.x] : 0.0;
+#pragma unroll
+    for (int d = kFinish / kWave / 2; d > 0; d /= 2) v += __shfl_down(v, d, kWave);
+    return v;
 }
 
-// One workgroup takes every (sequence, tile of 256 experts) item in order and
-// has the whole loss; more take one each and write its part.
+// Outputs are the (sequence, expert) pairs in order.  A workgroup takes `cols`
+// of them at a time (a power of two, 64 to kFinish), kFinish / cols threads
+// each adding every kFinish / cols-th row of partial sums.  One workgroup
+// alone has the whole loss; several write their parts.
 __global__ __launch_bounds__(kFinish) void balance_mean_kernel(
-    int E, int tiles, int runs, int64_t items, const float* probs, const int32_t* hist,
+    int E, int cols, int runs, int64_t outputs, const float* probs, const int32_t* hist,
     const int32_t* live_rows, int32_t* counts, float* mean_prob, int32_t* num_valid, double* part,
     double factor, float* loss) {
-    __shared__ double sum_s[kSlices][256];
-    __shared__ int32_t sum_c[kSlices][256];
-    __shared__ double red[kFinish];
-    __shared__ int32_t live;
-    const int col = threadIdx.x % 256, slice = threadIdx.x / 256;
+    __shared__ double sum_s[kFinish];
+    __shared__ int32_t sum_c[kFinish], sum_n[kFinish];
+    const int col = threadIdx.x % cols, slice = threadIdx.x / cols, slices = kFinish / cols;
     double term = 0.0;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int64_t seq = item / tiles;
-        const int tile = static_cast<int>(item % tiles);
-        const int e = tile * 256 + col;
-        if (threadIdx.x == 0) live = 0;
-        __syncthreads();
-        int n = 0;
-        for (int r = threadIdx.x; r < runs; r += kFinish) n += live_rows[seq * runs + r];
-        if (n) atomicAdd(&live, n);
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * cols; base < outputs;
+         base += static_cast<int64_t>(gridDim.x) * cols) {
+        const int64_t o = base + col;
+        const int64_t seq = o / E;
+        const int e = static_cast<int>(o % E);
         double s = 0.0;
-        int c = 0;
-        if (e < E) {
-            const int64_t at = seq * runs * E + e;
-#pragma unroll 8
-            for (int r = slice; r < runs; r += kSlices) {
-                s += static_cast<double>(probs[at + static_cast<int64_t>(r) * E]);
-                c += hist[at + static_cast<int64_t>(r) * E];
+        int c = 0, n = 0;
+        if (o < outputs) {
+            const int64_t row = seq * runs;
+#pragma unroll 16
+            for (int r = slice; r < runs; r += slices) {
+                s += static_cast<double>(probs[(row + r) * E + e]);
+                c += hist[(row + r) * E + e];
+                n += live_rows[row + r];
             }
         }
-        sum_s[slice][col] = s;
-        sum_c[slice][col] = c;
-        __syncthreads();
-        n = live;
-        if (slice == 0 && e < E) {
-#pragma unroll
-            for (int q = 1; q < kSlices; ++q) {
-                s += sum_s[q][col];
-                c += sum_c[q][col];
+        if (slices > 1) {
+            __syncthreads();
+            sum_s[threadIdx.x] = s;
+            sum_c[threadIdx.x] = c;
+            sum_n[threadIdx.x] = n;
+            __syncthreads();
+        }
+        if (slice == 0 && o < outputs) {
+            for (int q = 1; q < slices; ++q) {
+                s += sum_s[q * cols + col];
+                c += sum_c[q * cols + col];
+                n += sum_n[q * cols + col];
             }
             const double mean = n ? s / n : 0.0;
-            counts[seq * E + e] = c;
-            mean_prob[seq * E + e] = static_cast<float>(mean);
+            counts[o] = c;
+            mean_prob[o] = static_cast<float>(mean);
             if (n) term += mean * c / n;
+            if (e == 0) num_valid[seq] = n;
         }
-        if (tile == 0 && threadIdx.x == 0) num_valid[seq] = n;
-        if (gridDim.x > 1) {
-            const double p = group_sum(term, red);
-            if (threadIdx.x == 0) part[item] = p;
-            term = 0.0;
-        }
-        __syncthreads();
     }
-    if (gridDim.x == 1) {
-        const double p = group_sum(term, red);
-        if (threadIdx.x == 0) loss[0] = static_cast<float>(p * factor);
+    __syncthreads();
+    const double p = group_sum(term, sum_s);
+    if (threadIdx.x == 0) {
+        if (gridDim.x == 1)
+            loss[0] = static_cast<float>(p * factor);
+        else
+            part[blockIdx.x] = p;
     }
 }
 
 __global__ __launch_bounds__(kFinish) void balance_loss_kernel(int64_t parts, const double* part,
                                                                double factor, float* loss) {
-    __shared__ double red[kFinish];
+    __shared__ double red[kFinish / kWave];
     double s = 0.0;
     for (int64_t i = threadIdx.x; i < parts; i += kFinish) s += part[i];
     s = group_sum(s, red);
@@ -252,17 +247,23 @@ hipError_t launch_balance(const RouteArgs& a, const BalanceArgs& b, void* worksp
         launch_sum<64, 16>(a, b, g, ws, stream);
     }
     double* part = reinterpret_cast<double*>(ws + g.part);
-    const int64_t items = static_cast<int64_t>(a.num_seqs) * g.tiles;
-    const bool one = static_cast<int64_t>(a.num_seqs) * g.runs * a.num_experts <= kOneGroup;
+    const int64_t outputs = static_cast<int64_t>(a.num_seqs) * a.num_experts;
+    // One workgroup and no third kernel up to kOneGroup partial sums; above
+    // that 64 outputs and 16 slices of rows per workgroup.
+    const bool one = outputs * g.runs <= kOneGroup;
+    int cols = 64;
+    while (one && cols < kFinish && cols < outputs) cols *= 2;
+    int64_t groups = one ? 1 : (outputs + cols - 1) / cols;
+    groups = groups < kMostGroups ? groups : kMostGroups;
     const double factor = static_cast<double>(b.coef) / a.num_seqs * a.num_experts / a.num_topk;
-    hipLaunchKernelGGL(balance_mean_kernel, dim3(one ? 1 : static_cast<unsigned>(items)),
-                       dim3(kFinish), 0, stream, a.num_experts, g.tiles, g.runs, items,
+    hipLaunchKernelGGL(balance_mean_kernel, dim3(static_cast<unsigned>(groups)), dim3(kFinish), 0,
+                       stream, a.num_experts, cols, g.runs, outputs,
                        reinterpret_cast<float*>(ws + g.probs),
                        reinterpret_cast<int32_t*>(ws + g.hist),
                        reinterpret_cast<int32_t*>(ws + g.live), b.counts, b.mean_prob, b.num_valid,
                        part, factor, b.loss);
-    if (!one && items > 1)
-        hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(kFinish), 0, stream, items, part,
+    if (groups > 1)
+        hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(kFinish), 0, stream, groups, part,
                            factor, b.loss);
     return hipGetLastError();
 }

@@ -122,7 +122,7 @@ __device__ __forceinline__ void limit_groups(uint32_t (&key)[VPL], uint32_t* key
 // One launch, a token per LPT lanes.  The k best keys are taken one after the
 // other: every lane keeps the best of its own keys, a reduction over the
 // token's lanes finds the best of all, and the lowest lane that holds it gives
-// it up.  Entry j goes to lane j % LPT through LDS; the weights are then computed with one
+// up its first expert with that key.  Entry j goes to lane j % LPT through LDS; the weights are then computed with one
 // lane per entry from the logits themselves (the bias only steers the choice).
 template <int LPT, int VPL, bool BF16>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const float* bias,
@@ -158,23 +158,27 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
     }
     if (a.num_groups > 1) limit_groups<LPT, VPL>(key, lds_keys[slot], lds_score[slot], lane, a);
 
-    uint32_t best = 0;
-    int at = 0;
+    const auto largest = [&]() {
+        uint32_t v = 0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-        if (key[i] > best) best = key[i], at = i;
+        for (int i = 0; i < VPL; ++i) v = max(v, key[i]);
+        return v;
+    };
+    uint32_t best = largest();
     for (int j = 0; j < a.num_topk; ++j) {
         const uint32_t top = token_max<LPT>(best);
         if (lane == token_first<LPT>(best == top, wave_lane)) {
-            lds_chosen[slot][j] = top ? lane * VPL + at : -1;
-            const int gone = at;
-            best = 0;
-            at = 0;
+            int at = -1;
+            bool found = false;
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
-                if (i == gone) key[i] = 0;
-                if (key[i] > best) best = key[i], at = i;
+                const bool hit = key[i] == top && !found;
+                found |= hit;
+                key[i] = hit ? 0u : key[i];
+                at = hit ? i : at;
             }
+            lds_chosen[slot][j] = top ? lane * VPL + at : -1;
+            best = largest();
         }
     }
     wave_sync();
@@ -317,8 +321,11 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
         gw = token_sum<LPT>(gw);
 #pragma unroll
         for (int q = 0; q < kSel; ++q) {
-            const float neg = a.sigmoid && e[q] >= 0 ? sigmoids(xe[q]).neg : 1.0f;
-            part[q] = e[q] < 0 ? 0.0f : w[q] * (a.normalize ? g[q] - gw : g[q]) * neg;
+            part[q] = 0.0f;
+            if (q * LPT < k && e[q] >= 0) {
+                const float neg = a.sigmoid ? sigmoids(xe[q]).neg : 1.0f;
+                part[q] = w[q] * (a.normalize ? g[q] - gw : g[q]) * neg;
+            }
         }
         if (spread) {
 #pragma unroll

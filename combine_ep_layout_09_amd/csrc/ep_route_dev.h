@@ -139,21 +139,32 @@ __device__ __forceinline__ float order_value(uint32_t k) {
     return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
 }
 
+// exp(x) for x <= 0: 2^t with t = x log2(e) rounded, times 1 + the rounding's
+// part.  v_exp_f32 is good to one unit in the last place, so the result is to
+// about two, in half the instructions of a library exponential.  Below -150
+// the result is 0 either way; the bound keeps the rounding's part finite.
+__device__ __forceinline__ float exp_neg(float x) {
+    constexpr float kLog2e = 1.44269504088896340736f;
+    constexpr float kLog2eRest = static_cast<float>(1.44269504088896340736 - kLog2e);
+    constexpr float kLn2 = 0.693147180559945309417f;
+    x = fmaxf(x, -150.0f);
+    const float t = x * kLog2e;
+    const float rest = fmaf(x, kLog2eRest, fmaf(x, kLog2e, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, rest * kLn2, e);
+}
+
 // sigma(x) and sigma(-x), both to full relative precision: with
 // t = exp(-|x|), the larger of the two is 1 / (1 + t), the smaller t times it.
 struct Sigmoids {
     float pos, neg;
 };
 __device__ __forceinline__ Sigmoids sigmoids(float x) {
-    const float t = expf(-fabsf(x));
-    const float r = 1.0f / (1.0f + t);
+    const float t = exp_neg(-fabsf(x));
+    const float r = __builtin_amdgcn_rcpf(1.0f + t);  // one unit in the last place
     const float s = t * r;
     return x >= 0.0f ? Sigmoids{r, s} : Sigmoids{s, r};
 }
-__device__ __forceinline__ float log_sigmoid(float x) {
-    return fminf(x, 0.0f) - log1pf(expf(-fabsf(x)));
-}
-
 // Row of `n` logits: VPL of them from index lane * VPL on, NaN (an expert
 // that is off) past the end.  `piece` is the host's word that rows may be
 // read in aligned pieces of min(VPL, 16 bytes' worth) elements that do not
@@ -220,10 +231,13 @@ __device__ __forceinline__ void load_logits(const void* base, int64_t row_start,
     }
 }
 
+// Where even the largest logit is below this, sigma(x) is exp(x) to 2e-9.
+constexpr float kSmallScore = -20.0f;
+
 // Unnormalised scores of a token's experts: z[i] / (sum of z over the token)
 // are its probabilities; 0 for experts that are off.  Softmax: exp(x - max).
-// Sigmoid: sigma(x); where even the largest logit is below -20, sigma(x) is
-// exp(x) to 2e-9, and exp(x - max) keeps a row of tiny scores from vanishing.
+// Sigmoid: sigma(x), or for a row of small scores exp(x - max), which keeps it
+// from vanishing.
 // slope[i] is d log z / dx of the score: 1, or sigma(-x).  m is the largest
 // logit.
 template <int LPT, int VPL>
@@ -240,12 +254,12 @@ __device__ __forceinline__ void scores(const float (&x)[VPL], bool sigmoid, floa
         z[i] = 0.0f;
         slope[i] = 1.0f;
         if (finite(x[i])) {
-            if (sigmoid && m > -20.0f) {
+            if (sigmoid && m > kSmallScore) {
                 const Sigmoids g = sigmoids(x[i]);
                 z[i] = g.pos;
                 slope[i] = g.neg;
             } else {
-                z[i] = expf(x[i] - m);
+                z[i] = exp_neg(x[i] - m);
                 // below -20 sigma(-x) rounds to 1
             }
         }
@@ -273,26 +287,30 @@ template <int LPT, int SEL>
 __device__ __forceinline__ void entry_weights(const float (&xe)[SEL], const RouteArgs& a, float m,
                                               float total, float (&w)[SEL]) {
     if (a.normalize) {
-        float l[SEL], top = -3.402823466e38f, s = 0.0f;
+        float top = -3.402823466e38f, s = 0.0f;
 #pragma unroll
-        for (int q = 0; q < SEL; ++q) {
-            l[q] = a.sigmoid ? log_sigmoid(xe[q]) : xe[q];
-            if (finite(xe[q])) top = fmaxf(top, l[q]);
-        }
+        for (int q = 0; q < SEL; ++q)
+            if (finite(xe[q])) top = fmaxf(top, xe[q]);
         top = token_fmax<LPT>(top);
-#pragma unroll
-        for (int q = 0; q < SEL; ++q) {
-            w[q] = finite(xe[q]) ? expf(l[q] - top) : 0.0f;
-            s += w[q];
-        }
-        s = token_sum<LPT>(s);
-#pragma unroll
-        for (int q = 0; q < SEL; ++q) w[q] = s > 0.0f ? w[q] / s : 0.0f;
-    } else {
+        const bool sigmoid = a.sigmoid && top > kSmallScore;
 #pragma unroll
         for (int q = 0; q < SEL; ++q) {
             w[q] = 0.0f;
-            if (finite(xe[q])) w[q] = a.sigmoid ? sigmoids(xe[q]).pos : expf(xe[q] - m) / total;
+            if (q * LPT < a.num_topk && finite(xe[q]))
+                w[q] = sigmoid ? sigmoids(xe[q]).pos : exp_neg(xe[q] - top);
+            s += w[q];
+        }
+        s = token_sum<LPT>(s);
+        const float r = s > 0.0f ? 1.0f / s : 0.0f;
+#pragma unroll
+        for (int q = 0; q < SEL; ++q) w[q] *= r;
+    } else {
+        const float r = 1.0f / total;
+#pragma unroll
+        for (int q = 0; q < SEL; ++q) {
+            w[q] = 0.0f;
+            if (q * LPT < a.num_topk && finite(xe[q]))
+                w[q] = a.sigmoid ? sigmoids(xe[q]).pos : exp_neg(xe[q] - m) * r;
         }
     }
 }
