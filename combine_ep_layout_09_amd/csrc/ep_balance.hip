@@ -69,6 +69,7 @@ __global__ __launch_bounds__(kSum) void balance_sum_kernel(RouteArgs a, const in
     __shared__ int32_t counts[kWidth];
     __shared__ int32_t live_count;
     const int lane = threadIdx.x % LPT;
+    const Experts own = spread<LPT, VPL, BF16>(lane);
     const int slot = threadIdx.x / LPT;
     const int wave = threadIdx.x / kWave;
     const int E = a.num_experts, k = a.num_topk;
@@ -90,8 +91,8 @@ __global__ __launch_bounds__(kSum) void balance_sum_kernel(RouteArgs a, const in
         const int64_t t = t0 + at;
         const bool live = at < end && (valid == nullptr || valid[t] != 0);
         float x[VPL], z[VPL], slope[VPL], total, top;
-        load_logits<VPL, BF16>(a.logits, (live ? t : t0) * a.stride, live ? E : 0, lane * VPL,
-                               a.pieces, x);
+        load_logits<VPL, BF16>(a.logits, (live ? t : t0) * a.stride, live ? E : 0, own, a.pieces,
+                               x);
         if (live) {
             if (lane == 0) ++mine;
             for (int j = lane; j < k; j += LPT) {
@@ -113,7 +114,7 @@ __global__ __launch_bounds__(kSum) void balance_sum_kernel(RouteArgs a, const in
             p = swap32(__float_as_uint(acc[i]));
             acc[i] = __uint_as_float(p.x) + __uint_as_float(p.y);
         }
-        if (LPT == 64 || threadIdx.x % kWave < 16) sums[wave][lane * VPL + i] = acc[i];
+        if (LPT == 64 || threadIdx.x % kWave < 16) sums[wave][expert<VPL, BF16>(own, i)] = acc[i];
     }
     if (mine) atomicAdd(&live_count, mine);
     __syncthreads();

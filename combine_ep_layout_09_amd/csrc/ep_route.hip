@@ -143,7 +143,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
     const int64_t row = (inside ? t : 0) * a.stride;
 
     float x[VPL];
-    load_logits<VPL, BF16>(a.logits, row, live ? E : 0, lane * VPL, a.pieces, x);
+    load_logits<VPL, BF16>(a.logits, row, live ? E : 0, consecutive<VPL, BF16>(lane), a.pieces, x);
     float m = 0.0f, total = 1.0f;
     if (!a.sigmoid && !a.normalize) {
         float z[VPL], slope[VPL];
@@ -243,20 +243,19 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     const int32_t* counts, const int32_t* num_valid, const float* d_loss, void* d_logits) {
     constexpr int kTokens = kThreads / LPT;
     constexpr int kSel = kMaxTopk > LPT ? kMaxTopk / LPT : 1;
-    // lane runs of VPL, padded so that 16-byte reads of 8 lanes meet 32 banks
-    constexpr int kRun = VPL >= 8 ? VPL + 4 : VPL;
-    __shared__ __attribute__((aligned(16))) float add[kTokens][LPT * kRun];
+    constexpr int W = kPiece<VPL, BF16>;
+    __shared__ __attribute__((aligned(16))) float add[kTokens][LPT * VPL];
     const int lane = threadIdx.x % LPT;
     const int slot = threadIdx.x / LPT;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + slot;
     const bool inside = t < a.num_tokens;
     const bool live = inside && (valid == nullptr || valid[t] != 0);
     const int E = a.num_experts, k = a.num_topk;
-    const int first = lane * VPL;
+    const Experts own = spread<LPT, VPL, BF16>(lane);
     const int64_t row = (inside ? t : 0) * a.stride;
 
     float x[VPL], dx[VPL];
-    load_logits<VPL, BF16>(a.logits, row, live ? E : 0, first, a.pieces, x);
+    load_logits<VPL, BF16>(a.logits, row, live ? E : 0, own, a.pieces, x);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) dx[i] = 0.0f;
     const bool loss = d_loss != nullptr;
@@ -277,16 +276,20 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
                         (static_cast<float>(a.num_seqs) * static_cast<float>(k)) * d_loss[0] / n / n;
         const int32_t c0 = c[0];
         int32_t ci[VPL];
-        if (VPL >= 4 && a.count_pieces) {
+        if (W >= 4 && a.count_pieces) {
 #pragma unroll
             for (int i = 0; i + 3 < VPL; i += 4) {
-                const int4 v = first + i < E ? *reinterpret_cast<const int4*>(c + first + i)
-                                             : make_int4(c0, c0, c0, c0);
+                const int at = expert<VPL, BF16>(own, i);
+                const int4 v = at < E ? *reinterpret_cast<const int4*>(c + at)
+                                      : make_int4(c0, c0, c0, c0);
                 ci[i] = v.x, ci[i + 1] = v.y, ci[i + 2] = v.z, ci[i + 3] = v.w;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) ci[i] = first + i < E ? c[first + i] : c0;
+            for (int i = 0; i < VPL; ++i) {
+                const int at = expert<VPL, BF16>(own, i);
+                ci[i] = at < E ? c[at] : c0;
+            }
         }
         float d[VPL], dot = 0.0f;
 #pragma unroll
@@ -338,20 +341,20 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
         join_entries<LPT, kSel, 0>(e, part, k, lane, sum, mine);
         float* to = add[slot];
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) to[lane * kRun + i] = 0.0f;
+        for (int i = 0; i < VPL; ++i) to[expert<VPL, BF16>(own, i)] = 0.0f;
         wave_sync();
 #pragma unroll
         for (int q = 0; q < kSel; ++q)
-            if (mine[q]) to[e[q] / VPL * kRun + e[q] % VPL] = sum[q];
+            if (mine[q]) to[e[q]] = sum[q];
         wave_sync();
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) dx[i] += to[lane * kRun + i];
+        for (int i = 0; i < VPL; ++i) dx[i] += to[expert<VPL, BF16>(own, i)];
     }
     if (inside) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
             if (!finite(x[i])) dx[i] = 0.0f;
-        store_logits<VPL, BF16>(d_logits, t * E, E, first, a.out_pieces, dx);
+        store_logits<VPL, BF16>(d_logits, t * E, E, own, a.out_pieces, dx);
     }
 }
 

@@ -1,8 +1,10 @@
 // ep_route_dev.h -- device helpers of the routing kernels (gfx950, wave64).
 //
 // A token is handled by LPT consecutive lanes of one wave (16 or 64), each
-// holding VPL consecutive experts, so LPT * VPL >= E and the lowest lane with
-// a value also holds the lowest expert index.  Reductions leave their result
+// holding VPL experts, LPT * VPL >= E.  Where the order of the experts matters
+// a lane's are consecutive, so the lowest lane with a value also holds the
+// lowest expert index; elsewhere they lie in pieces of up to 16 bytes spread so
+// that the lanes of a token access consecutive memory.  Reductions leave their result
 // in every lane of the token and combine in a fixed order.
 #pragma once
 
@@ -165,33 +167,55 @@ __device__ __forceinline__ Sigmoids sigmoids(float x) {
     const float s = t * r;
     return x >= 0.0f ? Sigmoids{r, s} : Sigmoids{s, r};
 }
-// Row of `n` logits: VPL of them from index lane * VPL on, NaN (an expert
-// that is off) past the end.  `piece` is the host's word that rows may be
-// read in aligned pieces of min(VPL, 16 bytes' worth) elements that do not
-// straddle the row's end.
+// Elements of a piece: 16 bytes, or all that a lane holds.
 template <int VPL, bool BF16>
-__device__ __forceinline__ void load_logits(const void* base, int64_t row_start, int n, int first,
-                                            bool piece, float (&x)[VPL]) {
+constexpr int kPiece = VPL < (BF16 ? 8 : 4) ? VPL : (BF16 ? 8 : 4);
+
+// The experts of a lane: register i is expert first + (i / W) * step + i % W
+// with W = kPiece.
+struct Experts {
+    int first, step;
+};
+template <int VPL, bool BF16>
+__device__ __forceinline__ Experts consecutive(int lane) {
+    return {lane * VPL, kPiece<VPL, BF16>};
+}
+template <int LPT, int VPL, bool BF16>
+__device__ __forceinline__ Experts spread(int lane) {
+    return {lane * kPiece<VPL, BF16>, LPT * kPiece<VPL, BF16>};
+}
+template <int VPL, bool BF16>
+__device__ __forceinline__ int expert(const Experts& x, int i) {
+    return x.first + i / kPiece<VPL, BF16> * x.step + i % kPiece<VPL, BF16>;
+}
+
+// A lane's logits of a row of n, NaN (an expert that is off) past the end.
+// `piece` is the host's word that rows may be read in aligned pieces that do
+// not straddle the row's end.
+template <int VPL, bool BF16>
+__device__ __forceinline__ void load_logits(const void* base, int64_t row_start, int n,
+                                            const Experts& at, bool piece, float (&x)[VPL]) {
     const float nan = __uint_as_float(0x7fc00000u);
+    constexpr int W = kPiece<VPL, BF16>;
     if constexpr (BF16) {
-        const uint16_t* p = static_cast<const uint16_t*>(base) + row_start + first;
-        constexpr int W = VPL < 8 ? VPL : 8;
+        const uint16_t* p = static_cast<const uint16_t*>(base) + row_start;
         if (W > 1 && piece) {
 #pragma unroll
             for (int i = 0; i < VPL; i += W) {
-                const bool in = first + i < n;
+                const int e = at.first + i / W * at.step;
+                const bool in = e < n;
                 uint32_t w[W > 1 ? W / 2 : 1];
 #pragma unroll
                 for (int q = 0; q < W / 2; ++q) w[q] = 0x7fc07fc0u;
                 if (in) {
                     if constexpr (W == 8) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(p + i);
+                        const uint4 v = *reinterpret_cast<const uint4*>(p + e);
                         w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
                     } else if constexpr (W == 4) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(p + i);
+                        const uint2 v = *reinterpret_cast<const uint2*>(p + e);
                         w[0] = v.x, w[1] = v.y;
                     } else if constexpr (W == 2) {
-                        w[0] = *reinterpret_cast<const uint32_t*>(p + i);
+                        w[0] = *reinterpret_cast<const uint32_t*>(p + e);
                     }
                 }
 #pragma unroll
@@ -202,31 +226,36 @@ __device__ __forceinline__ void load_logits(const void* base, int64_t row_start,
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                x[i] = first + i < n ? __uint_as_float(static_cast<uint32_t>(p[i]) << 16) : nan;
+            for (int i = 0; i < VPL; ++i) {
+                const int e = expert<VPL, BF16>(at, i);
+                x[i] = e < n ? __uint_as_float(static_cast<uint32_t>(p[e]) << 16) : nan;
+            }
         }
     } else {
-        const float* p = static_cast<const float*>(base) + row_start + first;
-        constexpr int W = VPL < 4 ? VPL : 4;
+        const float* p = static_cast<const float*>(base) + row_start;
         if (W > 1 && piece) {
 #pragma unroll
             for (int i = 0; i < VPL; i += W) {
-                const bool in = first + i < n;
+                const int e = at.first + i / W * at.step;
+                const bool in = e < n;
 #pragma unroll
                 for (int q = 0; q < W; ++q) x[i + q] = nan;
                 if (in) {
                     if constexpr (W == 4) {
-                        const float4 v = *reinterpret_cast<const float4*>(p + i);
+                        const float4 v = *reinterpret_cast<const float4*>(p + e);
                         x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
                     } else if constexpr (W == 2) {
-                        const float2 v = *reinterpret_cast<const float2*>(p + i);
+                        const float2 v = *reinterpret_cast<const float2*>(p + e);
                         x[i] = v.x, x[i + 1] = v.y;
                     }
                 }
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) x[i] = first + i < n ? p[i] : nan;
+            for (int i = 0; i < VPL; ++i) {
+                const int e = expert<VPL, BF16>(at, i);
+                x[i] = e < n ? p[e] : nan;
+            }
         }
     }
 }
@@ -315,52 +344,58 @@ __device__ __forceinline__ void entry_weights(const float (&xe)[SEL], const Rout
     }
 }
 
-// Dense row of n gradients in the logits' type, rounded to nearest even.
+// A lane's part of a dense row of n gradients in the logits' type, rounded to
+// nearest even.
 template <int VPL, bool BF16>
-__device__ __forceinline__ void store_logits(void* base, int64_t row_start, int n, int first,
-                                             bool piece, const float (&v)[VPL]) {
+__device__ __forceinline__ void store_logits(void* base, int64_t row_start, int n,
+                                             const Experts& at, bool piece, const float (&v)[VPL]) {
+    constexpr int W = kPiece<VPL, BF16>;
     if constexpr (BF16) {
-        uint16_t* p = static_cast<uint16_t*>(base) + row_start + first;
-        constexpr int W = VPL < 8 ? VPL : 8;
+        uint16_t* p = static_cast<uint16_t*>(base) + row_start;
         uint32_t h[VPL];
 #pragma unroll
         for (int i = 0; i < VPL; ++i) h[i] = f32_to_bf16_rne(v[i]);
         if (W > 1 && piece) {
 #pragma unroll
             for (int i = 0; i < VPL; i += W) {
-                if (first + i >= n) continue;
+                const int e = at.first + i / W * at.step;
+                if (e >= n) continue;
                 if constexpr (W == 8)
-                    *reinterpret_cast<uint4*>(p + i) =
+                    *reinterpret_cast<uint4*>(p + e) =
                         make_uint4(h[i] | h[i + 1] << 16, h[i + 2] | h[i + 3] << 16,
                                    h[i + 4] | h[i + 5] << 16, h[i + 6] | h[i + 7] << 16);
                 else if constexpr (W == 4)
-                    *reinterpret_cast<uint2*>(p + i) =
+                    *reinterpret_cast<uint2*>(p + e) =
                         make_uint2(h[i] | h[i + 1] << 16, h[i + 2] | h[i + 3] << 16);
                 else if constexpr (W == 2)
-                    *reinterpret_cast<uint32_t*>(p + i) = h[i] | h[i + 1] << 16;
+                    *reinterpret_cast<uint32_t*>(p + e) = h[i] | h[i + 1] << 16;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (first + i < n) p[i] = static_cast<uint16_t>(h[i]);
+            for (int i = 0; i < VPL; ++i) {
+                const int e = expert<VPL, BF16>(at, i);
+                if (e < n) p[e] = static_cast<uint16_t>(h[i]);
+            }
         }
     } else {
-        float* p = static_cast<float*>(base) + row_start + first;
-        constexpr int W = VPL < 4 ? VPL : 4;
+        float* p = static_cast<float*>(base) + row_start;
         if (W > 1 && piece) {
 #pragma unroll
             for (int i = 0; i < VPL; i += W) {
-                if (first + i >= n) continue;
+                const int e = at.first + i / W * at.step;
+                if (e >= n) continue;
                 if constexpr (W == 4)
-                    *reinterpret_cast<float4*>(p + i) =
+                    *reinterpret_cast<float4*>(p + e) =
                         make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 else if constexpr (W == 2)
-                    *reinterpret_cast<float2*>(p + i) = make_float2(v[i], v[i + 1]);
+                    *reinterpret_cast<float2*>(p + e) = make_float2(v[i], v[i + 1]);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (first + i < n) p[i] = v[i];
+            for (int i = 0; i < VPL; ++i) {
+                const int e = expert<VPL, BF16>(at, i);
+                if (e < n) p[e] = v[i];
+            }
         }
     }
 }
