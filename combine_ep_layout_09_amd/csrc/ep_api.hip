@@ -133,7 +133,7 @@ int check_logits(const ep_routing& rt, const void* logits, int bf16, int64_t str
 }
 
 ep::RouteArgs route_args(const ep_routing& rt, const void* logits, int bf16, int64_t stride,
-                         const void* d_logits, const void* counts) {
+                         const void* d_logits, const void* per_expert) {
     ep::RouteArgs a;
     a.logits = logits;
     a.stride = stride;
@@ -164,7 +164,7 @@ ep::RouteArgs route_args(const ep_routing& rt, const void* logits, int bf16, int
     };
     a.pieces = fits(logits, stride);
     a.out_pieces = fits(d_logits, rt.num_experts);
-    a.count_pieces = rt.num_experts % 4 == 0 && aligned16(counts);
+    a.fours = rt.num_experts % 4 == 0 && aligned16(per_expert);
     return a;
 }
 
@@ -280,8 +280,9 @@ int ep_route(const ep_routing* rt, const void* logits, int logits_bf16, int64_t 
     if (!aligned4(expert_bias) || !aligned4(topk_idx) || !aligned4(topk_weights))
         return EP_ERR_ALIGN;
     const ep::RouteForward f = {expert_bias, valid, topk_idx, topk_weights};
-    return from_hip(ep::launch_route(route_args(*rt, logits, logits_bf16, logits_stride, nullptr, nullptr),
-                                     f, static_cast<hipStream_t>(stream)));
+    return from_hip(ep::launch_route(
+        route_args(*rt, logits, logits_bf16, logits_stride, nullptr, expert_bias), f,
+        static_cast<hipStream_t>(stream)));
 }
 
 int64_t ep_balance_workspace_bytes(const ep_routing* rt) {

@@ -155,9 +155,9 @@ __global__ __launch_bounds__(kFinish) void balance_mean_kernel(
     double term = 0.0;
     for (int64_t base = static_cast<int64_t>(blockIdx.x) * cols; base < outputs;
          base += static_cast<int64_t>(gridDim.x) * cols) {
-        const int64_t o = base + col;
-        const int64_t seq = o / E;
-        const int e = static_cast<int>(o % E);
+        const uint32_t o = static_cast<uint32_t>(base) + col;  // B * E is at most 2^30
+        const int64_t seq = o / static_cast<uint32_t>(E);
+        const int e = static_cast<int>(o % static_cast<uint32_t>(E));
         double s = 0.0;
         int c = 0, n = 0;
         if (o < outputs) {

@@ -84,7 +84,7 @@ hipError_t launch_combine(const ep_problem& p, const void* expert_out, const int
 // Routing (gate logits): the problem as the kernels take it.  `pieces` /
 // `out_pieces`: rows of the logits / of the dense gradient can be accessed in
 // aligned pieces of min(experts per lane, 16 bytes' worth) elements;
-// `count_pieces`: rows of counts in aligned groups of four.  `group_lanes`:
+// `fours`: the bias (or rows of counts) in aligned groups of four.  `group_lanes`:
 // lanes of a token that a group of experts fills exactly, 0 if it does not.
 struct RouteArgs {
     const void* logits;
@@ -93,7 +93,7 @@ struct RouteArgs {
     int32_t num_seqs, seq_len;
     float scale;
     int32_t group_lanes;
-    bool bf16, sigmoid, normalize, pieces, out_pieces, count_pieces;
+    bool bf16, sigmoid, normalize, pieces, out_pieces, fours;
 };
 // Lanes per token and experts per lane of the routing kernels.
 struct TokenShape {

@@ -130,7 +130,9 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
                                                          float* topk_weights) {
     constexpr int kTokens = kThreads / LPT;
     constexpr int kSel = kMaxTopk > LPT ? kMaxTopk / LPT : 1;
-    __shared__ uint32_t lds_keys[kTokens][LPT * VPL];
+    // runs of VPL experts, padded so that 16-byte accesses of 8 lanes meet 32 banks
+    constexpr int kRun = VPL >= 8 ? VPL + 4 : VPL;
+    __shared__ __attribute__((aligned(16))) uint32_t lds_keys[kTokens][LPT * kRun];
     __shared__ double lds_score[kTokens][kMaxGroups];
     __shared__ int lds_chosen[kTokens][kMaxTopk];
     const int lane = threadIdx.x % LPT;
@@ -142,8 +144,9 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
     const int E = a.num_experts;
     const int64_t row = (inside ? t : 0) * a.stride;
 
+    const Experts from = spread<LPT, VPL, BF16>(lane);
     float x[VPL];
-    load_logits<VPL, BF16>(a.logits, row, live ? E : 0, consecutive<VPL, BF16>(lane), a.pieces, x);
+    load_logits<VPL, BF16>(a.logits, row, live ? E : 0, from, a.pieces, x);
     float m = 0.0f, total = 1.0f;
     if (!a.sigmoid && !a.normalize) {
         float z[VPL], slope[VPL];
@@ -151,10 +154,40 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
     }
     uint32_t key[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        float v = x[i];
-        if (bias != nullptr && lane * VPL + i < E) v += bias[lane * VPL + i];
-        key[i] = finite(x[i]) && finite(v) ? order_key(v) : 0u;
+    for (int i = 0; i < VPL; ++i) key[i] = finite(x[i]) ? order_key(x[i]) : 0u;
+    if (bias != nullptr) {
+        float more[VPL];
+        if (kPiece<VPL, BF16> >= 4 && a.fours) {
+#pragma unroll
+            for (int i = 0; i + 3 < VPL; i += 4) {
+                const int e = expert<VPL, BF16>(from, i);
+                const float4 v = e < E ? *reinterpret_cast<const float4*>(bias + e)
+                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                more[i] = v.x, more[i + 1] = v.y, more[i + 2] = v.z, more[i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const int e = expert<VPL, BF16>(from, i);
+                more[i] = e < E ? bias[e] : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const float v = x[i] + more[i];
+            key[i] = finite(x[i]) && finite(v) ? order_key(v) : 0u;
+        }
+    }
+    if constexpr (VPL > kPiece<VPL, BF16>) {  // to consecutive experts, through LDS
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int e = expert<VPL, BF16>(from, i);
+            lds_keys[slot][e / VPL * kRun + e % VPL] = key[i];
+        }
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) key[i] = lds_keys[slot][lane * kRun + i];
+        wave_sync();
     }
     if (a.num_groups > 1) limit_groups<LPT, VPL>(key, lds_keys[slot], lds_score[slot], lane, a);
 
@@ -276,7 +309,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
                         (static_cast<float>(a.num_seqs) * static_cast<float>(k)) * d_loss[0] / n / n;
         const int32_t c0 = c[0];
         int32_t ci[VPL];
-        if (W >= 4 && a.count_pieces) {
+        if (W >= 4 && a.fours) {
 #pragma unroll
             for (int i = 0; i + 3 < VPL; i += 4) {
                 const int at = expert<VPL, BF16>(own, i);
