@@ -522,7 +522,7 @@ def _logits_args(rt, logits):
     if inner != 1 and E > 1:
         raise ValueError("logits must be contiguous along the experts")
     if T <= 1:
-        stride = max(stride, E)
+        stride = E
     if stride < E:
         raise ValueError(f"logits rows overlap: row pitch {stride} below {E}")
     return dev, logits.data_ptr(), bf16, stride

@@ -113,14 +113,13 @@ int check_routing(const ep_routing* rt) {
         rt->normalize < 0 || rt->normalize > 1 || !std::isfinite(rt->weight_scale))
         return EP_ERR_ARG;
     if (rt->num_experts > ep::kMaxExperts || rt->num_topk > ep::kMaxTopk ||
-        rt->num_groups > ep::kMaxGroups || rt->num_seqs > ep::kMaxSeqs)
+        rt->num_groups > ep::kMaxGroups || rt->num_seqs > ep::kMaxSeqs ||
+        rt->num_tokens > ep::kMaxRouted)
         return EP_ERR_UNSUPPORTED;
     if (rt->num_experts % rt->num_groups != 0 || rt->topk_groups > rt->num_groups ||
         rt->num_topk > rt->topk_groups * (rt->num_experts / rt->num_groups) ||
         rt->num_tokens % rt->num_seqs != 0)
         return EP_ERR_ARG;
-    if (static_cast<int64_t>(rt->num_tokens) * rt->num_topk >= (int64_t{1} << 31))
-        return EP_ERR_UNSUPPORTED;
     return EP_OK;
 }
 
@@ -310,8 +309,9 @@ int ep_balance_loss(const ep_routing* rt, const void* logits, int logits_bf16,
         !aligned4(loss) || !aligned16(workspace))
         return EP_ERR_ALIGN;
     const ep::BalanceArgs b = {topk_idx, valid, coef, counts, mean_prob, num_valid, loss};
-    return from_hip(ep::launch_balance(route_args(*rt, logits, logits_bf16, logits_stride, nullptr, nullptr),
-                                       b, workspace, static_cast<hipStream_t>(stream)));
+    return from_hip(ep::launch_balance(
+        route_args(*rt, logits, logits_bf16, logits_stride, nullptr, nullptr), b, workspace,
+        static_cast<hipStream_t>(stream)));
 }
 
 int ep_route_backward(const ep_routing* rt, const void* logits, int logits_bf16,

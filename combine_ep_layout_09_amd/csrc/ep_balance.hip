@@ -13,7 +13,9 @@
 // partial sums.  Second kernel: the rows are added in order, in fp64.  Up to
 // kOneGroup partial sums one workgroup does it, and the loss with them; above
 // that many workgroups, and a third kernel adds their parts of the loss.  No
-// sum depends on the order in which workgroups run.
+// sum depends on the order in which workgroups run.  16384 x 256 fp32 in four
+// sequences: 8, 4.8 and 1.8 us; with one workgroup for all 65536 partial sums the
+// call took 38 us, so 16.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

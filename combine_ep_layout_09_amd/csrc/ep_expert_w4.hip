@@ -6,20 +6,21 @@
 // for the rows r of expert e, summed in fp32; optionally the gated activation
 // silu(y[r, n]) * y[r, N + n]; one rounding to bf16.
 //
-// A decode batch gives each expert a handful of rows, so the weights, 17/32
-// byte each, are the traffic and every one should be read once.  A workgroup
-// takes 64 weight rows of one expert against up to 16 * MT rows; its four
-// waves split the input channels in turns of 128 and add their sums in LDS, in
-// wave order.  Weights and rows meet in bf16 MFMA: every E2M1 value times a
-// power of two is a bf16, and v_cvt_scalef32_pk_bf16_fp4 makes two of them
-// from one byte, so the products are those of the formula and only the sum
-// rounds.  (The MFMA that takes E2M1 itself keeps fewer bits of its partial
-// sums than fp32: 3e-5 of the result on random data.)
+// Weights and rows meet in bf16 MFMA: every E2M1 value times a power of two is
+// a bf16, and v_cvt_scalef32_pk_bf16_fp4 makes two of them from one byte at the
+// rate of any other instruction, so the products are those of the formula and
+// only the sums round.  (The MFMA that takes E2M1 itself keeps fewer bits of
+// its partial sums than fp32: 3e-5 of the result on random data.)
 //
 // The channels of an MFMA may be taken in any order if both operands agree.
-// Lane l holds weight row l % 16 and the 16 bytes, 32 channels, one scale, at
-// block l / 16 of the 128: a wave reads the codes as they lie in memory, row
-// by row, and needs neither a shuffle nor LDS.
+// Lane l multiplies weight row l % 16 and the 32 channels, 16 bytes of codes
+// and one scale, at block l / 16 of a chunk of 128: codes are used as they lie
+// in memory.
+//
+// Two kernels.  A decode batch gives each expert a handful of rows, so the
+// weights, 17/32 byte each, are the traffic and should be read once, at the
+// memory's rate: expert_w4_kernel.  With many rows per expert the matrix cores
+// and the rows' own traffic count as well: expert_w4_tile_kernel.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -33,9 +34,9 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kTiles = 4;            // 16-row weight tiles per workgroup
-constexpr int kRows = 16 * kTiles;   // weight rows per workgroup
-constexpr int kStep = 128;           // channels per wave and step
+constexpr int kTiles = 4;            // 16-row weight tiles of a wave
+constexpr int kRows = 16 * kTiles;   // weight rows of a wave
+constexpr int kStep = 128;           // channels of a chunk
 constexpr int kSegment = 8192;       // channels whose scales LDS holds at a time
 constexpr int kSegSteps = kSegment / kStep;
 constexpr int kScaleRow = kSegment / 32 + 4;  // bytes; a step's four scales of 16
@@ -186,14 +187,23 @@ struct Stage {
     u32x4 x[2][MT][FP8 ? 2 : 4];
 };
 
-// Few rows per expert.  FP8: rows are E4M3FN with one scale per 128 channels
-// (UE8: a UE8M0 byte, else fp32), which multiplies the step's sum.  GATED:
-// tiles 0, 1 are rows n of the gate half and tiles 2, 3 rows N + n.  WORDS:
-// K % 128 == 0, so rows of scales are whole words.
+// Few rows per expert.  A workgroup takes 64 weight rows of one expert against
+// up to 16 * MT rows; its WAVES waves take pairs of chunks in turns and add
+// their sums in LDS, in wave order.  FP8: rows are E4M3FN with one scale per 128
+// channels (UE8: a UE8M0 byte, else fp32), which multiplies the chunk's sum.
+// GATED: tiles 0, 1 are rows n of the gate half and tiles 2, 3 rows N + n.
+// WORDS: K % 128 == 0, so rows of scales are whole words.
 //
-// WAVES waves take the steps of a segment in turns.  Each keeps the loads of
-// its next step in flight while it multiplies the present one.  The scales,
-// scattered bytes in memory, are read once, whole rows at a time, into LDS.
+// What bounds it is how the codes are read.  A load covers 8 rows x 128 bytes:
+// whole cache lines, so they need not be kept for another wave (non-temporal),
+// which this memory rewards: reading alone reaches 7.0 TB/s so, 6.2 with 64-byte
+// pieces of 16 rows, the MFMA's own layout, or when the lines are kept.  Pairing
+// two chunks across lanes afterwards costs 1.5 instructions per word.  The
+// scales, scattered bytes in memory, come once, whole rows at a time, to LDS.
+// Loads two steps ahead, or more waves, were slower: what is in flight then
+// outgrows the caches.  256 experts, K 7168, N 2048 gated, 4 FP8 rows each: 590 us,
+// 6.8 TB/s (696 with 64-byte pieces, 640 with the lines kept); K 2048, N 7168, bf16
+// rows: 335 us, 5.9 TB/s; 8 experts of one token: 25 us, 4.9 TB/s.
 template <int WAVES, int MT, bool FP8, bool UE8, bool GATED, bool WORDS>
 __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void expert_w4_kernel(Args a) {
     constexpr int kThreads = WAVES * kWave;
@@ -411,9 +421,11 @@ __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void e
 // Many rows per expert: a workgroup takes 256 weight rows, 64 per wave, against
 // up to 16 * MT rows.  The rows' operands are the same for the four waves: each
 // chunk of 128 channels passes through LDS, as bf16, once for all of them,
-// while the next chunk is on its way; the weights' next pair of chunks is in
-// flight as in the kernel above.  GATED: a wave's tiles 0, 1 are gate and 2, 3
-// up of the same 32 outputs.
+// loaded two chunks ahead; the weights' next pair of chunks is in flight as
+// well.  GATED: a wave's tiles 0, 1 are gate and 2, 3 up of the same 32 outputs.
+// 64 skewed experts, 48 rows each in the mean, K 4096, N 1408 gated, bf16: 132 us
+// (242 with the other kernel).  Matrix instructions are a third of that, their
+// operands' conversion another; memory alone would take 83.
 constexpr int kTileSegment = 4096;                 // channels of weight scales in LDS
 constexpr int kTileScaleRow = kTileSegment / 32 + 4;  // bytes
 constexpr int kTileRow = kStep * 2 + 16;           // bytes of a row's chunk in LDS

@@ -13,6 +13,7 @@ constexpr int kMaxTopk = 32;
 constexpr int kMaxHidden = 65536;
 constexpr int kMaxGroups = 64;
 constexpr int kMaxSeqs = 1 << 20;
+constexpr int kMaxRouted = 1 << 25;  // tokens: 64 lanes each stay below 2^32 threads
 
 // Workgroup width (a multiple of 64, at most 1024) and number of column tiles
 // that cover a row of nvec 16-byte pieces with vpl pieces per lane.

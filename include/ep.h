@@ -242,7 +242,7 @@ int ep_e4m3_encode(const float* in, uint8_t* out, int64_t n, void* stream);
  * z_e = 1 / (1 + exp(-x_e)).  Probabilities p_e = z_e / sum_i z_i over the
  * token's experts.  Sums, maxima and gradients are held in fp32 or fp64. */
 typedef struct ep_routing {
-    int32_t num_tokens;   /* T >= 0 */
+    int32_t num_tokens;   /* T, 0 .. 2^25 */
     int32_t num_experts;  /* E, 1 .. 1024 */
     int32_t num_topk;     /* k, 1 .. 32, at most topk_groups * (E / num_groups) */
     int32_t num_groups;   /* G, 1 .. 64, divides E; groups are runs of E / G experts */
@@ -329,8 +329,10 @@ typedef struct ep_expert_w4_t {
 
 /* out[r, n] = sum_k rows[r, k] * weight[e, n, k] for every receive row r that
  * an entry of expert e fills (activation 0; see above for 1).  Products are
- * exact, sums fp32 in a fixed order, one rounding to bf16.  Rows that no
- * entry fills are neither read nor written.
+ * exact, sums fp32 in a fixed order (FP8 rows: each block of 128 channels is
+ * summed, then multiplied by its scale), one rounding to bf16.  Rows that no
+ * entry fills are neither read nor written; a row's sum does not depend on the
+ * other rows' values.
  *   prob        T, k, E and capacity of the layout; hidden and use_fp8 are not read beyond
  *               the common checks.
  *   rows        [R, K], bf16 or E4M3FN bytes, in the receive-row layout (ep_dispatch's

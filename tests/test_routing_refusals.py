@@ -32,6 +32,7 @@ BAD = [
     (dict(num_tokens=1 << 21, num_seqs=1 << 21), UNSUPPORTED),
     (dict(num_experts=60), ARG), (dict(topk_groups=9), ARG), (dict(num_topk=17), ARG),
     (dict(num_seqs=3), ARG), (dict(num_tokens=1 << 30), UNSUPPORTED),
+    (dict(num_tokens=(1 << 25) + 2), UNSUPPORTED),
 ]
 
 
