@@ -451,6 +451,12 @@ def _arg(t, name, dtype, numel, dev, allow_none=False):
     """Pointer of a contiguous tensor of `numel` elements on device `dev`."""
     if t is None and allow_none:
         return None
+    try:  # what nearly every call passes, checked without naming what is wrong
+        if (t.dtype is dtype and t.numel() == numel and t.is_contiguous()
+                and t.get_device() == dev):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -638,13 +644,12 @@ def prepare_route_backward(rt, logits, topk_idx, d_logits, d_weights=None, coef=
 def _expert_w4_args(prob, mm, rows, layout, codes, scales, out, row_scales):
     torch = _torch()
     dev = _device_of(rows, "rows")
-    R = ep_num_recv_rows(prob)
     K, N, E, fmt = mm.in_features, mm.out_features, prob.num_experts, mm.in_format
+    R = E * prob.capacity if prob.capacity else prob.num_tokens * prob.num_topk
     n2 = 2 * N if mm.activation == 1 else N
     u8 = torch.uint8
-    s = _LayoutPtrs()
-    s.count = _arg(layout.count, "count", torch.int32, E, dev)
-    s.offset = _arg(layout.offset, "offset", torch.int32, E + 1, dev)
+    s = _LayoutPtrs(_arg(layout.count, "count", torch.int32, E, dev),
+                    _arg(layout.offset, "offset", torch.int32, E + 1, dev))
     if fmt == 0:
         rp = _arg(rows, "rows", torch.bfloat16, R * K, dev)
         sp = None

@@ -423,6 +423,9 @@ __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void e
 // chunk of 128 channels passes through LDS, as bf16, once for all of them,
 // loaded two chunks ahead; the weights' next pair of chunks is in flight as
 // well.  GATED: a wave's tiles 0, 1 are gate and 2, 3 up of the same 32 outputs.
+// With 32-row tiles an expert mostly has one and its codes are read once (not
+// kept: 48.5 us, kept 51.6, at 24 rows each); with 64-row tiles several read
+// them (128 rows each: kept 124, not 127).
 // 64 skewed experts, 48 rows each in the mean, K 4096, N 1408 gated, bf16: 132 us
 // (242 with the other kernel).  Matrix instructions are a third of that, their
 // operands' conversion another; memory alone would take 83.
@@ -491,7 +494,7 @@ __global__ __launch_bounds__(256, 2) void expert_w4_tile_kernel(Args a) {
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                next_w[i][t] = load16<false>(t * 16 < kOut ? w_view : up_view,
+                next_w[i][t] = load16<MT == 2>(t * 16 < kOut ? w_view : up_view,
                                              at + (t * 16 % kOut + i * 8) * w_pitch, p * 128);
     };
     // A chunk's rows on their way to LDS: even and odd chunks have a set each,
@@ -592,7 +595,6 @@ __global__ __launch_bounds__(256, 2) void expert_w4_tile_kernel(Args a) {
                 part[t][m] = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[t][m];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            __builtin_amdgcn_sched_barrier(0);
             bf16x8 xf[MT];
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
