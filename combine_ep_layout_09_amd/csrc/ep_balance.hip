@@ -66,6 +66,7 @@ __global__ __launch_bounds__(kSum) void balance_sum_kernel(RouteArgs a, const in
                                                            int32_t* hist, int32_t* live_rows) {
     constexpr int kTokens = kSum / LPT;
     constexpr int kWidth = LPT * VPL;
+    constexpr int kSel = kMaxTopk > LPT ? kMaxTopk / LPT : 1;
     constexpr int kWaves = kSum / kWave;
     __shared__ float sums[kWaves][kWidth];
     __shared__ int32_t counts[kWidth];
@@ -90,18 +91,24 @@ __global__ __launch_bounds__(kSum) void balance_sum_kernel(RouteArgs a, const in
     int mine = 0;
     for (int base = begin; base < end; base += kTokens) {  // the same count for every wave
         const int at = base + slot;
-        const int64_t t = t0 + at;
-        const bool live = at < end && (valid == nullptr || valid[t] != 0);
+        const bool inside = at < end;
+        const int64_t t = inside ? t0 + at : t0;
         float x[VPL], z[VPL], slope[VPL], total, top;
-        load_logits<VPL, BF16>(a.logits, (live ? t : t0) * a.stride, live ? E : 0, own, a.pieces,
-                               x);
-        if (live) {
-            if (lane == 0) ++mine;
-            for (int j = lane; j < k; j += LPT) {
-                const int id = topk_idx[t * k + j];
-                if (id >= 0 && id < E) atomicAdd(&counts[id], 1);
-            }
+        load_logits<VPL, BF16>(a.logits, t * a.stride, inside ? E : 0, own, a.pieces, x);
+        int ids[kSel];
+#pragma unroll
+        for (int q = 0; q < kSel; ++q) {
+            const int j = q * LPT + lane;
+            ids[q] = inside && j < k ? topk_idx[t * k + j] : -1;
         }
+        const bool live = inside && (valid == nullptr || valid[t] != 0);
+        if (live && lane == 0) ++mine;
+#pragma unroll
+        for (int q = 0; q < kSel; ++q)
+            if (live && ids[q] >= 0 && ids[q] < E) atomicAdd(&counts[ids[q]], 1);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (!live) x[i] = __uint_as_float(0x7fc00000u);
         scores<LPT, VPL>(x, a.sigmoid, z, slope, total, top);
         const float r = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll

@@ -143,29 +143,19 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
     const int wave_lane = threadIdx.x % kWave;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + slot;
     const bool inside = t < a.num_tokens;
-    const bool live = inside && (valid == nullptr || valid[t] != 0);
     const int E = a.num_experts;
     const int64_t row = (inside ? t : 0) * a.stride;
 
     const Experts from = spread<LPT, VPL, BF16>(lane);
-    float x[VPL];
-    load_logits<VPL, BF16>(a.logits, row, live ? E : 0, from, a.pieces, x);
-    float m = 0.0f, total = 1.0f;
-    if (!a.sigmoid && !a.normalize) {
-        float z[VPL], slope[VPL];
-        scores<LPT, VPL>(x, false, z, slope, total, m);
-    }
-    uint32_t key[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = finite(x[i]) ? order_key(x[i]) : 0u;
+    float x[VPL], more[VPL];
+    load_logits<VPL, BF16>(a.logits, row, inside ? E : 0, from, a.pieces, x);
     if (bias != nullptr) {
-        float more[VPL];
         if (kPiece<VPL, BF16> >= 4 && a.fours) {
 #pragma unroll
             for (int i = 0; i + 3 < VPL; i += 4) {
                 const int e = expert<VPL, BF16>(from, i);
-                const float4 v = e < E ? *reinterpret_cast<const float4*>(bias + e)
-                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (e < E) v = *reinterpret_cast<const float4*>(bias + e);
                 more[i] = v.x, more[i + 1] = v.y, more[i + 2] = v.z, more[i + 3] = v.w;
             }
         } else {
@@ -175,11 +165,21 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
                 more[i] = e < E ? bias[e] : 0.0f;
             }
         }
+    }
+    const bool live = inside && (valid == nullptr || valid[t] != 0);
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const float v = x[i] + more[i];
-            key[i] = finite(x[i]) && finite(v) ? order_key(v) : 0u;
-        }
+    for (int i = 0; i < VPL; ++i)
+        if (!live) x[i] = __uint_as_float(0x7fc00000u);
+    float m = 0.0f, total = 1.0f;
+    if (!a.sigmoid && !a.normalize) {
+        float z[VPL], slope[VPL];
+        scores<LPT, VPL>(x, false, z, slope, total, m);
+    }
+    uint32_t key[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const float v = bias != nullptr ? x[i] + more[i] : x[i];
+        key[i] = finite(x[i]) && finite(v) ? order_key(v) : 0u;
     }
     if constexpr (VPL > kPiece<VPL, BF16>) {  // to consecutive experts, through LDS
 #pragma unroll
@@ -272,8 +272,9 @@ __device__ __forceinline__ void join_entries(const int (&e)[SEL], const float (&
 // Counts enter as their (exact) distance from the first expert's: adding a
 // constant to A changes nothing, and the difference keeps the digits that
 // A_e - sum A p would cancel.  16384 x 256 fp32, both parts: 12.7 us, 2.7 TB/s
-// (16.0 with each lane reading and writing a run of experts).  Entries that name one expert twice are added
-// up in their order by the first of them, so no order of atomics matters.
+// (16.0 with each lane reading and writing a run of experts).  Entries that
+// name one expert twice are added up in their order by the first of them, so
+// no order of atomics matters.
 template <int LPT, int VPL, bool BF16>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     RouteArgs a, const int32_t* topk_idx, const float* d_weights, const uint8_t* valid, float coef,
@@ -286,20 +287,42 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     const int slot = threadIdx.x / LPT;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + slot;
     const bool inside = t < a.num_tokens;
-    const bool live = inside && (valid == nullptr || valid[t] != 0);
     const int E = a.num_experts, k = a.num_topk;
     const Experts own = spread<LPT, VPL, BF16>(lane);
     const int64_t row = (inside ? t : 0) * a.stride;
 
-    float x[VPL], dx[VPL];
-    load_logits<VPL, BF16>(a.logits, row, live ? E : 0, own, a.pieces, x);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) dx[i] = 0.0f;
+    // What a token needs of its own is read first, none of it waiting for another
+    // load but the entries' logits.
     const bool loss = d_loss != nullptr;
-    const bool spread = d_weights != nullptr && !a.sigmoid && !a.normalize;
+    const bool spread_weights = d_weights != nullptr && !a.sigmoid && !a.normalize;
+    float x[VPL], dx[VPL];
+    load_logits<VPL, BF16>(a.logits, row, inside ? E : 0, own, a.pieces, x);
+    int e[kSel];
+    float xe[kSel], g[kSel];
+#pragma unroll
+    for (int q = 0; q < kSel; ++q) {
+        const int j = q * LPT + lane;
+        e[q] = -1;
+        g[q] = 0.0f;
+        if (d_weights != nullptr && inside && j < k) {
+            e[q] = topk_idx[t * k + j];
+            g[q] = d_weights[t * k + j];
+        }
+    }
+    const bool live = inside && (valid == nullptr || valid[t] != 0);
+#pragma unroll
+    for (int q = 0; q < kSel; ++q) {
+        if (!live || e[q] < 0 || e[q] >= E) e[q] = -1;
+        xe[q] = logit_at<BF16>(a.logits, row, e[q], e[q] >= 0);
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        if (!live) x[i] = __uint_as_float(0x7fc00000u);
+        dx[i] = 0.0f;
+    }
     float m = 0.0f, total = 1.0f;
     float p[VPL], slope[VPL];
-    if (loss || spread) {
+    if (loss || spread_weights) {
         scores<LPT, VPL>(x, a.sigmoid, p, slope, total, m);
         const float r = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
@@ -308,26 +331,26 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     if (loss) {
         const int64_t seq = (inside ? t : 0) / a.seq_len;
         const int32_t* c = counts + seq * E;
-        const float n = static_cast<float>(max(num_valid[seq], 1));
-        const float f = coef * static_cast<float>(E) /
-                        (static_cast<float>(a.num_seqs) * static_cast<float>(k)) * d_loss[0] / n / n;
         const int32_t c0 = c[0];
         int32_t ci[VPL];
         if (W >= 4 && a.fours) {
 #pragma unroll
             for (int i = 0; i + 3 < VPL; i += 4) {
                 const int at = expert<VPL, BF16>(own, i);
-                const int4 v = at < E ? *reinterpret_cast<const int4*>(c + at)
-                                      : make_int4(c0, c0, c0, c0);
+                int4 v = make_int4(0, 0, 0, 0);
+                if (at < E) v = *reinterpret_cast<const int4*>(c + at);
                 ci[i] = v.x, ci[i + 1] = v.y, ci[i + 2] = v.z, ci[i + 3] = v.w;
             }
         } else {
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
                 const int at = expert<VPL, BF16>(own, i);
-                ci[i] = at < E ? c[at] : c0;
+                ci[i] = at < E ? c[at] : 0;
             }
         }
+        const float n = static_cast<float>(max(num_valid[seq], 1));
+        const float f = coef * static_cast<float>(E) /
+                        (static_cast<float>(a.num_seqs) * static_cast<float>(k)) * d_loss[0] / n / n;
         float d[VPL], dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
@@ -339,21 +362,12 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
         for (int i = 0; i < VPL; ++i) dx[i] = f * (p[i] * (d[i] - dot) * slope[i]);
     }
     if (d_weights != nullptr) {
-        int e[kSel];
-        float xe[kSel], g[kSel], w[kSel], part[kSel];
+        float w[kSel], part[kSel];
         float gw = 0.0f;
 #pragma unroll
         for (int q = 0; q < kSel; ++q) {
-            const int j = q * LPT + lane;
-            e[q] = -1;
-            g[q] = 0.0f;
-            if (live && j < k) {
-                const int id = topk_idx[t * k + j];
-                if (id >= 0 && id < E) e[q] = id;
-            }
-            xe[q] = logit_at<BF16>(a.logits, row, e[q], e[q] >= 0);
             if (!finite(xe[q])) e[q] = -1;
-            if (e[q] >= 0) g[q] = a.scale * d_weights[t * k + j];
+            g[q] = e[q] >= 0 ? a.scale * g[q] : 0.0f;
         }
         entry_weights<LPT, kSel>(xe, a, m, total, w);
 #pragma unroll
@@ -367,7 +381,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
                 part[q] = w[q] * (a.normalize ? g[q] - gw : g[q]) * neg;
             }
         }
-        if (spread) {
+        if (spread_weights) {
 #pragma unroll
             for (int i = 0; i < VPL; ++i) dx[i] -= p[i] * gw;
         }

@@ -235,8 +235,8 @@ int ep_e4m3_encode(const float* in, uint8_t* out, int64_t n, void* stream);
  *
  * A logit that is not finite (NaN, -inf, +inf) switches its expert off for
  * that token: it has no probability, is never chosen, and gets gradient 0.
- * A token whose `valid` byte is 0 (padding) has every expert off and its
- * logits are not read.
+ * A token whose `valid` byte is 0 (padding) has every expert off, whatever its
+ * logits hold.
  *
  * Scores of token t: softmax (score = 0): z_e = exp(x_e); sigmoid (1):
  * z_e = 1 / (1 + exp(-x_e)).  Probabilities p_e = z_e / sum_i z_i over the
