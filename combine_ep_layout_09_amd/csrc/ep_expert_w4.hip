@@ -118,6 +118,20 @@ __device__ __forceinline__ void pair_chunks(u32x4& a, u32x4& b) {
     }
 }
 
+// Inclusive sum over the lanes of a wave, stopping at `top` (v at most top,
+// top below 2^31).
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v, uint32_t top) {
+    const auto step = [&](auto shifted) { v = min(v + static_cast<uint32_t>(shifted), top); };
+    const auto now = [&]() { return static_cast<int>(v); };
+    step(__builtin_amdgcn_update_dpp(0, now(), 0x111, 0xf, 0xf, false));  // row_shr 1
+    step(__builtin_amdgcn_update_dpp(0, now(), 0x112, 0xf, 0xf, false));
+    step(__builtin_amdgcn_update_dpp(0, now(), 0x114, 0xf, 0xf, false));
+    step(__builtin_amdgcn_update_dpp(0, now(), 0x118, 0xf, 0xf, false));
+    step(__builtin_amdgcn_update_dpp(0, now(), 0x142, 0xa, 0xf, false));  // row_bcast 15
+    step(__builtin_amdgcn_update_dpp(0, now(), 0x143, 0xc, 0xf, false));  // row_bcast 31
+    return v;
+}
+
 // The expert, rows and row tile that number pick(number of tiles) names: experts
 // with rows, in order, each with one tile per MC rows; expert -1 if there are
 // fewer.
@@ -146,15 +160,9 @@ __device__ __forceinline__ Found find_tile(const Args& a, Pick pick) {
         rows = min(rows + n, top_rows);
         tiles = min(tiles + tiles_of(n), top_tiles);
     }
-    uint32_t rows_to = rows, tiles_to = tiles;  // sums up to and with this lane
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-        const uint32_t r = __shfl_up(rows_to, d, kWave), q = __shfl_up(tiles_to, d, kWave);
-        if (lane >= d) {
-            rows_to = min(rows_to + r, top_rows);
-            tiles_to = min(tiles_to + q, top_tiles);
-        }
-    }
+    // sums up to and with this lane
+    const uint32_t rows_to = wave_scan(rows, top_rows);
+    const uint32_t tiles_to = wave_scan(tiles, top_tiles);
     const uint32_t want = pick(__builtin_amdgcn_readlane(tiles_to, kWave - 1));
     const uint64_t beyond = __ballot(tiles_to > want);
     Found f{-1, 0, 0, 0};
