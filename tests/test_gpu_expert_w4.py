@@ -348,3 +348,21 @@ def test_the_decode_workloads_layout():
     """The decode batch: 128 tokens, 256 experts, k 8, capacity 128, FP8 rows."""
     wl = workloads.make(2, H=256)
     Case(wl.topk_idx, wl.E, wl.cap, 256, 48, 1, True).check()
+
+
+@pytest.mark.parametrize("K,fmt", [(4640, 0), (8320, 0), (8704, 0), (8320, 1), (12288, 2)])
+@pytest.mark.parametrize("T", [9, 60, 200])
+def test_long_inputs(K, T, fmt):
+    """Inputs whose scales take several turns through LDS, words and not, with
+    few and many rows per expert."""
+    Case(uniform(T, 2, 1), 2, 0, K, 68, fmt, True).check()
+    Case(uniform(T, 2, 1), 2, 0, K, 131, fmt, False).check()
+
+
+def test_one_expert_takes_everything():
+    """All entries on one expert, every token on it twice: the other experts'
+    weights are NaN and unread."""
+    idx = np.full((150, 2), 5, np.int32)
+    for fmt in (0, 1):
+        Case(idx, 64, 0, 256, 100, fmt, True).check()
+        Case(idx, 64, 17, 256, 100, fmt, False).check()

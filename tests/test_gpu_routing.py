@@ -385,3 +385,29 @@ def test_prepared_calls():
     assert torch.equal(idx, i2) and torch.equal(w, w2) and torch.equal(d1, d2)
     for n in o:
         assert torch.equal(o[n], o2[n])
+
+
+def test_bool_padding_and_values_of_padded_rows():
+    """Padding as torch.bool; what a padded row's logits hold does not matter."""
+    c = Case(90, 128, 4, G=4, KG=2, score=1, pad=0.5, B=3)
+    idx, w = c.route()
+    o = c.balance(idx)
+    dw = torch.randn((90, 4), device=DEV)
+
+    def gradient(valid):
+        dx = torch.empty((90, 128), device=DEV)
+        ep.ep_route_backward(c.rt, c.logits, idx, dx, d_weights=dw, coef=0.1, counts=o["counts"],
+                             num_valid=o["num_valid"], d_loss=torch.ones(1, device=DEV),
+                             valid=valid)
+        return dx
+
+    d = gradient(c.d_valid)
+    off = c.d_valid == 0
+    c.logits[off] = float("nan")
+    c.logits[off, ::3] = float("inf")
+    c.d_valid = c.d_valid.bool()
+    i2, w2 = c.route()
+    o2 = c.balance(idx)
+    assert torch.equal(idx, i2) and torch.equal(w, w2) and torch.equal(d, gradient(c.d_valid))
+    assert all(torch.equal(o[n], o2[n]) for n in o)
+    assert (d[off] == 0).all() and (idx[off] == -1).all() and (w[off] == 0).all()
