@@ -90,14 +90,15 @@ class Routing(ctypes.Structure):
                 ("normalize", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
                 ("weight_scale", ctypes.c_float)]
 
+    _scores = {"softmax": 0, "sigmoid": 1, 0: 0, 1: 1}
+
     def __init__(self, num_tokens, num_experts, num_topk, num_groups=1, topk_groups=1,
                  score="softmax", normalize=True, num_seqs=1, weight_scale=1.0):
-        if isinstance(score, str):
-            if score not in ("softmax", "sigmoid"):
-                raise ValueError(f"score is {score!r}, expected 'softmax' or 'sigmoid'")
-            score = int(score == "sigmoid")
-        super().__init__(num_tokens, num_experts, num_topk, num_groups, topk_groups, score,
-                         int(normalize), num_seqs, weight_scale)
+        if score not in self._scores:
+            raise ValueError(f"score is {score!r}, expected 'softmax' or 'sigmoid'")
+        ctypes.Structure.__init__(self, num_tokens, num_experts, num_topk, num_groups,
+                                  topk_groups, self._scores[score], int(normalize), num_seqs,
+                                  weight_scale)
 
     def __repr__(self):
         return (f"Routing(T={self.num_tokens}, E={self.num_experts}, k={self.num_topk}, "
@@ -484,17 +485,22 @@ def _raw_stream(dev):
     return raw(dev)
 
 
+_gpus = None  # visible GPUs, once counted
+
+
 def _issue(name, fn, args, dev, stream):
     """The C call on device `dev`, on its current stream by default."""
-    torch = _torch()
+    global _gpus
+    if _gpus is None:
+        _gpus = _torch().cuda.device_count()
     if stream is None:
         handle = _raw_stream(dev)
     else:
         handle = stream if isinstance(stream, int) else stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if _gpus == 1 or _torch().cuda.current_device() == dev:
         code = fn(*args, handle)
     else:
-        with torch.cuda.device(dev):
+        with _torch().cuda.device(dev):
             code = fn(*args, handle)
     if code != EP_OK:
         raise EpError(name, code)
@@ -522,7 +528,7 @@ def _logits_args(rt, logits):
     else:
         raise TypeError(f"logits has dtype {logits.dtype}, expected float32 or bfloat16")
     T, E = rt.num_tokens, rt.num_experts
-    if logits.dim() != 2 or logits.shape[0] != T or logits.shape[1] != E:
+    if logits.shape != (T, E):
         raise ValueError(f"logits has shape {tuple(logits.shape)}, expected {(T, E)}")
     stride, inner = logits.stride()
     if inner != 1 and E > 1:
@@ -536,15 +542,18 @@ def _logits_args(rt, logits):
 
 def _valid_arg(rt, valid, dev):
     torch = _torch()
-    return _arg(valid, "valid", (torch.uint8, torch.bool), rt.num_tokens, dev, allow_none=True)
+    return _arg(valid, "valid", (torch.uint8, torch.bool), rt.num_tokens, dev)
 
 
 def _route_args(rt, logits, topk_idx, topk_weights, expert_bias, valid):
     torch = _torch()
     dev, lp, bf16, stride = _logits_args(rt, logits)
     n = rt.num_tokens * rt.num_topk
-    bp = _arg(expert_bias, "expert_bias", torch.float32, rt.num_experts, dev, allow_none=True)
-    vp = _valid_arg(rt, valid, dev)
+    bp = vp = None
+    if expert_bias is not None:
+        bp = _arg(expert_bias, "expert_bias", torch.float32, rt.num_experts, dev)
+    if valid is not None:
+        vp = _valid_arg(rt, valid, dev)
     ip = _arg(topk_idx, "topk_idx", torch.int32, n, dev)
     wp = _arg(topk_weights, "topk_weights", torch.float32, n, dev)
     return dev, (ctypes.byref(rt), lp, bf16, stride, bp, vp, ip, wp)
@@ -573,7 +582,7 @@ def _balance_args(rt, logits, topk_idx, coef, counts, mean_prob, num_valid, loss
     dev, lp, bf16, stride = _logits_args(rt, logits)
     T, E, B = rt.num_tokens, rt.num_experts, rt.num_seqs
     ip = _arg(topk_idx, "topk_idx", torch.int32, T * rt.num_topk, dev)
-    vp = _valid_arg(rt, valid, dev)
+    vp = None if valid is None else _valid_arg(rt, valid, dev)
     cp = _arg(counts, "counts", torch.int32, B * E, dev)
     mp = _arg(mean_prob, "mean_prob", torch.float32, B * E, dev)
     np_ = _arg(num_valid, "num_valid", torch.int32, B, dev)
@@ -616,7 +625,7 @@ def _route_backward_args(rt, logits, topk_idx, d_logits, d_weights, coef, counts
         raise ValueError("counts and num_valid are required with d_loss")
     ip = _arg(topk_idx, "topk_idx", torch.int32, n, dev, allow_none=True)
     gp = _arg(d_weights, "d_weights", torch.float32, n, dev, allow_none=True)
-    vp = _valid_arg(rt, valid, dev)
+    vp = None if valid is None else _valid_arg(rt, valid, dev)
     cp = _arg(counts, "counts", torch.int32, B * E, dev, allow_none=True)
     np_ = _arg(num_valid, "num_valid", torch.int32, B, dev, allow_none=True)
     sp = _arg(d_loss, "d_loss", torch.float32, 1, dev, allow_none=True)
