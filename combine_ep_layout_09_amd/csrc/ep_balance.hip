@@ -12,10 +12,10 @@
 // registers, its entries in an LDS histogram, and writes both as one row of
 // partial sums.  Second kernel: the rows are added in order, in fp64.  Up to
 // kOneGroup partial sums one workgroup does it, and the loss with them; above
-// that many workgroups, and a third kernel adds their parts of the loss.  No
-// sum depends on the order in which workgroups run.  16384 x 256 fp32 in four
-// sequences: 8, 4.8 and 1.8 us; with one workgroup for all 65536 partial sums the
-// call took 38 us, so 16.
+// that many, of which the last to finish adds their parts of the loss, in
+// order.  No sum depends on the order in which workgroups run.  16384 x 256 fp32
+// in four sequences: 8.6 and 6.3 us, the call 15.0, with a third kernel for the
+// parts 16.2; with one workgroup for all 65536 partial sums 38.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -28,15 +28,15 @@ namespace {
 using namespace route;
 
 constexpr int kSum = 1024;     // threads of the first kernel
-constexpr int kFinish = 1024;  // and of the others
-constexpr int64_t kMostGroups = 1024;  // of the second
+constexpr int kFinish = 1024;  // and of the second
+constexpr int64_t kMostGroups = kFinish;  // workgroups of the second: a thread adds each part
 constexpr int kRowsWanted = 256;
 constexpr int64_t kOneGroup = 16384;
 
 struct Geometry {
     int runs;        // runs of tokens per sequence
     int run_tokens;  // tokens per run
-    int64_t probs, hist, live, part, bytes;  // workspace offsets and size
+    int64_t probs, hist, live, part, done, bytes;  // workspace offsets and size
 };
 
 Geometry geometry(int T, int E, int B) {
@@ -55,7 +55,8 @@ Geometry geometry(int T, int E, int B) {
     g.hist = up(g.probs + rows * E * 4);
     g.live = up(g.hist + rows * E * 4);
     g.part = up(g.live + rows * 4);
-    g.bytes = up(g.part + kMostGroups * 8);
+    g.done = g.part + kMostGroups * 8;
+    g.bytes = up(g.done + 4);
     return g;
 }
 
@@ -63,7 +64,8 @@ template <int LPT, int VPL, bool BF16>
 __global__ __launch_bounds__(kSum) void balance_sum_kernel(RouteArgs a, const int32_t* topk_idx,
                                                            const uint8_t* valid, int runs,
                                                            int run_tokens, float* probs,
-                                                           int32_t* hist, int32_t* live_rows) {
+                                                           int32_t* hist, int32_t* live_rows,
+                                                           uint32_t* done) {
     constexpr int kTokens = kSum / LPT;
     constexpr int kWidth = LPT * VPL;
     constexpr int kSel = kMaxTopk > LPT ? kMaxTopk / LPT : 1;
@@ -136,6 +138,7 @@ __global__ __launch_bounds__(kSum) void balance_sum_kernel(RouteArgs a, const in
         hist[out + e] = counts[e];
     }
     if (threadIdx.x == 0) live_rows[blockIdx.x] = live_count;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *done = 0;  // for the second kernel
 }
 
 // Sum over the workgroup of one double per thread, in thread 0.
@@ -152,12 +155,13 @@ __device__ __forceinline__ double group_sum(double v, double* lds) {
 
 // Outputs are the (sequence, expert) pairs in order.  A workgroup takes `cols`
 // of them at a time (a power of two, 64 to kFinish), kFinish / cols threads
-// each adding every kFinish / cols-th row of partial sums.  One workgroup
-// alone has the whole loss; several write their parts.
+// each adding every kFinish / cols-th row of partial sums.  Every workgroup
+// writes its part of the loss; the one that is last to count itself in `done`
+// adds them in order.
 __global__ __launch_bounds__(kFinish) void balance_mean_kernel(
     int E, int cols, int runs, int64_t outputs, const float* probs, const int32_t* hist,
     const int32_t* live_rows, int32_t* counts, float* mean_prob, int32_t* num_valid, double* part,
-    double factor, float* loss) {
+    uint32_t* done, double factor, float* loss) {
     __shared__ double sum_s[kFinish];
     __shared__ int32_t sum_c[kFinish], sum_n[kFinish];
     const int col = threadIdx.x % cols, slice = threadIdx.x / cols, slices = kFinish / cols;
@@ -199,22 +203,22 @@ __global__ __launch_bounds__(kFinish) void balance_mean_kernel(
         }
     }
     __syncthreads();
-    const double p = group_sum(term, sum_s);
-    if (threadIdx.x == 0) {
-        if (gridDim.x == 1)
-            loss[0] = static_cast<float>(p * factor);
-        else
-            part[blockIdx.x] = p;
+    double p = group_sum(term, sum_s);
+    if (gridDim.x > 1) {
+        __shared__ bool last;
+        if (threadIdx.x == 0) {
+            __hip_atomic_store(&part[blockIdx.x], p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+                   gridDim.x - 1;
+        }
+        __syncthreads();
+        if (!last) return;
+        p = threadIdx.x < gridDim.x ? __hip_atomic_load(&part[threadIdx.x], __ATOMIC_RELAXED,
+                                                        __HIP_MEMORY_SCOPE_AGENT)
+                                    : 0.0;
+        p = group_sum(p, sum_s);
     }
-}
-
-__global__ __launch_bounds__(kFinish) void balance_loss_kernel(int64_t parts, const double* part,
-                                                               double factor, float* loss) {
-    __shared__ double red[kFinish / kWave];
-    double s = 0.0;
-    for (int64_t i = threadIdx.x; i < parts; i += kFinish) s += part[i];
-    s = group_sum(s, red);
-    if (threadIdx.x == 0) loss[0] = static_cast<float>(s * factor);
+    if (threadIdx.x == 0) loss[0] = static_cast<float>(p * factor);
 }
 
 template <int LPT, int VPL>
@@ -224,12 +228,13 @@ void launch_sum(const RouteArgs& a, const BalanceArgs& b, const Geometry& g, cha
     float* probs = reinterpret_cast<float*>(ws + g.probs);
     int32_t* hist = reinterpret_cast<int32_t*>(ws + g.hist);
     int32_t* live = reinterpret_cast<int32_t*>(ws + g.live);
+    uint32_t* done = reinterpret_cast<uint32_t*>(ws + g.done);
     if (a.bf16)
         hipLaunchKernelGGL((balance_sum_kernel<LPT, VPL, true>), grid, dim3(kSum), 0, stream, a,
-                           b.topk_idx, b.valid, g.runs, g.run_tokens, probs, hist, live);
+                           b.topk_idx, b.valid, g.runs, g.run_tokens, probs, hist, live, done);
     else
         hipLaunchKernelGGL((balance_sum_kernel<LPT, VPL, false>), grid, dim3(kSum), 0, stream, a,
-                           b.topk_idx, b.valid, g.runs, g.run_tokens, probs, hist, live);
+                           b.topk_idx, b.valid, g.runs, g.run_tokens, probs, hist, live, done);
 }
 
 }  // namespace
@@ -258,8 +263,8 @@ hipError_t launch_balance(const RouteArgs& a, const BalanceArgs& b, void* worksp
     }
     double* part = reinterpret_cast<double*>(ws + g.part);
     const int64_t outputs = static_cast<int64_t>(a.num_seqs) * a.num_experts;
-    // One workgroup and no third kernel up to kOneGroup partial sums; above
-    // that 64 outputs and 16 slices of rows per workgroup.
+    // One workgroup up to kOneGroup partial sums; above that 64 outputs and 16
+    // slices of rows per workgroup.
     const bool one = outputs * g.runs <= kOneGroup;
     int cols = 64;
     while (one && cols < kFinish && cols < outputs) cols *= 2;
@@ -271,10 +276,7 @@ hipError_t launch_balance(const RouteArgs& a, const BalanceArgs& b, void* worksp
                        reinterpret_cast<float*>(ws + g.probs),
                        reinterpret_cast<int32_t*>(ws + g.hist),
                        reinterpret_cast<int32_t*>(ws + g.live), b.counts, b.mean_prob, b.num_valid,
-                       part, factor, b.loss);
-    if (groups > 1)
-        hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(kFinish), 0, stream, groups, part,
-                           factor, b.loss);
+                       part, reinterpret_cast<uint32_t*>(ws + g.done), factor, b.loss);
     return hipGetLastError();
 }
 
