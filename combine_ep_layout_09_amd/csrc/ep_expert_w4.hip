@@ -89,7 +89,8 @@ __device__ __forceinline__ bf16x8 rows8(uint32_t lo, uint32_t hi) {
 }
 
 // Bounded view of `bytes` bytes at p: loads past its end give 0 and touch
-// nothing.  p and bytes are the same in every lane, and said to be: a view in
+// nothing.  A lane's own offset alone has to say so, since the step's offset,
+// the same in every lane, need not count in that check.  p and bytes are the same in every lane, and said to be: a view in
 // vector registers is loaded through in a loop over its values.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t view(const void* p, uint32_t bytes) {
     const uint64_t v = reinterpret_cast<uint64_t>(p);

@@ -121,12 +121,13 @@ __device__ __forceinline__ void limit_groups(uint32_t (&key)[VPL], uint32_t* key
 
 // One launch, a token per LPT lanes; logits are read in pieces that lie
 // consecutively over a token's lanes (with each lane reading its own run of
-// experts, 16384 x 256 fp32 took 16.6 us, so 11.1: 1.6 TB/s, about half of it
-// instructions, the other half the one read before them).  The k best keys are taken one after the
-// other: every lane keeps the best of its own keys, a reduction over the
-// token's lanes finds the best of all, and the lowest lane that holds it gives
-// up its first expert with that key.  Entry j goes to lane j % LPT through LDS; the weights are then computed with one
-// lane per entry from the logits themselves (the bias only steers the choice).
+// experts, 16384 x 256 fp32 took 16.6 us, so 11.7: 1.5 TB/s, about half of it
+// instructions, the other half the one read before them).  The k best keys are
+// taken one after the other: every lane keeps the best of its own keys, a
+// reduction over the token's lanes finds the best of all, and the lowest lane
+// that holds it gives up its first expert with that key.  Entry j goes to lane
+// j % LPT through LDS; the weights are then computed with one lane per entry
+// from the logits themselves (the bias only steers the choice).
 template <int LPT, int VPL, bool BF16>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const float* bias,
                                                          const uint8_t* valid, int32_t* topk_idx,

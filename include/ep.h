@@ -276,7 +276,8 @@ int ep_route(const ep_routing* rt, const void* logits, int logits_bf16, int64_t 
              float* topk_weights, void* stream);
 
 /* Bytes of device workspace ep_balance_loss needs, or -1 if the problem is
- * invalid.  Needs no initialisation; scratch after the call. */
+ * invalid.  Needs no initialisation; scratch after the call.  Calls that may
+ * run at the same time, replayed graphs among them, need one each. */
 int64_t ep_balance_workspace_bytes(const ep_routing* rt);
 
 /* Balance loss of a routing:
@@ -338,7 +339,8 @@ typedef struct ep_expert_w4_t {
  *   rows        [R, K], bf16 or E4M3FN bytes, in the receive-row layout (ep_dispatch's
  *               recv_x, or another ep_expert_w4's out).
  *   row_scales  [R, K / 128] fp32 (in_format 1) or UE8M0 bytes (2); ignored for 0.
- *   layout      as written by ep_layout for the same problem (count and offset are read).
+ *   layout      as written by ep_layout for the same problem (contiguous rows start where the
+ *               counts before them end, as offset says).
  *   codes       uint8 [E, N or 2N, K / 2]: channel 2i in the low, 2i + 1 in the high four
  *               bits of byte i; bit 3 the sign.
  *   scales      uint8 [E, N or 2N, K / 32]: value 2^(byte - 127); 255 is NaN.  A weight of

@@ -257,6 +257,43 @@ def test_large_batches():
     Case(3001, 256, 8, G=8, KG=4, score=1, bias=True, pad=0.1).all()
 
 
+def test_loss_joined_by_many_workgroups():
+    """More partial sums than one workgroup adds.  One workspace serves problems of
+    different sizes in turn, eager and replayed; equal calls give equal bits."""
+    c = Case(5000, 256, 8, B=4, pad=0.1)
+    small = Case(60, 16, 2, B=3)
+    idx, w = c.route()
+    want = c.balance(idx)
+    c.check_balance(want, idx.cpu().numpy())
+    idx_s, _ = small.route()
+    want_s = small.balance(idx_s)
+    n = ep.ep_balance_workspace_bytes(c.rt)
+    space = torch.full((n,), 0xA5, dtype=torch.uint8, device=DEV)
+    got = {name: torch.empty_like(v) for name, v in want.items()}
+    got_s = {name: torch.empty_like(v) for name, v in want_s.items()}
+
+    def both():
+        ep.ep_balance_loss(c.rt, c.logits, idx, 0.25, workspace=space, valid=c.d_valid, **got)
+        ep.ep_balance_loss(small.rt, small.logits, idx_s, 0.25, workspace=space, **got_s)
+
+    both()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        both()
+    for rep in range(6):
+        for t in (*got.values(), *got_s.values()):
+            t.zero_()
+        if rep % 2:
+            both()
+        else:
+            g.replay()
+        torch.cuda.synchronize()
+        for name in want:
+            assert torch.equal(got[name], want[name]), (rep, name)
+            assert torch.equal(got_s[name], want_s[name]), (rep, name)
+
+
 def test_no_tokens():
     c = Case(0, 64, 6, B=3)
     idx, w = c.route()
