@@ -119,6 +119,21 @@ __device__ __forceinline__ void limit_groups(uint32_t (&key)[VPL], uint32_t* key
     }
 }
 
+// A lane's run of VPL keys in LDS.
+template <int VPL>
+__device__ __forceinline__ void read_run(const uint32_t* from, uint32_t (&to)[VPL]) {
+    if constexpr (VPL >= 4) {
+#pragma unroll
+        for (int i = 0; i < VPL; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(from + i);
+            to[i] = v.x, to[i + 1] = v.y, to[i + 2] = v.z, to[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) to[i] = from[i];
+    }
+}
+
 // One launch, a token per LPT lanes; logits are read in pieces that lie
 // consecutively over a token's lanes (with each lane reading its own run of
 // experts, 16384 x 256 fp32 took 16.6 us, so 11.7: 1.5 TB/s, about half of it
@@ -193,30 +208,66 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
         for (int i = 0; i < VPL; ++i) key[i] = lds_keys[slot][lane * kRun + i];
         wave_sync();
     }
-    if (a.num_groups > 1) limit_groups<LPT, VPL>(key, lds_keys[slot], lds_score[slot], lane, a);
+    bool stored = VPL > kPiece<VPL, BF16>;  // lanes' runs of keys are in LDS
+    if (a.num_groups > 1) {
+        limit_groups<LPT, VPL>(key, lds_keys[slot], lds_score[slot], lane, a);
+        stored = stored && LPT == 16 && a.group_lanes > 0;
+    }
+    if (!stored) {
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) lds_keys[slot][lane * kRun + i] = key[i];
+        wave_sync();
+    }
 
-    const auto largest = [&]() {
-        uint32_t v = 0;
+    // The k best pairs of (key, lane); lane j keeps pair j.  The lane that gave a
+    // pair goes on to its largest key below that, by unsigned distance: keys at or
+    // above wrap round to more than the distance of 0.
+    uint32_t best = 0;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) v = max(v, key[i]);
-        return v;
-    };
-    uint32_t best = largest();
-    for (int j = 0; j < a.num_topk; ++j) {
-        const uint32_t top = token_max<LPT>(best);
-        if (lane == token_first<LPT>(best == top, wave_lane)) {
-            int at = -1;
-            bool found = false;
+    for (int i = 0; i < VPL; ++i) best = max(best, key[i]);
+    uint32_t top[kSel];
+    int owner[kSel];
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const bool hit = key[i] == top && !found;
-                found |= hit;
-                key[i] = hit ? 0u : key[i];
-                at = hit ? i : at;
+    for (int q = 0; q < kSel; ++q) {
+        top[q] = 0;
+        owner[q] = 0;
+        for (int j = 0; j < LPT && q * LPT + j < a.num_topk; ++j) {
+            const uint32_t now = token_max<LPT>(best);
+            const int first = token_first<LPT>(best == now, wave_lane);
+            top[q] = lane == j ? now : top[q];
+            owner[q] = lane == j ? first : owner[q];
+            if (lane == first && now != 0) {
+                const uint32_t below = best - 1;
+                uint32_t gap = below;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) gap = min(gap, below - key[i]);
+                best = below - gap;
             }
-            lds_chosen[slot][j] = top ? lane * VPL + at : -1;
-            best = largest();
         }
+    }
+    // A pair stands for every expert of its lane with that key, in their order:
+    // entries are the pairs' experts one after the other, up to k.
+    int before = 0;  // entries of the pairs before this lane's
+#pragma unroll
+    for (int q = 0; q < kSel; ++q) {
+        const bool there = q * LPT + lane < a.num_topk;
+        uint32_t mask = 0;
+        if (there && top[q] != 0) {
+            uint32_t held[VPL];
+            read_run<VPL>(&lds_keys[slot][owner[q] * kRun], held);
+#pragma unroll
+            for (int i = VPL - 1; i >= 0; --i) mask = mask + mask + (held[i] == top[q] ? 1 : 0);
+        }
+        const int entries = there ? max(__popc(mask), 1) : 0;
+        const int to = before + token_prefix<LPT>(entries);
+        if (there) {
+            int at = to - entries;
+            if (mask == 0 && at < a.num_topk) lds_chosen[slot][at] = -1;
+            for (; mask != 0 && at < a.num_topk; ++at, mask &= mask - 1)
+                lds_chosen[slot][at] = owner[q] * VPL + __ffs(static_cast<int>(mask)) - 1;
+        }
+        if (q + 1 < kSel) before = static_cast<int>(token_bcast<LPT, LPT - 1>(to));
     }
     wave_sync();
     int sel[kSel];

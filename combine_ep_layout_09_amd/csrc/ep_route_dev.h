@@ -118,6 +118,20 @@ __device__ __forceinline__ uint32_t token_bcast(uint32_t v) {
         return row_bcast<J>(v);
 }
 
+// Sum over the lanes of this lane's token up to and with this one.
+template <int LPT>
+__device__ __forceinline__ int token_prefix(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr 1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    if constexpr (LPT == 64) {
+        v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast 15
+        v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast 31
+    }
+    return v;
+}
+
 // Lowest lane of this lane's token for which `p` holds (p holds for one at
 // least).
 template <int LPT>
