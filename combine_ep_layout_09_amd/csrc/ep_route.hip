@@ -195,17 +195,17 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const float v = bias != nullptr ? x[i] + more[i] : x[i];
-        key[i] = finite(x[i]) && finite(v) ? order_key(v) : 0u;
+        key[i] = finite(v) ? order_key(v) : 0u;  // not if x is not
     }
     if constexpr (VPL > kPiece<VPL, BF16>) {  // to consecutive experts, through LDS
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
+        for (int i = 0; i < VPL; i += 4) {  // kPiece is 4 or 8 here
             const int e = expert<VPL, BF16>(from, i);
-            lds_keys[slot][e / VPL * kRun + e % VPL] = key[i];
+            *reinterpret_cast<uint4*>(&lds_keys[slot][e / VPL * kRun + e % VPL]) =
+                make_uint4(key[i], key[i + 1], key[i + 2], key[i + 3]);
         }
         wave_sync();
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) key[i] = lds_keys[slot][lane * kRun + i];
+        read_run<VPL>(&lds_keys[slot][lane * kRun], key);
         wave_sync();
     }
     bool stored = VPL > kPiece<VPL, BF16>;  // lanes' runs of keys are in LDS

@@ -143,7 +143,7 @@ __device__ __forceinline__ int token_first(bool p, int wave_lane) {
 }
 
 __device__ __forceinline__ bool finite(float x) {
-    return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u;
+    return __builtin_isfinite(x);
 }
 
 // Order-preserving map of a finite float to an integer > 0; -0 and +0 agree.
