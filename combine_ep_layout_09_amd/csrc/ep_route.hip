@@ -41,8 +41,8 @@ __device__ __forceinline__ int better_lanes(double s, int lane) {
         const uint64_t lo = row_ror<N>(static_cast<uint32_t>(u));
         const uint64_t hi = row_ror<N>(static_cast<uint32_t>(u >> 32));
         const double o = __builtin_bit_cast(double, hi << 32 | lo);
-        const int from = (lane - N) & 15;  // row_ror moves lane i - N to lane i
-        const bool better = o > s || (o == s && from < lane);
+        // row_ror moves lane i - N to lane i, so it is a lower one from lane N on
+        const bool better = o > s || (o == s && lane >= N);
         return (better ? 1 : 0) + better_lanes<S, N + (1 << S)>(s, lane);
     }
 }
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
     const int64_t row = (inside ? t : 0) * a.stride;
 
     const Experts from = spread<LPT, VPL, BF16>(lane);
-    float x[VPL], more[VPL];
+    float x[VPL], more[VPL] = {};
     load_logits<VPL, BF16>(a.logits, row, inside ? E : 0, from, a.pieces, x);
     if (bias != nullptr) {
         if (kPiece<VPL, BF16> >= 4 && a.fours) {
@@ -183,9 +183,6 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
         }
     }
     const bool live = inside && (valid == nullptr || valid[t] != 0);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-        if (!live) x[i] = __uint_as_float(0x7fc00000u);
     float m = 0.0f, total = 1.0f;
     if (!a.sigmoid && !a.normalize) {
         float z[VPL], slope[VPL];
@@ -194,7 +191,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
     uint32_t key[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        const float v = bias != nullptr ? x[i] + more[i] : x[i];
+        const float v = x[i] + more[i];
         key[i] = finite(v) ? order_key(v) : 0u;  // not if x is not
     }
     if constexpr (VPL > kPiece<VPL, BF16>) {  // to consecutive experts, through LDS
@@ -226,12 +223,14 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
     uint32_t best = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) best = max(best, key[i]);
+    if (!live) best = 0;
     uint32_t top[kSel];
     int owner[kSel];
 #pragma unroll
     for (int q = 0; q < kSel; ++q) {
         top[q] = 0;
         owner[q] = 0;
+#pragma unroll 1
         for (int j = 0; j < LPT && q * LPT + j < a.num_topk; ++j) {
             const uint32_t now = token_max<LPT>(best);
             const int first = token_first<LPT>(best == now, wave_lane);
@@ -251,15 +250,16 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
     int before = 0;  // entries of the pairs before this lane's
 #pragma unroll
     for (int q = 0; q < kSel; ++q) {
+        if (q > 0 && q * LPT >= a.num_topk) continue;
         const bool there = q * LPT + lane < a.num_topk;
         uint32_t mask = 0;
         if (there && top[q] != 0) {
             uint32_t held[VPL];
             read_run<VPL>(&lds_keys[slot][owner[q] * kRun], held);
 #pragma unroll
-            for (int i = VPL - 1; i >= 0; --i) mask = mask + mask + (held[i] == top[q] ? 1 : 0);
+            for (int i = 0; i < VPL; ++i) mask |= held[i] == top[q] ? 1u << i : 0u;
         }
-        const int entries = there ? max(__popc(mask), 1) : 0;
+        const int entries = there ? (mask == 0 ? 1 : __popc(mask)) : 0;
         const int to = before + token_prefix<LPT>(entries);
         if (there) {
             int at = to - entries;

@@ -23,14 +23,14 @@ constexpr int kThreads = 256;
 template <int N>
 __device__ __forceinline__ uint32_t row_ror(uint32_t v) {
     return static_cast<uint32_t>(
-        __builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x120 + N, 0xf, 0xf, false));
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x120 + N, 0xf, 0xf, true));
 }
 
 // Value of lane N of each row of 16 lanes, in every lane of it.
 template <int N>
 __device__ __forceinline__ uint32_t row_bcast(uint32_t v) {
     return static_cast<uint32_t>(
-        __builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x150 + N, 0xf, 0xf, false));
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x150 + N, 0xf, 0xf, true));
 }
 
 // All lanes of an aligned run of 2^S: after S - 1, run it with S.  Lane i meets
@@ -42,7 +42,7 @@ __device__ __forceinline__ uint32_t other_half(uint32_t v) {
                          : S == 3 ? 0x141   // mirrored in 8 lanes
                                   : 0x140;  // mirrored in 16 lanes
     return static_cast<uint32_t>(
-        __builtin_amdgcn_update_dpp(0, static_cast<int>(v), ctrl, 0xf, 0xf, false));
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(v), ctrl, 0xf, 0xf, true));
 }
 
 // LDS that one wave writes and reads needs no barrier, but the compiler has to
@@ -291,23 +291,25 @@ __device__ __forceinline__ void scores(const float (&x)[VPL], bool sigmoid, floa
     for (int i = 0; i < VPL; ++i)
         if (finite(x[i])) m = fmaxf(m, x[i]);
     m = token_fmax<LPT>(m);
+    // no branch per expert: what an expert that is off computes is dropped
+    if (sigmoid && m > kSmallScore) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const Sigmoids g = sigmoids(x[i]);
+            z[i] = finite(x[i]) ? g.pos : 0.0f;
+            slope[i] = finite(x[i]) ? g.neg : 1.0f;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const float v = exp_neg(x[i] - m);
+            z[i] = finite(x[i]) ? v : 0.0f;
+            slope[i] = 1.0f;  // below -20 sigma(-x) rounds to 1
+        }
+    }
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        z[i] = 0.0f;
-        slope[i] = 1.0f;
-        if (finite(x[i])) {
-            if (sigmoid && m > kSmallScore) {
-                const Sigmoids g = sigmoids(x[i]);
-                z[i] = g.pos;
-                slope[i] = g.neg;
-            } else {
-                z[i] = exp_neg(x[i] - m);
-                // below -20 sigma(-x) rounds to 1
-            }
-        }
-        s += z[i];
-    }
+    for (int i = 0; i < VPL; ++i) s += z[i];
     total = token_sum<LPT>(s);
 }
 
