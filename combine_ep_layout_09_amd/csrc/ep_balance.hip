@@ -108,11 +108,8 @@ __global__ __launch_bounds__(kSum) void balance_sum_kernel(RouteArgs a, const in
 #pragma unroll
         for (int q = 0; q < kSel; ++q)
             if (live && ids[q] >= 0 && ids[q] < E) atomicAdd(&counts[ids[q]], 1);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (!live) x[i] = __uint_as_float(0x7fc00000u);
         scores<LPT, VPL>(x, a.sigmoid, z, slope, total, top);
-        const float r = total > 0.0f ? 1.0f / total : 0.0f;
+        const float r = live && total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) acc[i] += z[i] * r;
     }

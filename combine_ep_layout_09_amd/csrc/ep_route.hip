@@ -368,10 +368,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
         xe[q] = logit_at<BF16>(a.logits, row, e[q], e[q] >= 0);
     }
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        if (!live) x[i] = __uint_as_float(0x7fc00000u);
-        dx[i] = 0.0f;
-    }
+    for (int i = 0; i < VPL; ++i) dx[i] = 0.0f;
     float m = 0.0f, total = 1.0f;
     float p[VPL], slope[VPL];
     if (loss || spread_weights) {
@@ -456,7 +453,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     if (inside) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            if (!finite(x[i])) dx[i] = 0.0f;
+            if (!(live && finite(x[i]))) dx[i] = 0.0f;
         store_logits<VPL, BF16>(d_logits, t * E, E, own, a.out_pieces, dx);
     }
 }
