@@ -66,11 +66,31 @@ __device__ __forceinline__ bool lane_group_kept(const uint32_t (&key)[VPL], int 
     return better_lanes<S, 1 << S>(s, lane) < a.topk_groups;
 }
 
+// Words of LDS for a lane's run of VPL keys: 16-byte accesses of 8 lanes meet 32
+// banks.
+template <int VPL>
+constexpr int kRun = VPL >= 8 ? VPL + 4 : VPL;
+
+// A lane's run of VPL keys in LDS.
+template <int VPL>
+__device__ __forceinline__ void read_run(const uint32_t* from, uint32_t (&to)[VPL]) {
+    if constexpr (VPL >= 4) {
+#pragma unroll
+        for (int i = 0; i < VPL; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(from + i);
+            to[i] = v.x, to[i + 1] = v.y, to[i + 2] = v.z, to[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) to[i] = from[i];
+    }
+}
+
 // Keys of experts outside the token's best topk_groups groups become 0 (off).
 // A group is kept if fewer than topk_groups groups are better; equal scores go
 // to the lower index.  Groups that are 1, 2, 4 or 8 whole lanes of a 16-lane
-// token are handled in registers; for others the keys pass through LDS, where
-// lane g scores groups g, g + LPT, ....
+// token are handled in registers; others in LDS, which has the keys in runs:
+// lane g scores groups g, g + LPT, ..., and switches off those that are not kept.
 template <int LPT, int VPL>
 __device__ __forceinline__ void limit_groups(uint32_t (&key)[VPL], uint32_t* keys, double* score,
                                              int lane, const RouteArgs& a) {
@@ -89,69 +109,47 @@ __device__ __forceinline__ void limit_groups(uint32_t (&key)[VPL], uint32_t* key
         for (int i = 0; i < VPL; ++i) key[i] = kept ? key[i] : 0u;
         return;
     }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-        if (lane * VPL + i < a.num_experts) keys[lane * VPL + i] = key[i];
-    wave_sync();
+    const auto key_of = [&](int e) -> uint32_t& { return keys[e / VPL * kRun<VPL> + e % VPL]; };
     for (int g = lane; g < a.num_groups; g += LPT) {
         uint32_t m1 = 0, m2 = 0;
         for (int i = 0; i < gs; ++i) {
-            const uint32_t k = keys[g * gs + i];
+            const uint32_t k = key_of(g * gs + i);
             m2 = max(m2, min(m1, k));
             m1 = max(m1, k);
         }
         score[g] = group_score(m1, m2, gs == 1);
     }
     wave_sync();
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = lane * VPL + i;
-        if (e < a.num_experts) {
-            const int g = e / gs;
-            const double s = score[g];
-            int better = 0;
-            for (int h = 0; h < a.num_groups; ++h) {
-                const double o = score[h];
-                better += (o > s || (o == s && h < g)) ? 1 : 0;
-            }
-            if (better >= a.topk_groups) key[i] = 0;
+    for (int g = lane; g < a.num_groups; g += LPT) {
+        const double s = score[g];
+        int better = 0;
+        for (int h = 0; h < a.num_groups; ++h) {
+            const double o = score[h];
+            better += (o > s || (o == s && h < g)) ? 1 : 0;
         }
+        if (better >= a.topk_groups)
+            for (int i = 0; i < gs; ++i) key_of(g * gs + i) = 0;
     }
-}
-
-// A lane's run of VPL keys in LDS.
-template <int VPL>
-__device__ __forceinline__ void read_run(const uint32_t* from, uint32_t (&to)[VPL]) {
-    if constexpr (VPL >= 4) {
-#pragma unroll
-        for (int i = 0; i < VPL; i += 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(from + i);
-            to[i] = v.x, to[i + 1] = v.y, to[i + 2] = v.z, to[i + 3] = v.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) to[i] = from[i];
-    }
+    wave_sync();
+    read_run<VPL>(&keys[lane * kRun<VPL>], key);
 }
 
 // One launch, a token per LPT lanes; logits are read in pieces that lie
 // consecutively over a token's lanes (with each lane reading its own run of
-// experts, 16384 x 256 fp32 took 16.6 us, so 11.7: 1.5 TB/s, about half of it
-// instructions, the other half the one read before them).  The k best keys are
-// taken one after the other: every lane keeps the best of its own keys, a
-// reduction over the token's lanes finds the best of all, and the lowest lane
-// that holds it gives up its first expert with that key.  Entry j goes to lane
-// j % LPT through LDS; the weights are then computed with one lane per entry
-// from the logits themselves (the bias only steers the choice).
+// experts, 16384 x 256 fp32 took 16.6 us, so 11.1).  The k best keys are taken
+// one after the other: every lane keeps the best of its own keys, a reduction
+// over the token's lanes finds the best of all, and the lowest lane that holds it
+// goes on to its next.  Entry j goes to lane j % LPT through LDS; the weights are
+// then computed with one lane per entry from the logits themselves (the bias only
+// steers the choice).  16384 x 256 fp32, 4 of 8 groups: 9.9 us, 1.7 TB/s; 700
+// instructions per wave are a half of it, the read before them the other.
 template <int LPT, int VPL, bool BF16>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const float* bias,
                                                          const uint8_t* valid, int32_t* topk_idx,
                                                          float* topk_weights) {
     constexpr int kTokens = kThreads / LPT;
     constexpr int kSel = kMaxTopk > LPT ? kMaxTopk / LPT : 1;
-    // runs of VPL experts, padded so that 16-byte accesses of 8 lanes meet 32 banks
-    constexpr int kRun = VPL >= 8 ? VPL + 4 : VPL;
-    __shared__ __attribute__((aligned(16))) uint32_t lds_keys[kTokens][LPT * kRun];
+    __shared__ __attribute__((aligned(16))) uint32_t lds_keys[kTokens][LPT * kRun<VPL>];
     __shared__ double lds_score[kTokens][kMaxGroups];
     __shared__ int lds_chosen[kTokens][kMaxTopk];
     const int lane = threadIdx.x % LPT;
@@ -198,28 +196,24 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
 #pragma unroll
         for (int i = 0; i < VPL; i += 4) {  // kPiece is 4 or 8 here
             const int e = expert<VPL, BF16>(from, i);
-            *reinterpret_cast<uint4*>(&lds_keys[slot][e / VPL * kRun + e % VPL]) =
+            *reinterpret_cast<uint4*>(&lds_keys[slot][e / VPL * kRun<VPL> + e % VPL]) =
                 make_uint4(key[i], key[i + 1], key[i + 2], key[i + 3]);
         }
         wave_sync();
-        read_run<VPL>(&lds_keys[slot][lane * kRun], key);
-        wave_sync();
-    }
-    bool stored = VPL > kPiece<VPL, BF16>;  // lanes' runs of keys are in LDS
-    if (a.num_groups > 1) {
-        limit_groups<LPT, VPL>(key, lds_keys[slot], lds_score[slot], lane, a);
-        stored = stored && LPT == 16 && a.group_lanes > 0;
-    }
-    if (!stored) {
-        wave_sync();
+        read_run<VPL>(&lds_keys[slot][lane * kRun<VPL>], key);
+    } else {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) lds_keys[slot][lane * kRun + i] = key[i];
+        for (int i = 0; i < VPL; ++i) lds_keys[slot][lane * kRun<VPL> + i] = key[i];
         wave_sync();
     }
+    if (a.num_groups > 1) limit_groups<LPT, VPL>(key, lds_keys[slot], lds_score[slot], lane, a);
 
     // The k best pairs of (key, lane); lane j keeps pair j.  The lane that gave a
-    // pair goes on to its largest key below that, by unsigned distance: keys at or
-    // above wrap round to more than the distance of 0.
+    // pair goes on to its largest key below that.  It finds it by unsigned
+    // distance (keys at or above wrap round to more than the distance of 0), or
+    // with 16 keys the token's lanes find it, one key each, from LDS (16384 tokens
+    // of 256 experts: 7.8 us against 8.4; of 64, 4 keys a lane: 4.8 against 4.6).
+    // Lanes of groups that are off still have keys in LDS, but are never first.
     uint32_t best = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) best = max(best, key[i]);
@@ -236,7 +230,11 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
             const int first = token_first<LPT>(best == now, wave_lane);
             top[q] = lane == j ? now : top[q];
             owner[q] = lane == j ? first : owner[q];
-            if (lane == first && now != 0) {
+            if constexpr (VPL == 16) {
+                const uint32_t k = lane < VPL ? lds_keys[slot][first * kRun<VPL> + lane] : 0u;
+                const uint32_t next = token_max<LPT>(k < now ? k : 0u);
+                best = lane == first ? next : best;
+            } else if (lane == first && now != 0) {
                 const uint32_t below = best - 1;
                 uint32_t gap = below;
 #pragma unroll
@@ -255,7 +253,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
         uint32_t mask = 0;
         if (there && top[q] != 0) {
             uint32_t held[VPL];
-            read_run<VPL>(&lds_keys[slot][owner[q] * kRun], held);
+            read_run<VPL>(&lds_keys[slot][owner[q] * kRun<VPL>], held);
 #pragma unroll
             for (int i = 0; i < VPL; ++i) mask |= held[i] == top[q] ? 1u << i : 0u;
         }
