@@ -148,7 +148,7 @@ ep::RouteArgs route_args(const ep_routing& rt, const void* logits, int bf16, int
     a.sigmoid = rt.score == 1;
     a.normalize = rt.normalize == 1;
     const int el = bf16 ? 2 : 4;
-    const ep::TokenShape shape = ep::token_shape(rt.num_experts);
+    const ep::TokenShape shape = ep::token_shape(rt.num_experts, ep::kSixteenLanes);
     const int vpl = shape.vpl;
     const int group = rt.num_experts / rt.num_groups;
     const int lanes = group / vpl;

@@ -30,6 +30,9 @@ using namespace route;
 constexpr int kSum = 1024;     // threads of the first kernel
 constexpr int kFinish = 1024;  // and of the second
 constexpr int64_t kMostGroups = kFinish;  // workgroups of the second: a thread adds each part
+// Experts up to which 16 lanes take a token: at 512, where a lane would hold 32,
+// 16000 tokens take 24.7 us with 16 lanes, 23.5 with 64, 256 tokens 12.5 and 9.9.
+constexpr int kSixteen = 256;
 constexpr int kRowsWanted = 256;
 constexpr int64_t kOneGroup = 16384;
 
@@ -42,7 +45,7 @@ struct Geometry {
 Geometry geometry(int T, int E, int B) {
     Geometry g;
     const int64_t len = T / B;
-    const int64_t pass = kSum / token_shape(E).lpt;  // tokens of a workgroup's pass
+    const int64_t pass = kSum / token_shape(E, kSixteen).lpt;  // tokens of a workgroup's pass
     int64_t runs = (kRowsWanted + B - 1) / B;
     const int64_t most = (len + pass - 1) / pass;
     if (runs > most) runs = most;
@@ -244,7 +247,7 @@ hipError_t launch_balance(const RouteArgs& a, const BalanceArgs& b, void* worksp
                           hipStream_t stream) {
     const Geometry g = geometry(a.num_tokens, a.num_experts, a.num_seqs);
     char* ws = static_cast<char*>(workspace);
-    const TokenShape s = token_shape(a.num_experts);
+    const TokenShape s = token_shape(a.num_experts, kSixteen);
     if (s.lpt == 16) {
         switch (s.vpl) {
             case 1: launch_sum<16, 1>(a, b, g, ws, stream); break;

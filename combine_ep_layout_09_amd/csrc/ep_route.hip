@@ -90,7 +90,9 @@ __device__ __forceinline__ void read_run(const uint32_t* from, uint32_t (&to)[VP
 // A group is kept if fewer than topk_groups groups are better; equal scores go
 // to the lower index.  Groups that are 1, 2, 4 or 8 whole lanes of a 16-lane
 // token are handled in registers; others in LDS, which has the keys in runs:
-// lane g scores groups g, g + LPT, ..., and switches off those that are not kept.
+// `split` lanes take a group each, score it, and switch it off if it is not kept:
+// one lane, or with 64 lanes a token a power of two (1024 experts in 8 groups,
+// 16000 tokens: 27 us, with one lane each 60).
 template <int LPT, int VPL>
 __device__ __forceinline__ void limit_groups(uint32_t (&key)[VPL], uint32_t* keys, double* score,
                                              int lane, const RouteArgs& a) {
@@ -110,17 +112,24 @@ __device__ __forceinline__ void limit_groups(uint32_t (&key)[VPL], uint32_t* key
         return;
     }
     const auto key_of = [&](int e) -> uint32_t& { return keys[e / VPL * kRun<VPL> + e % VPL]; };
-    for (int g = lane; g < a.num_groups; g += LPT) {
+    int split = 1;
+    while (LPT == 64 && split < 16 && 2 * split * a.num_groups <= LPT) split *= 2;
+    const int part = lane % split, step = LPT / split;
+    for (int g = lane / split; g < a.num_groups; g += step) {
         uint32_t m1 = 0, m2 = 0;
-        for (int i = 0; i < gs; ++i) {
+        for (int i = part; i < gs; i += split) {
             const uint32_t k = key_of(g * gs + i);
             m2 = max(m2, min(m1, k));
             m1 = max(m1, k);
         }
+        if (split >= 2) merge_half<1>(m1, m2);
+        if (split >= 4) merge_half<2>(m1, m2);
+        if (split >= 8) merge_half<3>(m1, m2);
+        if (split >= 16) merge_half<4>(m1, m2);
         score[g] = group_score(m1, m2, gs == 1);
     }
     wave_sync();
-    for (int g = lane; g < a.num_groups; g += LPT) {
+    for (int g = lane / split; g < a.num_groups; g += step) {
         const double s = score[g];
         int better = 0;
         for (int h = 0; h < a.num_groups; ++h) {
@@ -128,7 +137,7 @@ __device__ __forceinline__ void limit_groups(uint32_t (&key)[VPL], uint32_t* key
             better += (o > s || (o == s && h < g)) ? 1 : 0;
         }
         if (better >= a.topk_groups)
-            for (int i = 0; i < gs; ++i) key_of(g * gs + i) = 0;
+            for (int i = part; i < gs; i += split) key_of(g * gs + i) = 0;
     }
     wave_sync();
     read_run<VPL>(&keys[lane * kRun<VPL>], key);
@@ -211,7 +220,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
     // The k best pairs of (key, lane); lane j keeps pair j.  The lane that gave a
     // pair goes on to its largest key below that.  It finds it by unsigned
     // distance (keys at or above wrap round to more than the distance of 0), or
-    // with 16 keys the token's lanes find it, one key each, from LDS (16384 tokens
+    // with 16 keys or more the token's lanes find it together from LDS (16384 tokens
     // of 256 experts: 7.8 us against 8.4; of 64, 4 keys a lane: 4.8 against 4.6).
     // Lanes of groups that are off still have keys in LDS, but are never first.
     uint32_t best = 0;
@@ -230,9 +239,15 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, const floa
             const int first = token_first<LPT>(best == now, wave_lane);
             top[q] = lane == j ? now : top[q];
             owner[q] = lane == j ? first : owner[q];
-            if constexpr (VPL == 16) {
-                const uint32_t k = lane < VPL ? lds_keys[slot][first * kRun<VPL> + lane] : 0u;
-                const uint32_t next = token_max<LPT>(k < now ? k : 0u);
+            if constexpr (VPL >= 16) {
+                uint32_t next = 0;
+#pragma unroll
+                for (int i = 0; i < VPL; i += LPT) {
+                    const uint32_t k =
+                        i + lane < VPL ? lds_keys[slot][first * kRun<VPL> + i + lane] : 0u;
+                    next = max(next, k < now ? k : 0u);
+                }
+                next = token_max<LPT>(next);
                 best = lane == first ? next : best;
             } else if (lane == first && now != 0) {
                 const uint32_t below = best - 1;
@@ -475,30 +490,28 @@ template <bool BF16>
 hipError_t launch(const RouteArgs& a, const RouteForward* f, const RouteBackward* b,
                   hipStream_t stream) {
     if (a.num_tokens == 0) return hipSuccess;
-    const TokenShape s = token_shape(a.num_experts);
+    const TokenShape s = token_shape(a.num_experts, kSixteenLanes);
     if (s.lpt == 16) {
         switch (s.vpl) {
             case 1: launch_one<16, 1, BF16>(a, f, b, stream); break;
             case 2: launch_one<16, 2, BF16>(a, f, b, stream); break;
             case 4: launch_one<16, 4, BF16>(a, f, b, stream); break;
             case 8: launch_one<16, 8, BF16>(a, f, b, stream); break;
-            default: launch_one<16, 16, BF16>(a, f, b, stream); break;
+            case 16: launch_one<16, 16, BF16>(a, f, b, stream); break;
+            default: launch_one<16, 32, BF16>(a, f, b, stream); break;
         }
     } else {
-        if (s.vpl == 8)
-            launch_one<64, 8, BF16>(a, f, b, stream);
-        else
-            launch_one<64, 16, BF16>(a, f, b, stream);
+        launch_one<64, 16, BF16>(a, f, b, stream);
     }
     return hipGetLastError();
 }
 
 }  // namespace
 
-// 16 lanes a token up to 256 experts, so that four tokens share each of a
+// 16 lanes a token up to `most` experts, so that four tokens share each of a
 // wave's reductions; 64 lanes above.
-TokenShape token_shape(int num_experts) {
-    const int lpt = num_experts <= 256 ? 16 : 64;
+TokenShape token_shape(int num_experts, int most) {
+    const int lpt = num_experts <= most ? 16 : 64;
     int vpl = 1;
     while (lpt * vpl < num_experts) vpl *= 2;
     return {lpt, vpl};

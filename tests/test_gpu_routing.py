@@ -222,6 +222,26 @@ def test_ties_go_to_the_lowest_index(E, G, KG):
     Case(50, E, 8, G=G, KG=KG, logits=x, bf16=True, score=1).all()
 
 
+@pytest.mark.parametrize("E,G,KG", [(8, 1, 1), (40, 5, 2), (100, 1, 1), (256, 2, 1), (256, 32, 9),
+                                    (300, 3, 2), (512, 8, 4), (512, 16, 5), (512, 32, 32),
+                                    (640, 2, 1), (1000, 1, 1), (1024, 4, 3), (1024, 16, 7),
+                                    (1024, 32, 3)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_few_distinct_values(E, G, KG, bf16):
+    """Lanes with several experts of one key, some of them past the k-th entry, groups
+    of equal score, and rows with few experts or none left."""
+    r = np.random.default_rng(E + G)
+    for k in sorted({1, min(7, KG * (E // G)), min(32, KG * (E // G))}):
+        x = r.integers(-2, 3, (60, E)).astype(np.float32)
+        x[x == -2] = -np.inf
+        x[:12] = np.where(r.random((12, E)) < 0.02, x[:12], np.nan)
+        x[12:15] = 1.0
+        x[15] = np.nan
+        x[16:19] = np.where(r.random((3, E)) < 0.5, 0.0, -0.0)
+        c = Case(60, E, k, G=G, KG=KG, score=1, bf16=bf16, pad=0.1, logits=x)
+        c.check_route(*c.route())
+
+
 def test_repeated_and_foreign_ids_in_the_gradient():
     c = Case(40, 64, 6)
     idx = c.r.integers(-2, 70, (40, 6)).astype(np.int32)
