@@ -320,6 +320,7 @@ __device__ __forceinline__ void join_entries(const int (&e)[SEL], const float (&
             __uint_as_float(token_bcast<LPT, J % LPT>(__float_as_uint(part[J / LPT])));
 #pragma unroll
         for (int q = 0; q < SEL; ++q) {
+            if (J == 0) sum[q] = 0.0f;
             if (ej == e[q]) {
                 sum[q] += pj;
                 if (J < q * LPT + lane) mine[q] = false;
@@ -342,7 +343,7 @@ __device__ __forceinline__ void join_entries(const int (&e)[SEL], const float (&
 // no order of atomics matters.
 template <int LPT, int VPL, bool BF16>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(
-    RouteArgs a, const int32_t* topk_idx, const float* d_weights, const uint8_t* valid, float coef,
+    RouteArgs a, const int32_t* topk_idx, const float* d_weights, const uint8_t* valid, float factor,
     const int32_t* counts, const int32_t* num_valid, const float* d_loss, void* d_logits) {
     constexpr int kTokens = kThreads / LPT;
     constexpr int kSel = kMaxTopk > LPT ? kMaxTopk / LPT : 1;
@@ -391,8 +392,8 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
         for (int i = 0; i < VPL; ++i) p[i] *= r;
     }
     if (loss) {
-        const int64_t seq = (inside ? t : 0) / a.seq_len;
-        const int32_t* c = counts + seq * E;
+        const uint32_t seq = static_cast<uint32_t>(inside ? t : 0) / static_cast<uint32_t>(a.seq_len);
+        const int32_t* c = counts + static_cast<int64_t>(seq) * E;
         const int32_t c0 = c[0];
         int32_t ci[VPL];
         if (W >= 4 && a.fours) {
@@ -411,8 +412,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
             }
         }
         const float n = static_cast<float>(max(num_valid[seq], 1));
-        const float f = coef * static_cast<float>(E) /
-                        (static_cast<float>(a.num_seqs) * static_cast<float>(k)) * d_loss[0] / n / n;
+        const float f = factor * d_loss[0] / n / n;
         float d[VPL], dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
@@ -447,12 +447,26 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
 #pragma unroll
             for (int i = 0; i < VPL; ++i) dx[i] -= p[i] * gw;
         }
-        float sum[kSel] = {};
+        float sum[kSel];
         bool mine[kSel];
 #pragma unroll
-        for (int q = 0; q < kSel; ++q) mine[q] = e[q] >= 0;
-        join_entries<LPT, kSel, 0>(e, part, k, lane, sum, mine);
+        for (int q = 0; q < kSel; ++q) {
+            mine[q] = e[q] >= 0;
+            sum[q] = part[q];
+        }
+        // Every entry leaves its number at its expert: one that finds another's
+        // there shares the expert, which routing itself never gives.
         float* to = add[slot];
+#pragma unroll
+        for (int q = 0; q < kSel; ++q)
+            if (mine[q]) to[e[q]] = __int_as_float(q * LPT + lane);
+        wave_sync();
+        bool shared = false;
+#pragma unroll
+        for (int q = 0; q < kSel; ++q)
+            if (mine[q]) shared |= __float_as_int(to[e[q]]) != q * LPT + lane;
+        if (__any(shared)) join_entries<LPT, kSel, 0>(e, part, k, lane, sum, mine);
+        wave_sync();
 #pragma unroll
         for (int i = 0; i < VPL; ++i) to[expert<VPL, BF16>(own, i)] = 0.0f;
         wave_sync();
@@ -477,13 +491,16 @@ void launch_one(const RouteArgs& a, const RouteForward* f, const RouteBackward* 
     constexpr int kTokens = kThreads / LPT;
     const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(a.num_tokens) + kTokens - 1) /
                                                 kTokens);
-    if (f != nullptr)
+    if (f != nullptr) {
         hipLaunchKernelGGL((route_kernel<LPT, VPL, BF16>), dim3(grid), dim3(kThreads), 0, stream, a,
                            f->bias, f->valid, f->topk_idx, f->topk_weights);
-    else
+    } else {
+        const float factor = b->coef * static_cast<float>(a.num_experts) /
+                             (static_cast<float>(a.num_seqs) * static_cast<float>(a.num_topk));
         hipLaunchKernelGGL((route_backward_kernel<LPT, VPL, BF16>), dim3(grid), dim3(kThreads), 0,
-                           stream, a, b->topk_idx, b->d_weights, b->valid, b->coef, b->counts,
+                           stream, a, b->topk_idx, b->d_weights, b->valid, factor, b->counts,
                            b->num_valid, b->d_loss, b->d_logits);
+    }
 }
 
 template <bool BF16>

@@ -155,6 +155,11 @@ __device__ __forceinline__ float order_value(uint32_t k) {
     return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
 }
 
+// The larger of two numbers, without the quieting of NaN that fmaxf adds.
+__device__ __forceinline__ float larger(float x, float y) {
+    return __builtin_amdgcn_fmed3f(x, y, __builtin_inff());
+}
+
 // exp(x) for x <= 0: 2^t with t = x log2(e) rounded, times 1 + the rounding's
 // part.  v_exp_f32 is good to one unit in the last place, so the result is to
 // about two, in half the instructions of a library exponential.  Below -150
@@ -289,7 +294,7 @@ __device__ __forceinline__ void scores(const float (&x)[VPL], bool sigmoid, floa
     m = -3.402823466e38f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-        if (finite(x[i])) m = fmaxf(m, x[i]);
+        m = larger(m, finite(x[i]) ? x[i] : m);
     m = token_fmax<LPT>(m);
     // no branch per expert: what an expert that is off computes is dropped
     if (sigmoid && m > kSmallScore) {
