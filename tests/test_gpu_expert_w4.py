@@ -140,6 +140,22 @@ def test_rows_per_expert(m, fmt):
     Case(idx, 6, 64, 256, 72, fmt, False).check()
 
 
+SMALL = [0, 1, 9, 15, 16, 17, 24, 31, 32, 33, 20, 12]
+LARGE = [0, 1, 33, 63, 64, 65, 100, 129, 48, 16, 5, 70]
+
+
+@pytest.mark.parametrize("counts", [SMALL, LARGE], ids=["small", "large"])
+@pytest.mark.parametrize("K,N,cap", [(32, 1, 0), (96, 33, 0), (256, 72, 64), (544, 130, 0),
+                                     (1152, 260, 40), (4224, 33, 0), (4640, 5, 0), (8320, 3, 0)])
+@pytest.mark.parametrize("fmt,gated", [(0, False), (0, True), (1, True), (2, False)])
+def test_many_experts_with_many_rows(K, N, cap, counts, fmt, gated):
+    """Row tiles of every filling, enough of them to occupy the card."""
+    E = 228
+    idx = np.repeat(np.arange(E), np.resize(counts, E)).astype(np.int32)[:, None]
+    idx = np.random.default_rng(K).permutation(idx)
+    Case(idx, E, cap, (K + 127) // 128 * 128 if fmt else K, N, fmt, gated).check()
+
+
 def test_skewed_routing_and_foreign_ids():
     r = np.random.default_rng(3)
     idx = (r.zipf(1.3, (400, 6)) - 1).astype(np.int64)
