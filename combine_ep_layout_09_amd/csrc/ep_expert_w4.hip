@@ -788,9 +788,9 @@ hipError_t launch_expert_w4(const ep_problem& p, const ep_expert_w4_t& mm, const
     // (K 2048, 256 experts: 343 us against 403; K 7168: 589 against 587).
     // The many-row kernel gives 256 weight rows of a row tile to one workgroup, so
     // with few of those most CUs idle and the few-row kernel's smaller pieces win.
-    // K 4096, bf16: 58 workgroups 28 us against 12 with the few-row kernel, 116: 29
-    // and 27, 180 (1 expert, K 7168: 140): 30 and 41 (66 and 97); FP8: 58: 33 and
-    // 11, 72: 31 and 22, 232: 33 and 34, 288: 48 and 53.
+    // K 4096, bf16: 58 workgroups of 32 rows 28 us against 12 with the few-row
+    // kernel, 116: 29 and 27, 232: 30 and 41; 40 of 64 rows: 37 and 26, 160: 40 and
+    // 68; FP8: 58: 33 and 11, 72: 31 and 22, 232: 33 and 34, 288: 48 and 53.
     const bool fp8 = mm.in_format != 0;
     const int64_t blocks = (mm.out_features * (gated ? 2 : 1) + 4 * kRows - 1) / (4 * kRows);
     const auto many = [&](int rows, int mc) {
