@@ -14,7 +14,7 @@
 // kOneGroup partial sums one workgroup does it, and the loss with them; above
 // that many, of which the last to finish adds their parts of the loss, in
 // order.  No sum depends on the order in which workgroups run.  16384 x 256 fp32
-// in four sequences: 8.6 and 6.3 us, the call 15.0, with a third kernel for the
+// in four sequences: 8.5 and 7.0 us, the call 14.4, with a third kernel for the
 // parts 16.2; with one workgroup for all 65536 partial sums 38.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -34,7 +34,7 @@ constexpr int64_t kMostGroups = kFinish;  // workgroups of the second: a thread 
 // 16000 tokens take 24.7 us with 16 lanes, 23.5 with 64, 256 tokens 12.5 and 9.9.
 constexpr int kSixteen = 256;
 constexpr int kRowsWanted = 256;
-constexpr int64_t kOneGroup = 16384;
+constexpr int64_t kOneGroup = 8192;
 
 struct Geometry {
     int runs;        // runs of tokens per sequence
@@ -154,7 +154,7 @@ __device__ __forceinline__ double group_sum(double v, double* lds) {
 }
 
 // Outputs are the (sequence, expert) pairs in order.  A workgroup takes `cols`
-// of them at a time (a power of two, 64 to kFinish), kFinish / cols threads
+// of them at a time (a power of two, 32 to kFinish), kFinish / cols threads
 // each adding every kFinish / cols-th row of partial sums.  Every workgroup
 // writes its part of the loss; the one that is last to count itself in `done`
 // adds them in order.
@@ -263,10 +263,11 @@ hipError_t launch_balance(const RouteArgs& a, const BalanceArgs& b, void* worksp
     }
     double* part = reinterpret_cast<double*>(ws + g.part);
     const int64_t outputs = static_cast<int64_t>(a.num_seqs) * a.num_experts;
-    // One workgroup up to kOneGroup partial sums; above that 64 outputs and 16
-    // slices of rows per workgroup.
+    // One workgroup up to kOneGroup partial sums (4096 of them: 4.5 us, 6.4 with
+    // many; 16384: 10.1 and 7.1); above that 32 outputs and 32 slices of rows per
+    // workgroup (256 rows of 256 outputs: 8.6 us, with 64 outputs 12.4).
     const bool one = outputs * g.runs <= kOneGroup;
-    int cols = 64;
+    int cols = 32;
     while (one && cols < kFinish && cols < outputs) cols *= 2;
     int64_t groups = one ? 1 : (outputs + cols - 1) / cols;
     groups = groups < kMostGroups ? groups : kMostGroups;
