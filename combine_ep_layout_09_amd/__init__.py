@@ -83,27 +83,35 @@ class Problem(ctypes.Structure):
 class Routing(ctypes.Structure):
     """ep_routing: T, E, k, groups and how many of them a token may use, the
     score ("softmax" / 0 or "sigmoid" / 1), whether a token's weights are
-    normalised, sequences of the balance loss, factor of the weights."""
+    normalised, sequences of the balance loss, factor of the weights, and
+    whether the choice goes by "logits" / 0 or by "scores" / 1, as that of a
+    model with a sigmoid gate does (sigmoid only)."""
     _fields_ = [("num_tokens", ctypes.c_int32), ("num_experts", ctypes.c_int32),
                 ("num_topk", ctypes.c_int32), ("num_groups", ctypes.c_int32),
                 ("topk_groups", ctypes.c_int32), ("score", ctypes.c_int32),
                 ("normalize", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
-                ("weight_scale", ctypes.c_float)]
+                ("weight_scale", ctypes.c_float), ("choose_by_score", ctypes.c_int32)]
 
     _scores = {"softmax": 0, "sigmoid": 1, 0: 0, 1: 1}
+    _choices = {"logits": 0, "scores": 1, 0: 0, 1: 1}
 
     def __init__(self, num_tokens, num_experts, num_topk, num_groups=1, topk_groups=1,
-                 score="softmax", normalize=True, num_seqs=1, weight_scale=1.0):
+                 score="softmax", normalize=True, num_seqs=1, weight_scale=1.0,
+                 choose_by="logits"):
         if score not in self._scores:
             raise ValueError(f"score is {score!r}, expected 'softmax' or 'sigmoid'")
+        if choose_by not in self._choices:
+            raise ValueError(f"choose_by is {choose_by!r}, expected 'logits' or 'scores'")
         ctypes.Structure.__init__(self, num_tokens, num_experts, num_topk, num_groups,
                                   topk_groups, self._scores[score], int(normalize), num_seqs,
-                                  weight_scale)
+                                  weight_scale, self._choices[choose_by])
 
     def __repr__(self):
         return (f"Routing(T={self.num_tokens}, E={self.num_experts}, k={self.num_topk}, "
                 f"groups={self.topk_groups}/{self.num_groups}, "
-                f"score={'sigmoid' if self.score else 'softmax'}, normalize={self.normalize}, "
+                f"score={'sigmoid' if self.score else 'softmax'}, "
+                f"choose_by={'scores' if self.choose_by_score else 'logits'}, "
+                f"normalize={self.normalize}, "
                 f"seqs={self.num_seqs}, scale={self.weight_scale})")
 
 

@@ -110,11 +110,12 @@ int check_routing(const ep_routing* rt) {
     if (rt == nullptr) return EP_ERR_ARG;
     if (rt->num_tokens < 0 || rt->num_experts < 1 || rt->num_topk < 1 || rt->num_groups < 1 ||
         rt->topk_groups < 1 || rt->num_seqs < 1 || rt->score < 0 || rt->score > 1 ||
-        rt->normalize < 0 || rt->normalize > 1 || !std::isfinite(rt->weight_scale))
+        rt->normalize < 0 || rt->normalize > 1 || rt->choose_by_score < 0 ||
+        rt->choose_by_score > 1 || !std::isfinite(rt->weight_scale))
         return EP_ERR_ARG;
     if (rt->num_experts > ep::kMaxExperts || rt->num_topk > ep::kMaxTopk ||
         rt->num_groups > ep::kMaxGroups || rt->num_seqs > ep::kMaxSeqs ||
-        rt->num_tokens > ep::kMaxRouted)
+        rt->num_tokens > ep::kMaxRouted || (rt->choose_by_score == 1 && rt->score != 1))
         return EP_ERR_UNSUPPORTED;
     if (rt->num_experts % rt->num_groups != 0 || rt->topk_groups > rt->num_groups ||
         rt->num_topk > rt->topk_groups * (rt->num_experts / rt->num_groups) ||
@@ -147,6 +148,7 @@ ep::RouteArgs route_args(const ep_routing& rt, const void* logits, int bf16, int
     a.bf16 = bf16 != 0;
     a.sigmoid = rt.score == 1;
     a.normalize = rt.normalize == 1;
+    a.by_score = rt.choose_by_score == 1;
     const int el = bf16 ? 2 : 4;
     const ep::TokenShape shape = ep::token_shape(rt.num_experts, ep::kSixteenLanes);
     const int vpl = shape.vpl;

@@ -94,7 +94,7 @@ struct RouteArgs {
     int32_t num_seqs, seq_len;
     float scale;
     int32_t group_lanes;
-    bool bf16, sigmoid, normalize, pieces, out_pieces, fours;
+    bool bf16, sigmoid, normalize, pieces, out_pieces, fours, by_score;
 };
 // Lanes per token and experts per lane of the routing kernels.
 struct TokenShape {

@@ -186,6 +186,32 @@ __device__ __forceinline__ Sigmoids sigmoids(float x) {
     const float s = t * r;
     return x >= 0.0f ? Sigmoids{r, s} : Sigmoids{s, r};
 }
+
+// fp32(sigma(x)), from a value of sigma(x) good to about 2^-46.  The choice
+// compares keys made of it, and two fp32 units, which sigmoids() is good to,
+// would decide between close ones at random: with t = exp(-|x|) = 2^n exp(f ln 2),
+// |f| <= 1/2, the exponential is its series to f^12 (rest below 2^-52), the
+// quotient two Newton steps from the hardware's reciprocal.  46 instructions a
+// value, most of them fp64.
+__device__ __forceinline__ float sigmoid_rounded(float x) {
+    const double y = -fabs(static_cast<double>(x)) * 1.44269504088896340736;
+    const double v = fmax(y, -1000.0);  // exp is 0 in fp32 long before, and n stays an int
+    const double n = rint(v);
+    const double f = (v - n) * 0.693147180559945309417;
+    constexpr double kSeries[13] = {1.0,         1.0,          1.0 / 2,       1.0 / 6,     1.0 / 24,
+                                    1.0 / 120,   1.0 / 720,    1.0 / 5040,    1.0 / 40320, 1.0 / 362880,
+                                    1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600};
+    double p = kSeries[12];
+#pragma unroll
+    for (int i = 11; i >= 0; --i) p = fma(p, f, kSeries[i]);
+    const double t = ldexp(p, static_cast<int>(n));
+    const double d = 1.0 + t;
+    double r = __builtin_amdgcn_rcp(d);
+    r = fma(fma(-d, r, 1.0), r, r);
+    r = fma(fma(-d, r, 1.0), r, r);
+    return static_cast<float>(x >= 0.0f ? r : t * r);
+}
+
 // Elements of a piece: 16 bytes, or all that a lane holds.
 template <int VPL, bool BF16>
 constexpr int kPiece = VPL < (BF16 ? 8 : 4) ? VPL : (BF16 ? 8 : 4);

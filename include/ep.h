@@ -252,18 +252,24 @@ typedef struct ep_routing {
     int32_t num_seqs;     /* B, 1 .. 2^20, divides T: the balance loss is taken per sequence of
                              T / B consecutive tokens */
     float weight_scale;   /* factor of every weight, finite */
+    int32_t choose_by_score;  /* what the choice goes by: 0 the logits, 1 the scores (sigmoid
+                                 only).  A model whose gate is a sigmoid, with groups or with
+                                 a bias, chooses by its scores: neither a bias nor a sum of two
+                                 keys means the same on the logits. */
 } ep_routing;
 
 /* Experts and weights of each token.
  *   logits        [T, E] gate logits, fp32 (logits_bf16 = 0) or bf16 (1), device, at their
  *                 own alignment (4 / 2 bytes); row t starts logits_stride >= E elements after
  *                 row t - 1.
- *   expert_bias   fp32 [E], device, or NULL.  Added to the logits for the choice only.
+ *   expert_bias   fp32 [E], device, or NULL.  Added to the logits (choose_by_score = 0) or
+ *                 the scores (1), for the choice only.
  *   valid         uint8 [T], device, or NULL (every token is valid).
- *   topk_idx      int32 [T, k], written: the experts with the k largest keys
- *                 fp32(logit + bias), largest first, equal keys by the lower index; -1
- *                 where fewer than k experts are on (ep_layout skips those entries).  A key
- *                 that is not finite is off.
+ *   topk_idx      int32 [T, k], written: the experts with the k largest keys, largest
+ *                 first, equal keys by the lower index; -1 where fewer than k experts are on
+ *                 (ep_layout skips those entries).  The key is fp32(logit + bias), or with
+ *                 choose_by_score fp32(fp32(1 / (1 + exp(-logit))) + bias), the score taken
+ *                 in fp64 and rounded.  An expert whose key is not finite is off.
  *                 G > 1: only experts of the topk_groups best groups; a group's score is
  *                 the fp64 sum of its two largest keys (one, if it has one expert), an
  *                 expert that is off counting as -FLT_MAX; equal scores by the lower index.
