@@ -34,6 +34,10 @@ constexpr int64_t kMostGroups = kFinish;  // workgroups of the second: a thread 
 // 16000 tokens take 24.7 us with 16 lanes, 23.5 with 64, 256 tokens 12.5 and 9.9.
 constexpr int kSixteen = 256;
 constexpr int kRowsWanted = 256;
+// Passes of a workgroup: a lane adds one fp32 probability per pass, and those of
+// equal tokens all round the same way (1/17 added 2048 times is off by 420 units of
+// 2^-24).  Longer sequences get more workgroups; their rows are added in fp64.
+constexpr int64_t kMostPasses = 32;
 constexpr int64_t kOneGroup = 8192;
 
 struct Geometry {
@@ -48,6 +52,8 @@ Geometry geometry(int T, int E, int B) {
     const int64_t pass = kSum / token_shape(E, kSixteen).lpt;  // tokens of a workgroup's pass
     int64_t runs = (kRowsWanted + B - 1) / B;
     const int64_t most = (len + pass - 1) / pass;
+    const int64_t least = (most + kMostPasses - 1) / kMostPasses;
+    if (runs < least) runs = least;
     if (runs > most) runs = most;
     if (runs < 1) runs = 1;
     g.run_tokens = static_cast<int>((len + runs - 1) / runs);
