@@ -39,6 +39,7 @@ and marshal the arguments once and return a callable that only issues the C
 call, for loops that launch the same problem many times.
 """
 import ctypes
+import math
 import os
 
 __all__ = [
@@ -200,9 +201,15 @@ def ep_layout_workspace_bytes(prob):
     return int(load_library().ep_layout_workspace_bytes(ctypes.byref(prob)))
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_handle(stream):
@@ -447,21 +454,32 @@ def prepare_layout_dispatch(prob, topk_idx, layout, workspace, x, recv_x, recv_s
 
 def _device_of(t, name):
     """Index of the GPU that holds `t`."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    dev = t.get_device()
+    try:
+        dev = t.get_device()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
     if dev < 0:
         raise ValueError(f"{name} must be in GPU memory")
     return dev
 
 
-def _arg(t, name, dtype, numel, dev, allow_none=False):
-    """Pointer of a contiguous tensor of `numel` elements on device `dev`."""
+def _runs(shape):
+    """Sizes of the runs of memory that a contiguous tensor's dimensions mark."""
+    n, out = 1, set()
+    for d in reversed(shape):
+        n *= d
+        out.add(n)
+    return out - {1}
+
+
+def _arg(t, name, dtype, shape, dev, allow_none=False):
+    """Pointer of a contiguous tensor on device `dev`, of `shape` (or of a number
+    of elements, if that is an int).  Dimensions may be split or merged, as in
+    [B, L, k] or [B * L * k] for [T, k]; other orders of them are refused."""
     if t is None and allow_none:
         return None
     try:  # what nearly every call passes, checked without naming what is wrong
-        if (t.dtype is dtype and t.numel() == numel and t.is_contiguous()
+        if (t.dtype is dtype and t.shape == shape and t.is_contiguous()
                 and t.get_device() == dev):
             return t.data_ptr()
     except AttributeError:
@@ -471,10 +489,15 @@ def _arg(t, name, dtype, numel, dev, allow_none=False):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.numel() != numel:
-        raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
+    want = (shape,) if isinstance(shape, int) else shape
+    if t.numel() != math.prod(want):
+        raise ValueError(f"{name} has {t.numel()} elements, expected {math.prod(want)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    if t.shape != want and t.numel():
+        has, wants = _runs(t.shape), _runs(want)
+        if not (has <= wants or wants <= has):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {want}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be in GPU memory, on cuda:{dev}")
     return t.data_ptr()
@@ -550,16 +573,18 @@ def _logits_args(rt, logits):
 
 def _valid_arg(rt, valid, dev):
     torch = _torch()
-    return _arg(valid, "valid", (torch.uint8, torch.bool), rt.num_tokens, dev)
+    u8 = torch.uint8
+    dtype = u8 if getattr(valid, "dtype", None) is u8 else (u8, torch.bool)
+    return _arg(valid, "valid", dtype, (rt.num_tokens,), dev)
 
 
 def _route_args(rt, logits, topk_idx, topk_weights, expert_bias, valid):
     torch = _torch()
     dev, lp, bf16, stride = _logits_args(rt, logits)
-    n = rt.num_tokens * rt.num_topk
+    n = (rt.num_tokens, rt.num_topk)
     bp = vp = None
     if expert_bias is not None:
-        bp = _arg(expert_bias, "expert_bias", torch.float32, rt.num_experts, dev)
+        bp = _arg(expert_bias, "expert_bias", torch.float32, (rt.num_experts,), dev)
     if valid is not None:
         vp = _valid_arg(rt, valid, dev)
     ip = _arg(topk_idx, "topk_idx", torch.int32, n, dev)
@@ -589,15 +614,15 @@ def _balance_args(rt, logits, topk_idx, coef, counts, mean_prob, num_valid, loss
     torch = _torch()
     dev, lp, bf16, stride = _logits_args(rt, logits)
     T, E, B = rt.num_tokens, rt.num_experts, rt.num_seqs
-    ip = _arg(topk_idx, "topk_idx", torch.int32, T * rt.num_topk, dev)
+    ip = _arg(topk_idx, "topk_idx", torch.int32, (T, rt.num_topk), dev)
     vp = None if valid is None else _valid_arg(rt, valid, dev)
-    cp = _arg(counts, "counts", torch.int32, B * E, dev)
-    mp = _arg(mean_prob, "mean_prob", torch.float32, B * E, dev)
-    np_ = _arg(num_valid, "num_valid", torch.int32, B, dev)
-    op = _arg(loss, "loss", torch.float32, 1, dev)
+    cp = _arg(counts, "counts", torch.int32, (B, E), dev)
+    mp = _arg(mean_prob, "mean_prob", torch.float32, (B, E), dev)
+    np_ = _arg(num_valid, "num_valid", torch.int32, (B,), dev)
+    op = _arg(loss, "loss", torch.float32, (1,), dev)
     if not isinstance(workspace, torch.Tensor):
         raise TypeError("workspace must be a torch.Tensor")
-    wp = _arg(workspace, "workspace", workspace.dtype, workspace.numel(), dev)
+    wp = _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev)
     nbytes = workspace.numel() * workspace.element_size()
     return dev, (ctypes.byref(rt), lp, bf16, stride, ip, vp, coef, cp, mp, np_, op, wp, nbytes)
 
@@ -624,7 +649,7 @@ def _route_backward_args(rt, logits, topk_idx, d_logits, d_weights, coef, counts
     torch = _torch()
     dev, lp, bf16, stride = _logits_args(rt, logits)
     T, E, B = rt.num_tokens, rt.num_experts, rt.num_seqs
-    n = T * rt.num_topk
+    n = (T, rt.num_topk)
     if d_weights is None and d_loss is None:
         raise ValueError("d_weights or d_loss is required")
     if d_weights is not None and topk_idx is None:
@@ -634,10 +659,10 @@ def _route_backward_args(rt, logits, topk_idx, d_logits, d_weights, coef, counts
     ip = _arg(topk_idx, "topk_idx", torch.int32, n, dev, allow_none=True)
     gp = _arg(d_weights, "d_weights", torch.float32, n, dev, allow_none=True)
     vp = None if valid is None else _valid_arg(rt, valid, dev)
-    cp = _arg(counts, "counts", torch.int32, B * E, dev, allow_none=True)
-    np_ = _arg(num_valid, "num_valid", torch.int32, B, dev, allow_none=True)
-    sp = _arg(d_loss, "d_loss", torch.float32, 1, dev, allow_none=True)
-    dp = _arg(d_logits, "d_logits", logits.dtype, T * E, dev)
+    cp = _arg(counts, "counts", torch.int32, (B, E), dev, allow_none=True)
+    np_ = _arg(num_valid, "num_valid", torch.int32, (B,), dev, allow_none=True)
+    sp = _arg(d_loss, "d_loss", torch.float32, (1,), dev, allow_none=True)
+    dp = _arg(d_logits, "d_logits", logits.dtype, (T, E), dev)
     return dev, (ctypes.byref(rt), lp, bf16, stride, ip, gp, vp, coef, cp, np_, sp, dp)
 
 
@@ -665,17 +690,17 @@ def _expert_w4_args(prob, mm, rows, layout, codes, scales, out, row_scales):
     R = E * prob.capacity if prob.capacity else prob.num_tokens * prob.num_topk
     n2 = 2 * N if mm.activation == 1 else N
     u8 = torch.uint8
-    s = _LayoutPtrs(_arg(layout.count, "count", torch.int32, E, dev),
-                    _arg(layout.offset, "offset", torch.int32, E + 1, dev))
+    s = _LayoutPtrs(_arg(layout.count, "count", torch.int32, (E,), dev),
+                    _arg(layout.offset, "offset", torch.int32, (E + 1,), dev))
     if fmt == 0:
-        rp = _arg(rows, "rows", torch.bfloat16, R * K, dev)
+        rp = _arg(rows, "rows", torch.bfloat16, (R, K), dev)
         sp = None
     else:
-        rp = _arg(rows, "rows", (u8, torch.float8_e4m3fn), R * K, dev)
-        sp = _arg(row_scales, "row_scales", u8 if fmt == 2 else torch.float32, R * (K // 128), dev)
-    cp = _arg(codes, "codes", u8, E * n2 * (K // 2), dev)
-    wp = _arg(scales, "scales", u8, E * n2 * (K // 32), dev)
-    op = _arg(out, "out", torch.bfloat16, R * N, dev)
+        rp = _arg(rows, "rows", (u8, torch.float8_e4m3fn), (R, K), dev)
+        sp = _arg(row_scales, "row_scales", u8 if fmt == 2 else torch.float32, (R, K // 128), dev)
+    cp = _arg(codes, "codes", u8, (E, n2, K // 2), dev)
+    wp = _arg(scales, "scales", u8, (E, n2, K // 32), dev)
+    op = _arg(out, "out", torch.bfloat16, (R, N), dev)
     return dev, s, (ctypes.byref(prob), ctypes.byref(mm), rp, sp, ctypes.byref(s), cp, wp, op)
 
 
