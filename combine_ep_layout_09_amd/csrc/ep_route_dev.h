@@ -221,10 +221,6 @@ constexpr int kPiece = VPL < (BF16 ? 8 : 4) ? VPL : (BF16 ? 8 : 4);
 struct Experts {
     int first, step;
 };
-template <int VPL, bool BF16>
-__device__ __forceinline__ Experts consecutive(int lane) {
-    return {lane * VPL, kPiece<VPL, BF16>};
-}
 template <int LPT, int VPL, bool BF16>
 __device__ __forceinline__ Experts spread(int lane) {
     return {lane * kPiece<VPL, BF16>, LPT * kPiece<VPL, BF16>};
