@@ -190,14 +190,14 @@ __device__ __forceinline__ Found find_tile(const Args& a, Pick pick) {
 }
 
 // One step's operands of a wave: two chunks of 128 channels.
-template <int MT, bool FP8>
+template <bool FP8>
 struct Stage {
     u32x4 w[2][kTiles];
-    u32x4 x[2][MT][FP8 ? 2 : 4];
+    u32x4 x[2][FP8 ? 2 : 4];
 };
 
 // Few rows per expert.  A workgroup takes 64 weight rows of one expert against
-// up to 16 * MT rows; its WAVES waves take pairs of chunks in turns and add
+// up to 16 rows; its WAVES waves take pairs of chunks in turns and add
 // their sums in LDS, in wave order.  FP8: rows are E4M3FN with one scale per 128
 // channels (UE8: a UE8M0 byte, else fp32), which multiplies the chunk's sum.
 // GATED: tiles 0, 1 are rows n of the gate half and tiles 2, 3 rows N + n.
@@ -213,10 +213,10 @@ struct Stage {
 // outgrows the caches.  256 experts, K 7168, N 2048 gated, 4 FP8 rows each: 590 us,
 // 6.8 TB/s (696 with 64-byte pieces, 640 with the lines kept); K 2048, N 7168, bf16
 // rows: 335 us, 5.9 TB/s; 8 experts of one token: 25 us, 4.9 TB/s.
-template <int WAVES, int MT, bool FP8, bool UE8, bool GATED, bool WORDS>
-__global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void expert_w4_kernel(Args a) {
+template <int WAVES, bool FP8, bool UE8, bool GATED, bool WORDS>
+__global__ __launch_bounds__(WAVES* kWave, 4) void expert_w4_kernel(Args a) {
     constexpr int kThreads = WAVES * kWave;
-    constexpr int MC = 16 * MT;
+    constexpr int MC = 16;
     constexpr int kOut = GATED ? kRows / 2 : kRows;  // outputs per workgroup
     constexpr int kScaleBytes = kRows * kScaleRow;
     constexpr int kRowScaleBytes = FP8 ? MC * kRowScaleRow * 4 : 0;
@@ -255,18 +255,13 @@ __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void e
     const auto x_view = view(a.rows + (start + m0) * x_pitch, rows_here * x_pitch);
     const int half = lane / 8 % 2;
     const uint32_t w_at = lane % 8 * w_pitch + half * 64 + group * 16;
-    uint32_t x_at[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-        x_at[m] = (m * 16 + r16) * x_pitch + group * (FP8 ? 32 : 64);
+    const uint32_t x_at = r16 * x_pitch + group * (FP8 ? 32 : 64);
 
-    f32x4 acc[kTiles][MT];
+    f32x4 acc[kTiles];
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[t][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < kTiles; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    const auto load = [&](int p, Stage<MT, FP8>& s) {  // chunks 2p and 2p + 1
+    const auto load = [&](int p, Stage<FP8>& s) {  // chunks 2p and 2p + 1
         const uint32_t at = p * 8 + half * 4 + group < blocks ? w_at : kNowhere;
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
@@ -278,62 +273,46 @@ __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void e
         for (int h = 0; h < 2; ++h) {
             const bool has = p * 8 + h * 4 + group < blocks;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int i = 0; i < (FP8 ? 2 : 4); ++i)
-                    s.x[h][m][i] = load16<false>(x_view, has ? x_at[m] : kNowhere,
-                                                 (2 * p + h) * (FP8 ? 128 : 256) + i * 16);
+            for (int i = 0; i < (FP8 ? 2 : 4); ++i)
+                s.x[h][i] = load16<false>(x_view, has ? x_at : kNowhere,
+                                          (2 * p + h) * (FP8 ? 128 : 256) + i * 16);
         }
     };
     const auto multiply = [&](int c, const u32x4(&w)[kTiles],
-                              const u32x4(&x)[MT][FP8 ? 2 : 4]) {  // c within the segment
+                              const u32x4(&x)[FP8 ? 2 : 4]) {  // c within the segment
         float sf[kTiles];
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
             sf[t] = __uint_as_float(
                 static_cast<uint32_t>(lds_scale[t * 16 + r16][c * 4 + group]) << 23);
-        f32x4 part[kTiles][MT];
+        f32x4 part[kTiles];
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                part[t][m] = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[t][m];
+        for (int t = 0; t < kTiles; ++t) part[t] = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[t];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             __builtin_amdgcn_sched_barrier(0);  // or every operand is made at once
-            bf16x8 xf[MT];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if constexpr (FP8) {
-                    const u32x4 v = x[m][i / 2];
-                    xf[m] = i % 2 == 0 ? rows8(v.x, v.y) : rows8(v.z, v.w);
-                } else {
-                    Frag f;
-                    f.w = x[m][i];
-                    xf[m] = f.v;
-                }
+            bf16x8 xf;
+            if constexpr (FP8) {
+                const u32x4 v = x[i / 2];
+                xf = i % 2 == 0 ? rows8(v.x, v.y) : rows8(v.z, v.w);
+            } else {
+                Frag f;
+                f.w = x[i];
+                xf = f.v;
             }
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                const bf16x8 wf = weights8(w[t][i], sf[t]);
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    part[t][m] =
-                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[m], part[t][m], 0, 0, 0);
-            }
+            for (int t = 0; t < kTiles; ++t)
+                part[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(weights8(w[t][i], sf[t]), xf,
+                                                                  part[t], 0, 0, 0);
         }
+        const float xs = FP8 ? lds_row[r16][c] : 1.0f;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const float xs = FP8 ? lds_row[m * 16 + r16][c] : 1.0f;
+        for (int t = 0; t < kTiles; ++t) {
+            if constexpr (FP8) {
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                if constexpr (FP8) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[t][m][i] = fmaf(xs, part[t][m][i], acc[t][m][i]);
-                } else {
-                    acc[t][m] = part[t][m];
-                }
+                for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(xs, part[t][i], acc[t][i]);
+            } else {
+                acc[t] = part[t];
             }
         }
     };
@@ -371,7 +350,7 @@ __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void e
                             : static_cast<const float*>(a.row_scales)[at];
             }
         }
-        Stage<MT, FP8> s;
+        Stage<FP8> s;
         int p = wave;
         load(c0 / 2 + p, s);  // past the end of the channels it loads nothing
         if (seg > 0) __syncthreads();  // the scales before are done with
@@ -421,9 +400,7 @@ __global__ __launch_bounds__(WAVES* kWave, MT == 1 ? 4 : MT == 2 ? 3 : 2) void e
     // lane l holds weight rows 4 * (l / 16) .. + 3 of a tile against row l % 16
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-            *reinterpret_cast<f32x4*>(&red[wave][m * 16 + r16][t * 16 + group * 4]) = acc[t][m];
+        *reinterpret_cast<f32x4*>(&red[wave][r16][t * 16 + group * 4]) = acc[t];
     __syncthreads();
     for (int i = threadIdx.x; i < rows_here * kOut; i += kThreads) {
         const int m = i / kOut, n = i % kOut;
@@ -708,19 +685,20 @@ __global__ __launch_bounds__(256, 2) void expert_w4_tile_kernel(Args a) {
         }
 }
 
-// The kernel of WAVES waves for few rows, or (WAVES 0) the one for many.
+// The kernel of WAVES waves for few rows (MT 1), or (WAVES 0) the one for many.
 template <int WAVES, int MT, bool FP8, bool UE8, bool GATED, bool WORDS>
 void launch_one(const Args& a, dim3 grid, hipStream_t stream) {
     if constexpr (WAVES == 0)
         hipLaunchKernelGGL((expert_w4_tile_kernel<MT, FP8, UE8, GATED, WORDS>), grid, dim3(256), 0,
                            stream, a);
     else
-        hipLaunchKernelGGL((expert_w4_kernel<WAVES, MT, FP8, UE8, GATED, WORDS>), grid,
+        hipLaunchKernelGGL((expert_w4_kernel<WAVES, FP8, UE8, GATED, WORDS>), grid,
                            dim3(WAVES * kWave), 0, stream, a);
 }
 
 template <int WAVES, int MT, bool GATED>
 void launch_format(const Args& a, int format, dim3 grid, hipStream_t stream) {
+    static_assert(WAVES == 0 || MT == 1, "a few-row tile has 16 rows");
     if constexpr (MT < 4) {
         if (format == 1) return launch_one<WAVES, MT, true, false, GATED, true>(a, grid, stream);
         if (format == 2) return launch_one<WAVES, MT, true, true, GATED, true>(a, grid, stream);
