@@ -210,9 +210,9 @@ struct Stage {
 // two chunks across lanes afterwards costs 1.5 instructions per word.  The
 // scales, scattered bytes in memory, come once, whole rows at a time, to LDS.
 // Loads two steps ahead, or more waves, were slower: what is in flight then
-// outgrows the caches.  256 experts, K 7168, N 2048 gated, 4 FP8 rows each: 590 us,
-// 6.8 TB/s (696 with 64-byte pieces, 640 with the lines kept); K 2048, N 7168, bf16
-// rows: 335 us, 5.9 TB/s; 8 experts of one token: 25 us, 4.9 TB/s.
+// outgrows the caches.  256 experts, K 7168, N 2048 gated, 4 FP8 rows each: 595 to
+// 603 us, 6.6 TB/s (696 with 64-byte pieces, 640 with the lines kept); K 2048, N 7168,
+// bf16 rows: 344 to 359 us, 5.6 TB/s; 8 experts of one token: 25.4 us, 4.9 TB/s.
 template <int WAVES, bool FP8, bool UE8, bool GATED, bool WORDS>
 __global__ __launch_bounds__(WAVES* kWave, 4) void expert_w4_kernel(Args a) {
     constexpr int kThreads = WAVES * kWave;
@@ -422,12 +422,17 @@ __global__ __launch_bounds__(WAVES* kWave, 4) void expert_w4_kernel(Args a) {
 // chunk of 128 channels passes through LDS, as bf16, once for all of them,
 // loaded two chunks ahead; the weights' next pair of chunks is in flight as
 // well.  GATED: a wave's tiles 0, 1 are gate and 2, 3 up of the same 32 outputs.
-// With 32-row tiles an expert mostly has one and its codes are read once (not
-// kept: 48.5 us, kept 51.6, at 24 rows each); with 64-row tiles several read
-// them (128 rows each: kept 124, not 127).
-// 64 skewed experts, 48 rows each in the mean, K 4096, N 1408 gated, bf16: 132 us
-// (242 with the other kernel).  Matrix instructions are a third of that, their
-// operands' conversion another; memory alone would take 83.
+// bf16 rows have 32-row tiles where an expert mostly has one, whose codes are read
+// once (not kept: 48.5 us, kept 51.6, at 24 rows each), and 64-row tiles where
+// several read them (128 rows each: kept 124, not 127).  FP8 rows have 32-row tiles
+// at any number of rows, and their codes are never kept, which pays for few rows
+// only (64 experts, K 4096, N 1408 gated: 24 rows each 90 to 96 us, kept 100 to 103;
+// 64: 204, kept 187; 128: 342, kept 309; 512: 1184, kept 965).
+// 64 skewed experts, 48 rows each in the mean, K 4096, N 1408 gated, bf16: 127 to
+// 133 us (242 with the other kernel).  Matrix instructions are a third of that, their
+// operands' conversion another; memory alone would take 61 at the rate that reading
+// reaches.  128 rows each, 256 experts, K 7168, N 2048 gated: 2.25 ms, 854 TFLOP/s;
+// FP8 3.38 ms, 569 TFLOP/s: a tile of 32 rows converts the codes again for each.
 constexpr int kTileSegment = 4096;                 // channels of weight scales in LDS
 constexpr int kTileScaleRow = kTileSegment / 32 + 4;  // bytes
 constexpr int kTileRow = kStep * 2 + 16;           // bytes of a row's chunk in LDS

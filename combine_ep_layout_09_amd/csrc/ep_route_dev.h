@@ -162,8 +162,9 @@ __device__ __forceinline__ float larger(float x, float y) {
 
 // exp(x) for x <= 0: 2^t with t = x log2(e) rounded, times 1 + the rounding's
 // part.  v_exp_f32 is good to one unit in the last place, so the result is to
-// about two, in half the instructions of a library exponential.  Below -150
-// the result is 0 either way; the bound keeps the rounding's part finite.
+// about two, in half the instructions of a library exponential.  It gives 0 for
+// results below 2^-126, the smallest normal number (x below -87.3): v_exp_f32 does.
+// Below -150 the bound keeps the rounding's part finite.
 __device__ __forceinline__ float exp_neg(float x) {
     constexpr float kLog2e = 1.44269504088896340736f;
     constexpr float kLog2eRest = static_cast<float>(1.44269504088896340736 - kLog2e);

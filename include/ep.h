@@ -240,7 +240,9 @@ int ep_e4m3_encode(const float* in, uint8_t* out, int64_t n, void* stream);
  *
  * Scores of token t: softmax (score = 0): z_e = exp(x_e); sigmoid (1):
  * z_e = 1 / (1 + exp(-x_e)).  Probabilities p_e = z_e / sum_i z_i over the
- * token's experts.  Sums, maxima and gradients are held in fp32 or fp64. */
+ * token's experts.  Sums, maxima and gradients are held in fp32 or fp64.
+ * Scores below 2^-126 count as 0 (of softmax, and of sigmoid where all of a
+ * token's logits are below -20: below 2^-126 of the token's largest). */
 typedef struct ep_routing {
     int32_t num_tokens;   /* T, 0 .. 2^25 */
     int32_t num_experts;  /* E, 1 .. 1024 */
