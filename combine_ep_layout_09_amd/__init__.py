@@ -23,14 +23,26 @@ Entry points (same names as the C ABI):
   ep_route_backward(rt, logits, topk_idx, d_logits, d_weights=None, coef=0.0,
                     counts=None, num_valid=None, d_loss=None, valid=None, stream=None)
   ep_expert_w4(prob, mm, rows, layout, codes, scales, out, row_scales=None, stream=None)
+  ep_layer_norm(nm, x, weight, bias, y, mean=None, rstd=None, stream=None)
+  ep_layer_norm_workspace_bytes(nm)          -> bytes
+  ep_layer_norm_backward(nm, x, dy, weight, mean, rstd, dx, d_weight=None, d_bias=None,
+                         workspace=None, d_skip=None, stream=None)
+  ep_combine_dropout(prob, expert_out, layout, topk_weights, p, rng, y, residual=None,
+                     stream=None)
+  ep_combine_backward(prob, dy, expert_out, layout, topk_weights, p, rng, d_expert_out,
+                      d_weights=None, stream=None)
+  ep_dispatch_i8(prob, x, layout, recv_q, recv_scales, stream=None)
+  ep_expert_i8_workspace_bytes(prob, mm)     -> bytes
+  ep_expert_i8(prob, mm, rows, layout, weights, scales, out, row_scales=None,
+               workspace=None, stream=None)
   ep_e4m3_encode(inp, out, stream=None)
   ep_strerror(code)
 
 Helpers that allocate with torch (plumbing, outside the computation):
   Problem(...), Layout.empty(prob, device), alloc_workspace, alloc_recv,
-  Routing(...), ExpertW4(...).
+  Routing(...), ExpertW4(...), Norm(...), ExpertI8(...).
 
-The routing calls and ep_expert_w4 run on the GPU that holds their tensors,
+The calls from ep_route on run on the GPU that holds their tensors,
 by default on that GPU's current stream; tensors on several devices are
 refused.
 
@@ -51,6 +63,11 @@ __all__ = [
     "Routing", "ExpertW4", "ep_route", "ep_balance_workspace_bytes", "ep_balance_loss",
     "ep_route_backward", "ep_expert_w4", "prepare_route", "prepare_balance_loss",
     "prepare_route_backward", "prepare_expert_w4",
+    "Norm", "ExpertI8", "ep_layer_norm", "ep_layer_norm_workspace_bytes",
+    "ep_layer_norm_backward", "ep_combine_dropout", "ep_combine_backward", "ep_dispatch_i8",
+    "ep_expert_i8_workspace_bytes", "ep_expert_i8", "prepare_layer_norm",
+    "prepare_layer_norm_backward", "prepare_combine_dropout", "prepare_combine_backward",
+    "prepare_dispatch_i8", "prepare_expert_i8",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -130,6 +147,33 @@ class ExpertW4(ctypes.Structure):
                 f"format={self.in_format}, activation={self.activation})")
 
 
+class Norm(ctypes.Structure):
+    """ep_norm: T rows of H channels and what is added to their variance."""
+    _fields_ = [("num_tokens", ctypes.c_int32), ("hidden", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+    def __init__(self, num_tokens, hidden, eps=1e-5):
+        super().__init__(num_tokens, hidden, eps)
+
+    def __repr__(self):
+        return f"Norm(T={self.num_tokens}, H={self.hidden}, eps={self.eps})"
+
+
+class ExpertI8(ctypes.Structure):
+    """ep_expert_i8_t: K inputs, N outputs, format of the rows (0 bf16, quantised
+    by the call; 1 int8 with a scale per row) and activation (0 none,
+    1 silu(gate) * up)."""
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
+                ("in_format", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+    def __init__(self, in_features, out_features, in_format=0, activation=0):
+        super().__init__(in_features, out_features, int(in_format), int(activation))
+
+    def __repr__(self):
+        return (f"ExpertI8(K={self.in_features}, N={self.out_features}, "
+                f"format={self.in_format}, activation={self.activation})")
+
+
 class _LayoutPtrs(ctypes.Structure):
     _fields_ = [("count", ctypes.c_void_p), ("offset", ctypes.c_void_p),
                 ("slot_of", ctypes.c_void_p), ("src_of_slot", ctypes.c_void_p),
@@ -181,6 +225,25 @@ def load_library():
     lib.ep_route_backward.argtypes = [RT, vp, i32, i64, vp, vp, vp, f32, vp, vp, vp, vp, vp]
     lib.ep_expert_w4.restype = ctypes.c_int
     lib.ep_expert_w4.argtypes = [P, ctypes.POINTER(ExpertW4), vp, vp, L, vp, vp, vp, vp]
+    size, f64 = ctypes.c_size_t, ctypes.c_double
+    NM, I8 = ctypes.POINTER(Norm), ctypes.POINTER(ExpertI8)
+    lib.ep_layer_norm.restype = ctypes.c_int
+    lib.ep_layer_norm.argtypes = [NM, vp, i32, i64, vp, vp, i32, vp, vp, vp, vp]
+    lib.ep_layer_norm_workspace_bytes.restype = i64
+    lib.ep_layer_norm_workspace_bytes.argtypes = [NM]
+    lib.ep_layer_norm_backward.restype = ctypes.c_int
+    lib.ep_layer_norm_backward.argtypes = [NM, vp, i32, i64, vp, i64, vp, i32, vp, vp, vp, vp,
+                                           vp, vp, vp, size, vp]
+    lib.ep_combine_dropout.restype = ctypes.c_int
+    lib.ep_combine_dropout.argtypes = [P, vp, L, vp, vp, f64, vp, vp, vp]
+    lib.ep_combine_backward.restype = ctypes.c_int
+    lib.ep_combine_backward.argtypes = [P, vp, vp, L, vp, f64, vp, vp, vp, vp]
+    lib.ep_dispatch_i8.restype = ctypes.c_int
+    lib.ep_dispatch_i8.argtypes = [P, vp, L, vp, vp, vp]
+    lib.ep_expert_i8_workspace_bytes.restype = i64
+    lib.ep_expert_i8_workspace_bytes.argtypes = [P, I8]
+    lib.ep_expert_i8.restype = ctypes.c_int
+    lib.ep_expert_i8.argtypes = [P, I8, vp, vp, L, vp, vp, vp, vp, size, vp]
     lib.ep_e4m3_encode.restype = ctypes.c_int
     lib.ep_e4m3_encode.argtypes = [vp, vp, i64, vp]
     lib.ep_strerror.restype = ctypes.c_char_p
@@ -715,3 +778,276 @@ def prepare_expert_w4(prob, mm, rows, layout, codes, scales, out, row_scales=Non
     dev, s, args = _expert_w4_args(prob, mm, rows, layout, codes, scales, out, row_scales)
     return _PreparedOn("ep_expert_w4", lib.ep_expert_w4, args, dev,
                        (prob, mm, s, rows, layout, codes, scales, out, row_scales))
+
+
+# ------------------------- layer norm, dropout in the combine, 8-bit integers
+
+def _rows_arg(t, name, nm, dtype, dev):
+    """Pointer and row pitch of a [T, H] tensor, rows of any pitch."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    T, H = nm.num_tokens, nm.hidden
+    if t.shape != (T, H):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, H)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be in GPU memory, on cuda:{dev}")
+    stride, inner = t.stride()
+    if inner != 1 and H > 1:
+        raise ValueError(f"{name} must be contiguous along the channels")
+    if T <= 1:
+        stride = H
+    if stride < H:
+        raise ValueError(f"{name} rows overlap: row pitch {stride} below {H}")
+    return t.data_ptr(), stride
+
+
+def _norm_types(x, params):
+    """Whether x and the parameters are bf16 (1) or fp32 (0), and their types."""
+    torch = _torch()
+    kinds = {torch.float32: 0, torch.bfloat16: 1}
+    x_dtype = getattr(x, "dtype", None)
+    if x_dtype not in kinds:
+        raise TypeError(f"x has dtype {x_dtype}, expected float32 or bfloat16")
+    w_dtype = None
+    for p in params:
+        if p is not None:
+            w_dtype = getattr(p, "dtype", None)
+            break
+    else:
+        w_dtype = torch.float32
+    if w_dtype not in kinds:
+        raise TypeError(f"weight has dtype {w_dtype}, expected float32 or bfloat16")
+    return x_dtype, kinds[x_dtype], w_dtype, kinds[w_dtype]
+
+
+def _layer_norm_args(nm, x, weight, bias, y, mean, rstd):
+    torch = _torch()
+    dev = _device_of(x, "x")
+    x_dtype, x_bf16, w_dtype, w_bf16 = _norm_types(x, (weight, bias))
+    T, H = nm.num_tokens, nm.hidden
+    xp, stride = _rows_arg(x, "x", nm, x_dtype, dev)
+    wp = _arg(weight, "weight", w_dtype, (H,), dev, allow_none=True)
+    bp = _arg(bias, "bias", w_dtype, (H,), dev, allow_none=True)
+    yp = _arg(y, "y", x_dtype, (T, H), dev)
+    mp = _arg(mean, "mean", torch.float32, (T,), dev, allow_none=True)
+    rp = _arg(rstd, "rstd", torch.float32, (T,), dev, allow_none=True)
+    return dev, (ctypes.byref(nm), xp, x_bf16, stride, wp, bp, w_bf16, yp, mp, rp)
+
+
+def ep_layer_norm(nm, x, weight, bias, y, mean=None, rstd=None, stream=None):
+    lib = _lib or load_library()
+    dev, args = _layer_norm_args(nm, x, weight, bias, y, mean, rstd)
+    _issue("ep_layer_norm", lib.ep_layer_norm, args, dev, stream)
+
+
+def prepare_layer_norm(nm, x, weight, bias, y, mean=None, rstd=None):
+    lib = load_library()
+    dev, args = _layer_norm_args(nm, x, weight, bias, y, mean, rstd)
+    return _PreparedOn("ep_layer_norm", lib.ep_layer_norm, args, dev,
+                       (nm, x, weight, bias, y, mean, rstd))
+
+
+def ep_layer_norm_workspace_bytes(nm):
+    return int(load_library().ep_layer_norm_workspace_bytes(ctypes.byref(nm)))
+
+
+def _workspace_arg(workspace, dev):
+    """Pointer and bytes of a workspace that may be missing."""
+    if workspace is None:
+        return None, 0
+    if not isinstance(workspace, _torch().Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    wp = _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev)
+    return wp, workspace.numel() * workspace.element_size()
+
+
+def _layer_norm_backward_args(nm, x, dy, weight, mean, rstd, dx, d_weight, d_bias, workspace,
+                              d_skip):
+    torch = _torch()
+    dev = _device_of(x, "x")
+    x_dtype, x_bf16, w_dtype, w_bf16 = _norm_types(x, (weight, d_weight, d_bias))
+    T, H = nm.num_tokens, nm.hidden
+    xp, x_stride = _rows_arg(x, "x", nm, x_dtype, dev)
+    gp, g_stride = _rows_arg(dy, "dy", nm, x_dtype, dev)
+    wp = _arg(weight, "weight", w_dtype, (H,), dev, allow_none=True)
+    mp = _arg(mean, "mean", torch.float32, (T,), dev)
+    rp = _arg(rstd, "rstd", torch.float32, (T,), dev)
+    sp = _arg(d_skip, "d_skip", x_dtype, (T, H), dev, allow_none=True)
+    dp = _arg(dx, "dx", x_dtype, (T, H), dev)
+    dwp = _arg(d_weight, "d_weight", w_dtype, (H,), dev, allow_none=True)
+    dbp = _arg(d_bias, "d_bias", w_dtype, (H,), dev, allow_none=True)
+    space, nbytes = _workspace_arg(workspace, dev)
+    return dev, (ctypes.byref(nm), xp, x_bf16, x_stride, gp, g_stride, wp, w_bf16, mp, rp, sp, dp,
+                 dwp, dbp, space, nbytes)
+
+
+def ep_layer_norm_backward(nm, x, dy, weight, mean, rstd, dx, d_weight=None, d_bias=None,
+                           workspace=None, d_skip=None, stream=None):
+    lib = _lib or load_library()
+    dev, args = _layer_norm_backward_args(nm, x, dy, weight, mean, rstd, dx, d_weight, d_bias,
+                                          workspace, d_skip)
+    _issue("ep_layer_norm_backward", lib.ep_layer_norm_backward, args, dev, stream)
+
+
+def prepare_layer_norm_backward(nm, x, dy, weight, mean, rstd, dx, d_weight=None, d_bias=None,
+                                workspace=None, d_skip=None):
+    lib = load_library()
+    dev, args = _layer_norm_backward_args(nm, x, dy, weight, mean, rstd, dx, d_weight, d_bias,
+                                          workspace, d_skip)
+    return _PreparedOn("ep_layer_norm_backward", lib.ep_layer_norm_backward, args, dev,
+                       (nm, x, dy, weight, mean, rstd, dx, d_weight, d_bias, workspace, d_skip))
+
+
+def _recv_rows(prob):
+    return (prob.num_experts * prob.capacity if prob.capacity
+            else prob.num_tokens * prob.num_topk)
+
+
+def _slots(prob, layout, dev):
+    s = _LayoutPtrs()
+    s.slot_of = _arg(layout.slot_of, "slot_of", _torch().int32,
+                     (prob.num_tokens, prob.num_topk), dev)
+    return s
+
+
+def _rng_arg(rng, dev):
+    """{seed, offset} as two 64-bit words, int64 or uint64."""
+    if rng is None:
+        return None
+    torch = _torch()
+    i64 = torch.int64
+    dtype = i64 if getattr(rng, "dtype", None) is i64 else (i64, torch.uint64)
+    return _arg(rng, "rng", dtype, (2,), dev)
+
+
+def _combine_dropout_args(prob, expert_out, layout, topk_weights, p, rng, y, residual):
+    torch = _torch()
+    dev = _device_of(y, "y")
+    T, H, bf16 = prob.num_tokens, prob.hidden, torch.bfloat16
+    s = _slots(prob, layout, dev)
+    ep = _arg(expert_out, "expert_out", bf16, (_recv_rows(prob), H), dev)
+    wp = _arg(topk_weights, "topk_weights", torch.float32, (T, prob.num_topk), dev)
+    rp = _arg(residual, "residual", bf16, (T, H), dev, allow_none=True)
+    gp = _rng_arg(rng, dev)
+    yp = _arg(y, "y", bf16, (T, H), dev)
+    return dev, s, (ctypes.byref(prob), ep, ctypes.byref(s), wp, rp, p, gp, yp)
+
+
+def ep_combine_dropout(prob, expert_out, layout, topk_weights, p, rng, y, residual=None,
+                       stream=None):
+    lib = _lib or load_library()
+    dev, _s, args = _combine_dropout_args(prob, expert_out, layout, topk_weights, p, rng, y,
+                                          residual)
+    _issue("ep_combine_dropout", lib.ep_combine_dropout, args, dev, stream)
+
+
+def prepare_combine_dropout(prob, expert_out, layout, topk_weights, p, rng, y, residual=None):
+    lib = load_library()
+    dev, s, args = _combine_dropout_args(prob, expert_out, layout, topk_weights, p, rng, y,
+                                         residual)
+    return _PreparedOn("ep_combine_dropout", lib.ep_combine_dropout, args, dev,
+                       (prob, s, expert_out, layout, topk_weights, rng, y, residual))
+
+
+def _combine_backward_args(prob, dy, expert_out, layout, topk_weights, p, rng, d_expert_out,
+                           d_weights):
+    torch = _torch()
+    dev = _device_of(dy, "dy")
+    T, H, k, bf16 = prob.num_tokens, prob.hidden, prob.num_topk, torch.bfloat16
+    R = _recv_rows(prob)
+    s = _slots(prob, layout, dev)
+    gp = _arg(dy, "dy", bf16, (T, H), dev)
+    ep = _arg(expert_out, "expert_out", bf16, (R, H), dev, allow_none=True)
+    wp = _arg(topk_weights, "topk_weights", torch.float32, (T, k), dev)
+    rp = _rng_arg(rng, dev)
+    dp = _arg(d_expert_out, "d_expert_out", bf16, (R, H), dev)
+    dwp = _arg(d_weights, "d_weights", torch.float32, (T, k), dev, allow_none=True)
+    return dev, s, (ctypes.byref(prob), gp, ep, ctypes.byref(s), wp, p, rp, dp, dwp)
+
+
+def ep_combine_backward(prob, dy, expert_out, layout, topk_weights, p, rng, d_expert_out,
+                        d_weights=None, stream=None):
+    lib = _lib or load_library()
+    dev, _s, args = _combine_backward_args(prob, dy, expert_out, layout, topk_weights, p, rng,
+                                           d_expert_out, d_weights)
+    _issue("ep_combine_backward", lib.ep_combine_backward, args, dev, stream)
+
+
+def prepare_combine_backward(prob, dy, expert_out, layout, topk_weights, p, rng, d_expert_out,
+                             d_weights=None):
+    lib = load_library()
+    dev, s, args = _combine_backward_args(prob, dy, expert_out, layout, topk_weights, p, rng,
+                                          d_expert_out, d_weights)
+    return _PreparedOn("ep_combine_backward", lib.ep_combine_backward, args, dev,
+                       (prob, s, dy, expert_out, layout, topk_weights, rng, d_expert_out,
+                        d_weights))
+
+
+def _dispatch_i8_args(prob, x, layout, recv_q, recv_scales):
+    torch = _torch()
+    dev = _device_of(x, "x")
+    T, H, R = prob.num_tokens, prob.hidden, _recv_rows(prob)
+    s = _slots(prob, layout, dev)
+    xp = _arg(x, "x", torch.bfloat16, (T, H), dev)
+    qp = _arg(recv_q, "recv_q", torch.int8, (R, H), dev)
+    sp = _arg(recv_scales, "recv_scales", torch.float32, (R,), dev)
+    return dev, s, (ctypes.byref(prob), xp, ctypes.byref(s), qp, sp)
+
+
+def ep_dispatch_i8(prob, x, layout, recv_q, recv_scales, stream=None):
+    lib = _lib or load_library()
+    dev, _s, args = _dispatch_i8_args(prob, x, layout, recv_q, recv_scales)
+    _issue("ep_dispatch_i8", lib.ep_dispatch_i8, args, dev, stream)
+
+
+def prepare_dispatch_i8(prob, x, layout, recv_q, recv_scales):
+    lib = load_library()
+    dev, s, args = _dispatch_i8_args(prob, x, layout, recv_q, recv_scales)
+    return _PreparedOn("ep_dispatch_i8", lib.ep_dispatch_i8, args, dev,
+                       (prob, s, x, layout, recv_q, recv_scales))
+
+
+def ep_expert_i8_workspace_bytes(prob, mm):
+    return int(load_library().ep_expert_i8_workspace_bytes(ctypes.byref(prob), ctypes.byref(mm)))
+
+
+def _expert_i8_args(prob, mm, rows, layout, weights, scales, out, row_scales, workspace):
+    torch = _torch()
+    dev = _device_of(rows, "rows")
+    K, N, E, R = mm.in_features, mm.out_features, prob.num_experts, _recv_rows(prob)
+    n2 = 2 * N if mm.activation == 1 else N
+    i8, f32, bf16 = torch.int8, torch.float32, torch.bfloat16
+    s = _LayoutPtrs(_arg(layout.count, "count", torch.int32, (E,), dev),
+                    _arg(layout.offset, "offset", torch.int32, (E + 1,), dev))
+    sp = None
+    if mm.in_format == 0:
+        rp = _arg(rows, "rows", bf16, (R, K), dev)
+    else:
+        rp = _arg(rows, "rows", i8, (R, K), dev)
+        sp = _arg(row_scales, "row_scales", f32, (R,), dev)
+    wp = _arg(weights, "weights", i8, (E, n2, K), dev)
+    cp = _arg(scales, "scales", f32, (E, n2), dev)
+    op = _arg(out, "out", bf16, (R, N), dev)
+    space, nbytes = _workspace_arg(workspace, dev) if mm.in_format == 0 else (None, 0)
+    return dev, s, (ctypes.byref(prob), ctypes.byref(mm), rp, sp, ctypes.byref(s), wp, cp, op,
+                    space, nbytes)
+
+
+def ep_expert_i8(prob, mm, rows, layout, weights, scales, out, row_scales=None, workspace=None,
+                 stream=None):
+    lib = _lib or load_library()
+    dev, _s, args = _expert_i8_args(prob, mm, rows, layout, weights, scales, out, row_scales,
+                                    workspace)
+    _issue("ep_expert_i8", lib.ep_expert_i8, args, dev, stream)
+
+
+def prepare_expert_i8(prob, mm, rows, layout, weights, scales, out, row_scales=None,
+                      workspace=None):
+    lib = load_library()
+    dev, s, args = _expert_i8_args(prob, mm, rows, layout, weights, scales, out, row_scales,
+                                   workspace)
+    return _PreparedOn("ep_expert_i8", lib.ep_expert_i8, args, dev,
+                       (prob, mm, s, rows, layout, weights, scales, out, row_scales, workspace))

@@ -169,6 +169,83 @@ ep::RouteArgs route_args(const ep_routing& rt, const void* logits, int bf16, int
     return a;
 }
 
+// Tokens of the calls that give every token a workgroup.
+int check_rowed(const ep_problem* p) {
+    const int rc = check_problem(p);
+    if (rc != EP_OK) return rc;
+    return p->num_tokens > ep::kMaxRowed ? EP_ERR_UNSUPPORTED : EP_OK;
+}
+
+// Whether two buffers share a byte (missing ones and empty ones share none).
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    if (a == nullptr || b == nullptr || a_bytes <= 0 || b_bytes <= 0) return false;
+    const auto p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return p < q ? q - p < static_cast<uintptr_t>(a_bytes) : p - q < static_cast<uintptr_t>(b_bytes);
+}
+
+struct Buffer {
+    const void* at;
+    int64_t bytes;
+};
+
+// Whether an output shares a byte with an input or with another output.
+template <size_t O, size_t I>
+bool outputs_overlap(const Buffer (&outs)[O], const Buffer (&ins)[I]) {
+    for (size_t o = 0; o < O; ++o) {
+        for (size_t q = 0; q < o; ++q)
+            if (overlap(outs[o].at, outs[o].bytes, outs[q].at, outs[q].bytes)) return true;
+        for (size_t i = 0; i < I; ++i)
+            if (overlap(outs[o].at, outs[o].bytes, ins[i].at, ins[i].bytes)) return true;
+    }
+    return false;
+}
+
+bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+int check_norm(const ep_norm* nm) {
+    if (nm == nullptr) return EP_ERR_ARG;
+    if (nm->num_tokens < 0 || nm->hidden < 1 || !(nm->eps >= 0.0f) || !std::isfinite(nm->eps))
+        return EP_ERR_ARG;
+    if (nm->num_tokens > ep::kMaxRouted || nm->hidden > ep::kMaxHidden) return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+// A [T, H] tensor of a norm whose rows are `stride` elements apart.
+int check_norm_rows(const ep_norm& nm, const void* p, int bf16, int64_t stride) {
+    if (bf16 < 0 || bf16 > 1 || stride < nm.hidden) return EP_ERR_ARG;
+    if (stride > (int64_t{1} << 31)) return EP_ERR_UNSUPPORTED;
+    if (nm.num_tokens > 0 && p == nullptr) return EP_ERR_ARG;
+    return aligned_to(p, bf16 ? 2 : 4) ? EP_OK : EP_ERR_ALIGN;
+}
+
+int64_t norm_row_bytes(const ep_norm& nm, int bf16, int64_t stride) {
+    if (nm.num_tokens == 0) return 0;
+    return ((nm.num_tokens - 1) * stride + nm.hidden) * (bf16 ? 2 : 4);
+}
+
+// p and rng of the calls with dropout.
+int check_dropout(double p, const uint64_t* rng, ep::DropArgs* drop) {
+    if (!(p >= 0.0) || !(p < 1.0)) return EP_ERR_ARG;
+    if (p > 0.0 && rng == nullptr) return EP_ERR_ARG;
+    if (!aligned_to(rng, 8)) return EP_ERR_ALIGN;
+    const double border = std::nearbyint(p * 4294967296.0);
+    drop->rng = rng;
+    drop->border = border < 4294967295.0 ? static_cast<uint32_t>(border) : 0xffffffffu;
+    drop->factor = static_cast<float>(1.0 / (1.0 - p));
+    return EP_OK;
+}
+
+int check_expert_i8(const ep_expert_i8_t* mm) {
+    if (mm == nullptr) return EP_ERR_ARG;
+    if (mm->in_features < 1 || mm->out_features < 1 || mm->in_format < 0 || mm->in_format > 1 ||
+        mm->activation < 0 || mm->activation > 1)
+        return EP_ERR_ARG;
+    if (mm->in_features > ep::kMaxHidden || mm->out_features > ep::kMaxHidden ||
+        mm->in_features % 16 != 0)
+        return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -367,6 +444,180 @@ int ep_expert_w4(const ep_problem* prob, const ep_expert_w4_t* mm, const void* r
         return EP_ERR_ALIGN;
     return from_hip(ep::launch_expert_w4(*prob, *mm, rows, row_scales, *layout, codes, scales, out,
                                          static_cast<hipStream_t>(stream)));
+}
+
+int ep_layer_norm(const ep_norm* nm, const void* x, int x_bf16, int64_t x_stride,
+                  const void* weight, const void* bias, int w_bf16, void* y, float* mean,
+                  float* rstd, void* stream) {
+    int rc = check_norm(nm);
+    if (rc != EP_OK) return rc;
+    rc = check_norm_rows(*nm, x, x_bf16, x_stride);
+    if (rc != EP_OK) return rc;
+    rc = check_norm_rows(*nm, y, x_bf16, nm->hidden);
+    if (rc != EP_OK) return rc;
+    if (w_bf16 < 0 || w_bf16 > 1 || (mean == nullptr) != (rstd == nullptr)) return EP_ERR_ARG;
+    if (!aligned_to(weight, w_bf16 ? 2 : 4) || !aligned_to(bias, w_bf16 ? 2 : 4) ||
+        !aligned4(mean) || !aligned4(rstd))
+        return EP_ERR_ALIGN;
+    const int64_t T = nm->num_tokens, param = nm->hidden * (w_bf16 ? 2 : 4);
+    const Buffer outs[] = {{y, norm_row_bytes(*nm, x_bf16, nm->hidden)}, {mean, T * 4}, {rstd, T * 4}};
+    const Buffer ins[] = {{x, norm_row_bytes(*nm, x_bf16, x_stride)}, {weight, param}, {bias, param}};
+    if (outputs_overlap(outs, ins)) return EP_ERR_ARG;
+    const ep::NormArgs a = {x, x_stride, weight, bias, y, mean, rstd, nm->num_tokens, nm->hidden,
+                            nm->eps};
+    return from_hip(ep::launch_norm(a, x_bf16 != 0, w_bf16 != 0, static_cast<hipStream_t>(stream)));
+}
+
+int64_t ep_layer_norm_workspace_bytes(const ep_norm* nm) {
+    if (check_norm(nm) != EP_OK) return -1;
+    return ep::norm_workspace_bytes(nm->num_tokens, nm->hidden);
+}
+
+int ep_layer_norm_backward(const ep_norm* nm, const void* x, int x_bf16, int64_t x_stride,
+                           const void* dy, int64_t dy_stride, const void* weight, int w_bf16,
+                           const float* mean, const float* rstd, const void* d_skip, void* dx,
+                           void* d_weight, void* d_bias, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    int rc = check_norm(nm);
+    if (rc != EP_OK) return rc;
+    rc = check_norm_rows(*nm, x, x_bf16, x_stride);
+    if (rc != EP_OK) return rc;
+    rc = check_norm_rows(*nm, dy, x_bf16, dy_stride);
+    if (rc != EP_OK) return rc;
+    rc = check_norm_rows(*nm, dx, x_bf16, nm->hidden);
+    if (rc != EP_OK) return rc;
+    if (w_bf16 < 0 || w_bf16 > 1) return EP_ERR_ARG;
+    if (nm->num_tokens > 0 && (mean == nullptr || rstd == nullptr)) return EP_ERR_ARG;
+    const int64_t space = ep::norm_workspace_bytes(nm->num_tokens, nm->hidden);
+    const bool params = d_weight != nullptr || d_bias != nullptr;
+    if (params && space > 0 &&
+        (workspace == nullptr || static_cast<int64_t>(workspace_bytes) < space))
+        return EP_ERR_ARG;
+    const int wb = w_bf16 ? 2 : 4;
+    if (!aligned_to(weight, wb) || !aligned_to(d_weight, wb) || !aligned_to(d_bias, wb) ||
+        !aligned_to(d_skip, x_bf16 ? 2 : 4) || !aligned4(mean) || !aligned4(rstd) ||
+        (params && !aligned16(workspace)))
+        return EP_ERR_ALIGN;
+    const int64_t T = nm->num_tokens, param = nm->hidden * wb;
+    const int64_t dense = norm_row_bytes(*nm, x_bf16, nm->hidden);
+    const Buffer outs[] = {{dx, dense}, {d_weight, param}, {d_bias, param},
+                           {params ? workspace : nullptr, space}};
+    const Buffer ins[] = {{x, norm_row_bytes(*nm, x_bf16, x_stride)},
+                          {dy, norm_row_bytes(*nm, x_bf16, dy_stride)},
+                          {weight, param}, {mean, T * 4}, {rstd, T * 4}, {d_skip, dense}};
+    if (outputs_overlap(outs, ins)) return EP_ERR_ARG;
+    const ep::NormGradArgs a = {x, dy, x_stride, dy_stride, weight, mean, rstd, d_skip, dx,
+                                d_weight, d_bias, nm->num_tokens, nm->hidden};
+    return from_hip(ep::launch_norm_grad(a, x_bf16 != 0, w_bf16 != 0, workspace,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+int ep_combine_dropout(const ep_problem* prob, const void* expert_out, const ep_layout_t* layout,
+                       const float* topk_weights, const void* residual, double p,
+                       const uint64_t* rng, void* y, void* stream) {
+    int rc = check_rowed(prob);
+    if (rc != EP_OK) return rc;
+    rc = check_layout_ptrs(*prob, layout, false);
+    if (rc != EP_OK) return rc;
+    ep::DropArgs drop;
+    rc = check_dropout(p, rng, &drop);
+    if (rc != EP_OK) return rc;
+    if (prob->num_tokens > 0 && (expert_out == nullptr || topk_weights == nullptr || y == nullptr))
+        return EP_ERR_ARG;
+    if (!aligned16(expert_out) || !aligned16(y) || !aligned16(residual) || !aligned4(topk_weights))
+        return EP_ERR_ALIGN;
+    const int64_t entries = static_cast<int64_t>(prob->num_tokens) * prob->num_topk;
+    const int64_t row = prob->hidden * 2, dense = prob->num_tokens * row;
+    const Buffer outs[] = {{y, dense}};
+    const Buffer ins[] = {{expert_out, recv_rows(*prob) * row}, {residual, dense},
+                          {topk_weights, entries * 4}, {layout->slot_of, entries * 4}, {rng, 16}};
+    if (outputs_overlap(outs, ins)) return EP_ERR_ARG;
+    return from_hip(ep::launch_combine_dropout(*prob, expert_out, layout->slot_of, topk_weights,
+                                               residual, drop, y, static_cast<hipStream_t>(stream)));
+}
+
+int ep_combine_backward(const ep_problem* prob, const void* dy, const void* expert_out,
+                        const ep_layout_t* layout, const float* topk_weights, double p,
+                        const uint64_t* rng, void* d_expert_out, float* d_weights, void* stream) {
+    int rc = check_rowed(prob);
+    if (rc != EP_OK) return rc;
+    rc = check_layout_ptrs(*prob, layout, false);
+    if (rc != EP_OK) return rc;
+    ep::DropArgs drop;
+    rc = check_dropout(p, rng, &drop);
+    if (rc != EP_OK) return rc;
+    if (prob->num_tokens > 0) {
+        if (dy == nullptr || topk_weights == nullptr || d_expert_out == nullptr) return EP_ERR_ARG;
+        if (d_weights != nullptr && expert_out == nullptr) return EP_ERR_ARG;
+    }
+    if (!aligned16(dy) || !aligned16(expert_out) || !aligned16(d_expert_out) ||
+        !aligned4(topk_weights) || !aligned4(d_weights))
+        return EP_ERR_ALIGN;
+    const int64_t entries = static_cast<int64_t>(prob->num_tokens) * prob->num_topk;
+    const int64_t row = prob->hidden * 2, recv = recv_rows(*prob) * row;
+    const Buffer outs[] = {{d_expert_out, recv}, {d_weights, entries * 4}};
+    const Buffer ins[] = {{dy, prob->num_tokens * row}, {expert_out, recv},
+                          {topk_weights, entries * 4}, {layout->slot_of, entries * 4}, {rng, 16}};
+    if (outputs_overlap(outs, ins)) return EP_ERR_ARG;
+    return from_hip(ep::launch_combine_backward(*prob, dy, expert_out, layout->slot_of,
+                                                topk_weights, drop, d_expert_out, d_weights,
+                                                static_cast<hipStream_t>(stream)));
+}
+
+int ep_dispatch_i8(const ep_problem* prob, const void* x, const ep_layout_t* layout, void* recv_q,
+                   float* recv_scales, void* stream) {
+    int rc = check_rowed(prob);
+    if (rc != EP_OK) return rc;
+    rc = check_layout_ptrs(*prob, layout, false);
+    if (rc != EP_OK) return rc;
+    if (prob->num_tokens > 0 && (x == nullptr || recv_q == nullptr || recv_scales == nullptr))
+        return EP_ERR_ARG;
+    if (!aligned16(x) || !aligned16(recv_q) || !aligned4(recv_scales)) return EP_ERR_ALIGN;
+    const int64_t T = prob->num_tokens, H = prob->hidden, R = recv_rows(*prob);
+    const Buffer outs[] = {{recv_q, R * H}, {recv_scales, R * 4}};
+    const Buffer ins[] = {{x, T * H * 2}, {layout->slot_of, T * prob->num_topk * 4}};
+    if (outputs_overlap(outs, ins)) return EP_ERR_ARG;
+    return from_hip(ep::launch_dispatch_i8(*prob, x, layout->slot_of, recv_q, recv_scales,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+int64_t ep_expert_i8_workspace_bytes(const ep_problem* prob, const ep_expert_i8_t* mm) {
+    if (check_problem(prob) != EP_OK || check_expert_i8(mm) != EP_OK) return -1;
+    return ep::expert_i8_workspace_bytes(*prob, *mm);
+}
+
+int ep_expert_i8(const ep_problem* prob, const ep_expert_i8_t* mm, const void* rows,
+                 const float* row_scales, const ep_layout_t* layout, const int8_t* weights,
+                 const float* scales, void* out, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+    int rc = check_problem(prob);
+    if (rc != EP_OK) return rc;
+    rc = check_expert_i8(mm);
+    if (rc != EP_OK) return rc;
+    if (layout == nullptr || layout->count == nullptr ||
+        (prob->capacity == 0 && layout->offset == nullptr))
+        return EP_ERR_ARG;
+    if (!aligned4(layout->count) || !aligned4(layout->offset)) return EP_ERR_ALIGN;
+    const int64_t space = ep::expert_i8_workspace_bytes(*prob, *mm);
+    if (prob->num_tokens > 0) {
+        if (rows == nullptr || weights == nullptr || scales == nullptr || out == nullptr)
+            return EP_ERR_ARG;
+        if (mm->in_format == 1 && row_scales == nullptr) return EP_ERR_ARG;
+        if (space > 0 && (workspace == nullptr || static_cast<int64_t>(workspace_bytes) < space))
+            return EP_ERR_ARG;
+    }
+    if (!aligned16(rows) || !aligned16(weights) || !aligned16(out) || !aligned4(scales) ||
+        (mm->in_format == 1 && !aligned4(row_scales)) || (space > 0 && !aligned16(workspace)))
+        return EP_ERR_ALIGN;
+    const int64_t R = recv_rows(*prob), K = mm->in_features, E = prob->num_experts;
+    const int64_t n2 = static_cast<int64_t>(mm->out_features) * (mm->activation ? 2 : 1);
+    const Buffer outs[] = {{out, R * mm->out_features * 2}, {workspace, space}};
+    const Buffer ins[] = {{rows, R * K * (mm->in_format ? 1 : 2)},
+                          {row_scales, mm->in_format ? R * 4 : 0}, {weights, E * n2 * K},
+                          {scales, E * n2 * 4}, {layout->count, E * 4}, {layout->offset, E * 4 + 4}};
+    if (outputs_overlap(outs, ins)) return EP_ERR_ARG;
+    return from_hip(ep::launch_expert_i8(*prob, *mm, rows, row_scales, *layout, weights, scales,
+                                         out, workspace, static_cast<hipStream_t>(stream)));
 }
 
 const char* ep_strerror(int code) {

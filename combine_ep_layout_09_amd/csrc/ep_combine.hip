@@ -29,6 +29,7 @@
 // following FP8 dispatch of the 16384-token workload by about a third).
 
 #include "ep_device.h"
+#include "ep_dropout_dev.h"
 #include "ep_internal.h"
 
 namespace ep {
@@ -38,13 +39,46 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxThreads = 1024;
 
+// What follows a piece's sum, before it is rounded.  begin() is called where the
+// rows' loads are issued, its result goes to end() with the sum.  Plain: nothing
+// (ep_combine).
+struct Plain {
+    struct Begun {};
+    __device__ __forceinline__ Begun begin(int64_t, int, int) const { return {}; }
+    __device__ __forceinline__ void end(const Begun&, int, int, float (&)[8]) const {}
+};
+
+// Dropout and the skip connection (ep_combine_dropout).  Eight channels of a piece
+// are two counters of the generator.
+struct Dropped {
+    DropArgs drop;
+    const u32x4* residual;
+    struct Begun {
+        u32x4 residual;
+    };
+    __device__ __forceinline__ Begun begin(int64_t t, int nvec, int v) const {
+        Begun b = {u32x4{0, 0, 0, 0}};
+        if (residual != nullptr) b.residual = __builtin_nontemporal_load(residual + t * nvec + v);
+        return b;
+    }
+    __device__ __forceinline__ void end(const Begun& b, int t, int v, float (&acc)[8]) const {
+        const uint32_t kept = dropout::keep8(drop, t, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t w = b.residual[i / 2];
+            const float r = i % 2 == 0 ? bf16_lo(w) : bf16_hi(w);
+            acc[i] = r + (kept >> i & 1 ? acc[i] * drop.factor : 0.0f);
+        }
+    }
+};
+
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-template <int KB, int VPL>
+template <int KB, int VPL, class Fin>
 __global__ __launch_bounds__(kMaxThreads) void combine_kernel(
         const u32x4* __restrict__ eo, int nvec, int k, const int32_t* __restrict__ slot_of,
-        int64_t R, const float* __restrict__ weights, u32x4* __restrict__ y) {
+        int64_t R, const float* __restrict__ weights, u32x4* __restrict__ y, Fin fin) {
     const int t = blockIdx.x;
     const int32_t* slots = slot_of + static_cast<int64_t>(t) * k;
     const float* w = weights + static_cast<int64_t>(t) * k;
@@ -62,6 +96,10 @@ __global__ __launch_bounds__(kMaxThreads) void combine_kernel(
             break;
         }
     }
+
+    typename Fin::Begun begun[VPL];
+#pragma unroll
+    for (int u = 0; u < VPL; ++u) begun[u] = fin.begin(t, nvec, v[u]);
 
     float acc[VPL][8];
 #pragma unroll
@@ -107,6 +145,7 @@ __global__ __launch_bounds__(kMaxThreads) void combine_kernel(
     u32x4* out = y + static_cast<int64_t>(t) * nvec;
 #pragma unroll
     for (int u = 0; u < VPL; ++u) {
+        fin.end(begun[u], t, v[u], acc[u]);
         u32x4 r;
         r.x = f32_to_bf16_rne(acc[u][0]) | (f32_to_bf16_rne(acc[u][1]) << 16);
         r.y = f32_to_bf16_rne(acc[u][2]) | (f32_to_bf16_rne(acc[u][3]) << 16);
@@ -156,11 +195,13 @@ struct PersistShape {
 // so that the slot loads do not depend on each other.  EXACT: k == KB, a
 // compile-time count, so that the token's slots and weights are unconditional
 // (merged) scalar loads.
-template <int KB, bool EXACT>
+template <int KB, bool EXACT, class Fin>
 __device__ __forceinline__ u32x4 combine_piece(const u32x4* __restrict__ eo, int nvec, int k_arg,
                                                const int32_t* __restrict__ slots,
-                                               const float* __restrict__ w, int64_t R, int v) {
+                                               const float* __restrict__ w, int64_t R, int t, int v,
+                                               const Fin& fin) {
     const int k = EXACT ? KB : k_arg;
+    const auto begun = fin.begin(t, nvec, v);
     float acc[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
@@ -190,6 +231,7 @@ __device__ __forceinline__ u32x4 combine_piece(const u32x4* __restrict__ eo, int
             }
         }
     }
+    fin.end(begun, t, v, acc);
     u32x4 r;
     r.x = f32_to_bf16_rne(acc[0]) | (f32_to_bf16_rne(acc[1]) << 16);
     r.y = f32_to_bf16_rne(acc[2]) | (f32_to_bf16_rne(acc[3]) << 16);
@@ -221,10 +263,11 @@ __device__ __forceinline__ void load_entries(const int32_t* __restrict__ slots,
 // hand (s, w): issues the KB row loads, runs `between` (which fetches the
 // next chunk's entries into s and w's successors), then the FMA chain.  On
 // return s and w hold what `between` fetched.
-template <int KB, typename Between>
+template <int KB, typename Between, class Fin>
 __device__ __forceinline__ u32x4 reduce_rows(const u32x4* __restrict__ eo, int nvec, int64_t R,
-                                             int v, int32_t (&s)[KB], float (&w)[KB],
-                                             Between between) {
+                                             int t, int v, int32_t (&s)[KB], float (&w)[KB],
+                                             Between between, const Fin& fin) {
+    const auto begun = fin.begin(t, nvec, v);
     bool ok[KB];
     u32x4 buf[KB];
 #pragma unroll
@@ -253,6 +296,7 @@ __device__ __forceinline__ u32x4 reduce_rows(const u32x4* __restrict__ eo, int n
             acc[c] = ok[jj] ? a : acc[c];
         }
     }
+    fin.end(begun, t, v, acc);
     u32x4 r;
     r.x = f32_to_bf16_rne(acc[0]) | (f32_to_bf16_rne(acc[1]) << 16);
     r.y = f32_to_bf16_rne(acc[2]) | (f32_to_bf16_rne(acc[3]) << 16);
@@ -264,11 +308,12 @@ __device__ __forceinline__ u32x4 reduce_rows(const u32x4* __restrict__ eo, int n
 // One workgroup per CU is four waves per SIMD; telling the compiler so lets
 // it keep all of a chunk's row loads in flight instead of trading them for
 // registers.
-template <int KB, bool EXACT>
+template <int KB, bool EXACT, class Fin>
 __global__ __launch_bounds__(kPersistThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void combine_persistent_kernel(
         const u32x4* __restrict__ eo, int nvec, int k, const int32_t* __restrict__ slot_of,
-        int64_t R, const float* __restrict__ weights, u32x4* __restrict__ y, PersistShape ps) {
+        int64_t R, const float* __restrict__ weights, u32x4* __restrict__ y, PersistShape ps,
+        Fin fin) {
     const int lane = static_cast<int>(lane_id());
     // the same for every lane of a wave: scalar from here on
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
@@ -318,16 +363,16 @@ void combine_persistent_kernel(
             // this chunk's loads may not move above the previous result
             asm volatile("" : "+v"(v) : "v"(dep));
             if (EXACT) {
-                out[i] = reduce_rows<KB>(eo, nvec, R, v, sc, wc, [&](int32_t (&sn)[KB], float (&wn)[KB]) {
+                out[i] = reduce_rows<KB>(eo, nvec, R, t, v, sc, wc, [&](int32_t (&sn)[KB], float (&wn)[KB]) {
                     // the next chunk's slots and weights, while this chunk's
                     // rows load (the last chunk of a launch refetches its own)
                     const int cn = min(base + (i + 1) * kPersistWaves, ps.chunks - 1);
                     const int64_t tn = ps.t0 + cn / ps.C;
                     load_entries<KB, true>(slot_of + tn * KB, weights + tn * KB, sn, wn);
-                });
+                }, fin);
             } else {
                 out[i] = combine_piece<KB, EXACT>(eo, nvec, k, slot_of + static_cast<int64_t>(t) * k,
-                                                  weights + static_cast<int64_t>(t) * k, R, v);
+                                                  weights + static_cast<int64_t>(t) * k, R, t, v, fin);
             }
             dep = out[i].x;
         }
@@ -342,34 +387,33 @@ void combine_persistent_kernel(
     }
 }
 
-template <int KB>
+template <int KB, class Fin>
 void launch_kb(int vpl, dim3 grid, int threads, hipStream_t stream, const u32x4* eo, int nvec,
-               int k, const int32_t* slot_of, int64_t R, const float* w, u32x4* y) {
+               int k, const int32_t* slot_of, int64_t R, const float* w, u32x4* y, const Fin& fin) {
     if (vpl == 1)
-        hipLaunchKernelGGL((combine_kernel<KB, 1>), grid, dim3(threads), 0, stream, eo, nvec, k,
-                           slot_of, R, w, y);
+        hipLaunchKernelGGL((combine_kernel<KB, 1, Fin>), grid, dim3(threads), 0, stream, eo, nvec,
+                           k, slot_of, R, w, y, fin);
     else
-        hipLaunchKernelGGL((combine_kernel<KB, 2>), grid, dim3(threads), 0, stream, eo, nvec, k,
-                           slot_of, R, w, y);
+        hipLaunchKernelGGL((combine_kernel<KB, 2, Fin>), grid, dim3(threads), 0, stream, eo, nvec,
+                           k, slot_of, R, w, y, fin);
 }
 
 // k <= 8: KB = k exactly; larger k: batches of 8.
-template <int KB>
+template <int KB, class Fin>
 void launch_persistent(int nwg, hipStream_t stream, const u32x4* eo, int nvec, int k,
                        const int32_t* slot_of, int64_t R, const float* w, u32x4* y,
-                       const PersistShape& ps) {
+                       const PersistShape& ps, const Fin& fin) {
     if (k == KB)
-        hipLaunchKernelGGL((combine_persistent_kernel<KB, true>), dim3(nwg),
-                           dim3(kPersistThreads), 0, stream, eo, nvec, k, slot_of, R, w, y, ps);
+        hipLaunchKernelGGL((combine_persistent_kernel<KB, true, Fin>), dim3(nwg),
+                           dim3(kPersistThreads), 0, stream, eo, nvec, k, slot_of, R, w, y, ps, fin);
     else
-        hipLaunchKernelGGL((combine_persistent_kernel<KB, false>), dim3(nwg),
-                           dim3(kPersistThreads), 0, stream, eo, nvec, k, slot_of, R, w, y, ps);
+        hipLaunchKernelGGL((combine_persistent_kernel<KB, false, Fin>), dim3(nwg),
+                           dim3(kPersistThreads), 0, stream, eo, nvec, k, slot_of, R, w, y, ps, fin);
 }
 
-}  // namespace
-
-hipError_t launch_combine(const ep_problem& p, const void* expert_out, const int32_t* slot_of,
-                          const float* topk_weights, void* y, hipStream_t stream) {
+template <class Fin>
+hipError_t launch_forms(const ep_problem& p, const void* expert_out, const int32_t* slot_of,
+                        const float* topk_weights, void* y, const Fin& fin, hipStream_t stream) {
     const int T = p.num_tokens;
     if (T == 0) return hipSuccess;
     const int64_t R = p.capacity == 0 ? static_cast<int64_t>(T) * p.num_topk
@@ -405,14 +449,14 @@ hipError_t launch_combine(const ep_problem& p, const void* expert_out, const int
             ps.chunks = static_cast<int>(min(per, static_cast<int64_t>(T) - t0) * C);
             ps.Q = static_cast<int>((ps.chunks + nw - 1) / nw);
             switch (k) {
-                case 1: launch_persistent<1>(ncu, stream, eo, nvec, k, slot_of, R, topk_weights, yo, ps); break;
-                case 2: launch_persistent<2>(ncu, stream, eo, nvec, k, slot_of, R, topk_weights, yo, ps); break;
-                case 3: launch_persistent<3>(ncu, stream, eo, nvec, k, slot_of, R, topk_weights, yo, ps); break;
-                case 4: launch_persistent<4>(ncu, stream, eo, nvec, k, slot_of, R, topk_weights, yo, ps); break;
-                case 5: launch_persistent<5>(ncu, stream, eo, nvec, k, slot_of, R, topk_weights, yo, ps); break;
-                case 6: launch_persistent<6>(ncu, stream, eo, nvec, k, slot_of, R, topk_weights, yo, ps); break;
-                case 7: launch_persistent<7>(ncu, stream, eo, nvec, k, slot_of, R, topk_weights, yo, ps); break;
-                default: launch_persistent<8>(ncu, stream, eo, nvec, k, slot_of, R, topk_weights, yo, ps); break;
+                case 1: launch_persistent<1>(ncu, stream, eo, nvec, k, slot_of, R, topk_weights, yo, ps, fin); break;
+                case 2: launch_persistent<2>(ncu, stream, eo, nvec, k, slot_of, R, topk_weights, yo, ps, fin); break;
+                case 3: launch_persistent<3>(ncu, stream, eo, nvec, k, slot_of, R, topk_weights, yo, ps, fin); break;
+                case 4: launch_persistent<4>(ncu, stream, eo, nvec, k, slot_of, R, topk_weights, yo, ps, fin); break;
+                case 5: launch_persistent<5>(ncu, stream, eo, nvec, k, slot_of, R, topk_weights, yo, ps, fin); break;
+                case 6: launch_persistent<6>(ncu, stream, eo, nvec, k, slot_of, R, topk_weights, yo, ps, fin); break;
+                case 7: launch_persistent<7>(ncu, stream, eo, nvec, k, slot_of, R, topk_weights, yo, ps, fin); break;
+                default: launch_persistent<8>(ncu, stream, eo, nvec, k, slot_of, R, topk_weights, yo, ps, fin); break;
             }
             err = hipGetLastError();
             if (err != hipSuccess) return err;
@@ -434,16 +478,31 @@ hipError_t launch_combine(const ep_problem& p, const void* expert_out, const int
     }
     const dim3 grid(T, s.tiles);
     switch (k) {
-        case 1: launch_kb<1>(vpl, grid, s.threads, stream, eo, nvec, k, slot_of, R, topk_weights, yo); break;
-        case 2: launch_kb<2>(vpl, grid, s.threads, stream, eo, nvec, k, slot_of, R, topk_weights, yo); break;
-        case 3: launch_kb<3>(vpl, grid, s.threads, stream, eo, nvec, k, slot_of, R, topk_weights, yo); break;
-        case 4: launch_kb<4>(vpl, grid, s.threads, stream, eo, nvec, k, slot_of, R, topk_weights, yo); break;
-        case 5: launch_kb<5>(vpl, grid, s.threads, stream, eo, nvec, k, slot_of, R, topk_weights, yo); break;
-        case 6: launch_kb<6>(vpl, grid, s.threads, stream, eo, nvec, k, slot_of, R, topk_weights, yo); break;
-        case 7: launch_kb<7>(vpl, grid, s.threads, stream, eo, nvec, k, slot_of, R, topk_weights, yo); break;
-        default: launch_kb<8>(vpl, grid, s.threads, stream, eo, nvec, k, slot_of, R, topk_weights, yo); break;
+        case 1: launch_kb<1>(vpl, grid, s.threads, stream, eo, nvec, k, slot_of, R, topk_weights, yo, fin); break;
+        case 2: launch_kb<2>(vpl, grid, s.threads, stream, eo, nvec, k, slot_of, R, topk_weights, yo, fin); break;
+        case 3: launch_kb<3>(vpl, grid, s.threads, stream, eo, nvec, k, slot_of, R, topk_weights, yo, fin); break;
+        case 4: launch_kb<4>(vpl, grid, s.threads, stream, eo, nvec, k, slot_of, R, topk_weights, yo, fin); break;
+        case 5: launch_kb<5>(vpl, grid, s.threads, stream, eo, nvec, k, slot_of, R, topk_weights, yo, fin); break;
+        case 6: launch_kb<6>(vpl, grid, s.threads, stream, eo, nvec, k, slot_of, R, topk_weights, yo, fin); break;
+        case 7: launch_kb<7>(vpl, grid, s.threads, stream, eo, nvec, k, slot_of, R, topk_weights, yo, fin); break;
+        default: launch_kb<8>(vpl, grid, s.threads, stream, eo, nvec, k, slot_of, R, topk_weights, yo, fin); break;
     }
     return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_combine(const ep_problem& p, const void* expert_out, const int32_t* slot_of,
+                          const float* topk_weights, void* y, hipStream_t stream) {
+    return launch_forms(p, expert_out, slot_of, topk_weights, y, Plain{}, stream);
+}
+
+hipError_t launch_combine_dropout(const ep_problem& p, const void* expert_out,
+                                  const int32_t* slot_of, const float* topk_weights,
+                                  const void* residual, const DropArgs& drop, void* y,
+                                  hipStream_t stream) {
+    const Dropped fin = {drop, static_cast<const u32x4*>(residual)};
+    return launch_forms(p, expert_out, slot_of, topk_weights, y, fin, stream);
 }
 
 }  // namespace ep

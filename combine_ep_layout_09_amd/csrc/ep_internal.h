@@ -14,6 +14,7 @@ constexpr int kMaxHidden = 65536;
 constexpr int kMaxGroups = 64;
 constexpr int kMaxSeqs = 1 << 20;
 constexpr int kMaxRouted = 1 << 25;  // tokens: 64 lanes each stay below 2^32 threads
+constexpr int kMaxRowed = 1 << 21;   // tokens: 1024 lanes each stay below 2^32 threads
 
 // Workgroup width (a multiple of 64, at most 1024) and number of column tiles
 // that cover a row of nvec 16-byte pieces with vpl pieces per lane.
@@ -140,6 +141,64 @@ hipError_t launch_expert_w4(const ep_problem& p, const ep_expert_w4_t& mm, const
                             const void* row_scales, const ep_layout_t& layout,
                             const uint8_t* codes, const uint8_t* scales, void* out,
                             hipStream_t stream);
+
+// Layer norm: rows of x (and dy) a pitch apart, everything else dense.
+struct NormArgs {
+    const void* x;
+    int64_t x_stride;  // elements
+    const void* weight;
+    const void* bias;
+    void* y;
+    float* mean;
+    float* rstd;
+    int32_t num_tokens, hidden;
+    float eps;
+};
+struct NormGradArgs {
+    const void* x;
+    const void* dy;
+    int64_t x_stride, dy_stride;
+    const void* weight;
+    const float* mean;
+    const float* rstd;
+    const void* d_skip;
+    void* dx;
+    void* d_weight;
+    void* d_bias;
+    int32_t num_tokens, hidden;
+};
+int norm_parts(int num_tokens, int hidden);
+int64_t norm_workspace_bytes(int num_tokens, int hidden);
+hipError_t launch_norm(const NormArgs& a, bool x_bf16, bool w_bf16, hipStream_t stream);
+hipError_t launch_norm_grad(const NormGradArgs& a, bool x_bf16, bool w_bf16, void* workspace,
+                            hipStream_t stream);
+
+// Dropout of the combine: kept where the word is at least `border`, times `factor`.
+struct DropArgs {
+    const uint64_t* rng;  // {seed, offset}
+    uint32_t border;      // 0: nothing is dropped, rng is not read
+    float factor;
+};
+hipError_t launch_combine_dropout(const ep_problem& p, const void* expert_out,
+                                  const int32_t* slot_of, const float* topk_weights,
+                                  const void* residual, const DropArgs& drop, void* y,
+                                  hipStream_t stream);
+hipError_t launch_combine_backward(const ep_problem& p, const void* dy, const void* expert_out,
+                                   const int32_t* slot_of, const float* topk_weights,
+                                   const DropArgs& drop, void* d_expert_out, float* d_weights,
+                                   hipStream_t stream);
+
+hipError_t launch_dispatch_i8(const ep_problem& p, const void* x, const int32_t* slot_of,
+                              void* recv_q, float* recv_scales, hipStream_t stream);
+// 8-bit rows and their scales of the receive rows that an entry fills.
+hipError_t launch_quant_rows(const ep_problem& p, int K, const void* rows,
+                             const ep_layout_t& layout, int8_t* q, float* scales,
+                             hipStream_t stream);
+int64_t expert_i8_workspace_bytes(const ep_problem& p, const ep_expert_i8_t& mm);
+hipError_t launch_expert_i8(const ep_problem& p, const ep_expert_i8_t& mm, const void* rows,
+                            const float* row_scales, const ep_layout_t& layout,
+                            const int8_t* weights, const float* scales, void* out,
+                            void* workspace, hipStream_t stream);
 hipError_t launch_e4m3_encode(const float* in, uint8_t* out, int64_t n, hipStream_t stream);
 
 }  // namespace ep

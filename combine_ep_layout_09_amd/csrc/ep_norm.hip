@@ -1,0 +1,300 @@
+// ep_norm.hip -- layer norm of token rows and its backward pass.
+//
+//   y  = (x - m) r w + b,   m = mean(x),  r = 1 / sqrt(mean((x - m)^2) + eps)
+//   dx = r (a - mean(a) - n mean(a n)) + skip,   n = (x - m) r,  a = dy w
+//   dw = sum_t dy n,   db = sum_t dy
+//
+// Rows are moved in 16-byte pieces of P channels (8 bf16 or 4 fp32), at any
+// alignment that the element type allows; the last piece of a row whose length P
+// does not divide is moved channel by channel.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ep_internal.h"
+#include "ep_norm_dev.h"
+
+namespace ep {
+namespace {
+
+using namespace norm;
+
+constexpr int kMaxThreads = 1024;
+
+// Workgroups in rows of 2^20, since a dimension of a grid has to stay below 2^32
+// threads.
+__device__ __forceinline__ int64_t block_number() {
+    return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+}
+dim3 grid_of(int64_t blocks) {
+    const int64_t x = blocks < (1 << 20) ? blocks : 1 << 20;
+    return dim3(static_cast<unsigned>(x), static_cast<unsigned>((blocks + x - 1) / x));
+}
+
+// A group of L lanes (a multiple of 64 that divides the workgroup) takes a row,
+// which it holds in registers between the statistics and the output: x is read
+// once, and m is known before the squares of x - m are added.
+template <bool XB, bool WB, int VPL>
+__global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a, int L) {
+    typedef Piece<XB> X;
+    constexpr int P = X::P;
+    __shared__ float s_part[2][kMaxThreads / kWave];
+    const int group = threadIdx.x / L, l = threadIdx.x % L;
+    const int waves = L / kWave, wave0 = group * waves, wave = threadIdx.x / kWave;
+    const int64_t t = block_number() * (blockDim.x / L) + group;
+    const bool there = t < a.num_tokens;
+    const typename X::T* row = static_cast<const typename X::T*>(a.x) + (there ? t : 0) * a.x_stride;
+    X x[VPL];
+#pragma unroll
+    for (int u = 0; u < VPL; ++u) x[u].load(row, (l + u * L) * P, there ? a.hidden : 0);
+
+    float sum = 0.0f;
+#pragma unroll
+    for (int u = 0; u < VPL; ++u)
+#pragma unroll
+        for (int i = 0; i < P; ++i) sum += x[u].at(i);
+    const float m = group_sum(sum, s_part[0], wave0, waves, wave) / a.hidden;
+    float squares = 0.0f;
+#pragma unroll
+    for (int u = 0; u < VPL; ++u) {
+        const int left = a.hidden - (l + u * L) * P;  // channels from this piece on
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float d = i < left ? x[u].at(i) - m : 0.0f;
+            squares = fmaf(d, d, squares);
+        }
+    }
+    const float var = group_sum(squares, s_part[1], wave0, waves, wave) / a.hidden;
+    const float r = 1.0f / sqrtf(var + a.eps);
+    if (!there) return;
+    if (l == 0 && a.mean != nullptr) {
+        a.mean[t] = m;
+        a.rstd[t] = r;
+    }
+    typename X::T* out = static_cast<typename X::T*>(a.y) + t * a.hidden;
+#pragma unroll
+    for (int u = 0; u < VPL; ++u) {
+        const int c = (l + u * L) * P;
+        if (c >= a.hidden) continue;
+        float w[P], b[P], y[P];
+        load_params<P, WB>(a.weight, c, a.hidden, 1.0f, w);
+        load_params<P, WB>(a.bias, c, a.hidden, 0.0f, b);
+#pragma unroll
+        for (int i = 0; i < P; ++i) y[i] = fmaf((x[u].at(i) - m) * r, w[i], b[i]);
+        X::store(out, c, a.hidden, y);
+    }
+}
+
+// Gradient of the rows: a group of L lanes takes a row, reads it once for the
+// two means and once more for dx.
+template <bool XB, bool WB>
+__global__ __launch_bounds__(kMaxThreads) void norm_rows_kernel(NormGradArgs a, int L) {
+    typedef Piece<XB> X;
+    constexpr int P = X::P;
+    __shared__ float s_part[2][kMaxThreads / kWave];
+    const int group = threadIdx.x / L, l = threadIdx.x % L;
+    const int waves = L / kWave, wave0 = group * waves, wave = threadIdx.x / kWave;
+    const int64_t t = block_number() * (blockDim.x / L) + group;
+    const bool there = t < a.num_tokens;
+    const int H = there ? a.hidden : 0;
+    const int64_t at = there ? t : 0;
+    const typename X::T* xr = static_cast<const typename X::T*>(a.x) + at * a.x_stride;
+    const typename X::T* gr = static_cast<const typename X::T*>(a.dy) + at * a.dy_stride;
+    const float m = a.mean[at], r = a.rstd[at];
+    float c1 = 0.0f, c2 = 0.0f;
+    for (int c = l * P; c < H; c += L * P) {
+        X x, g;
+        x.load(xr, c, H);
+        g.load(gr, c, H);
+        float w[P];
+        load_params<P, WB>(a.weight, c, H, 1.0f, w);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float v = g.at(i) * w[i];  // 0 behind the row's end
+            c1 += v;
+            c2 = fmaf(v, (x.at(i) - m) * r, c2);
+        }
+    }
+    c1 = group_sum(c1, s_part[0], wave0, waves, wave) / a.hidden;
+    c2 = group_sum(c2, s_part[1], wave0, waves, wave) / a.hidden;
+    typename X::T* out = static_cast<typename X::T*>(a.dx) + at * a.hidden;
+    const typename X::T* skip =
+        a.d_skip == nullptr ? nullptr : static_cast<const typename X::T*>(a.d_skip) + at * a.hidden;
+    for (int c = l * P; c < H; c += L * P) {
+        X x, g, s;
+        x.load(xr, c, H);
+        g.load(gr, c, H);
+        s.load(skip, c, skip == nullptr ? 0 : H);
+        float w[P], d[P];
+        load_params<P, WB>(a.weight, c, H, 1.0f, w);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float n = (x.at(i) - m) * r;
+            d[i] = fmaf(r, fmaf(-n, c2, g.at(i) * w[i] - c1), s.at(i));
+        }
+        X::store(out, c, H, d);
+    }
+}
+
+// Sums over a run of rows for the gradients of weight and bias: a workgroup takes
+// 64 P channels, its waves the rows of the run in turns, joined in wave order.
+constexpr int kColumnWaves = 4;
+template <bool XB>
+__global__ __launch_bounds__(kColumnWaves* kWave) void norm_columns_kernel(NormGradArgs a, int run,
+                                                                           float* parts) {
+    typedef Piece<XB> X;
+    constexpr int P = X::P;
+    __shared__ float s_sum[kColumnWaves][2][kWave * P];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int c0 = blockIdx.x * kWave * P, c = c0 + lane * P;
+    const int64_t first = static_cast<int64_t>(blockIdx.y) * run;
+    const int64_t end = min(first + run, static_cast<int64_t>(a.num_tokens));
+    float dw[P], db[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) dw[i] = db[i] = 0.0f;
+    for (int64_t t = first + wave; t < end; t += kColumnWaves) {
+        X x, g;
+        x.load(static_cast<const typename X::T*>(a.x) + t * a.x_stride, c, a.hidden);
+        g.load(static_cast<const typename X::T*>(a.dy) + t * a.dy_stride, c, a.hidden);
+        const float m = a.mean[t], r = a.rstd[t];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            db[i] += g.at(i);
+            dw[i] = fmaf(g.at(i), (x.at(i) - m) * r, dw[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        s_sum[wave][0][lane * P + i] = dw[i];
+        s_sum[wave][1][lane * P + i] = db[i];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * kWave * P; i += kColumnWaves * kWave) {
+        const int which = i / (kWave * P), at = i % (kWave * P);
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kColumnWaves; ++w) s += s_sum[w][which][at];
+        if (c0 + at < a.hidden)
+            parts[(static_cast<int64_t>(blockIdx.y) * 2 + which) * a.hidden + c0 + at] = s;
+    }
+}
+
+// The parts [n][2][H] of the runs, added: 64 sums per workgroup, the parts taken
+// by its waves in turns.
+constexpr int kJoinWaves = 16;
+template <bool WB>
+__global__ __launch_bounds__(kJoinWaves* kWave) void norm_join_kernel(const float* parts, int n, int H,
+                                                                      void* dw, void* db) {
+    __shared__ float s_sum[kJoinWaves][kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int i = blockIdx.x * kWave + lane;  // of 2 H
+    float s = 0.0f;
+    if (i < 2 * H)
+        for (int p = wave; p < n; p += kJoinWaves) s += parts[static_cast<int64_t>(p) * 2 * H + i];
+    s_sum[wave][lane] = s;
+    __syncthreads();
+    if (wave != 0 || i >= 2 * H) return;
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWaves; ++w) s += s_sum[w][lane];
+    void* out = i < H ? dw : db;
+    const int c = i < H ? i : i - H;
+    if (out == nullptr) return;
+    if (WB)
+        static_cast<__bf16*>(out)[c] = static_cast<__bf16>(s);
+    else
+        static_cast<float*>(out)[c] = s;
+}
+
+// Lanes per row: as few as hold the row with at most `most` pieces each, more
+// where there are too few rows to fill the GPU.
+int lanes_per_row(int pieces, int most, int64_t tokens) {
+    int L = kWave;
+    while (L < kMaxThreads && pieces > most * L) L *= 2;
+    while (L < kMaxThreads && L < pieces && tokens * (L / kWave) < 2048) L *= 2;
+    return L;
+}
+
+template <bool XB, bool WB>
+void launch_norm_types(const NormArgs& a, hipStream_t stream) {
+    const int pieces = (a.hidden + Piece<XB>::P - 1) / Piece<XB>::P;
+    const int L = lanes_per_row(pieces, 8, a.num_tokens);
+    const int threads = L < 256 ? 256 : L;
+    const int rows = threads / L;
+    const dim3 grid = grid_of((a.num_tokens + rows - 1) / rows);
+    const auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, stream, a, L);
+    };
+    switch ((pieces + L - 1) / L) {
+        case 1: go(norm_kernel<XB, WB, 1>); break;
+        case 2: go(norm_kernel<XB, WB, 2>); break;
+        case 3: go(norm_kernel<XB, WB, 3>); break;
+        case 4: go(norm_kernel<XB, WB, 4>); break;
+        case 5: go(norm_kernel<XB, WB, 5>); break;
+        case 6: go(norm_kernel<XB, WB, 6>); break;
+        case 7: go(norm_kernel<XB, WB, 7>); break;
+        case 8: go(norm_kernel<XB, WB, 8>); break;
+        default:  // fp32 rows of more than 32768 channels
+            if constexpr (!XB) go(norm_kernel<XB, WB, 16>);
+    }
+}
+
+template <bool XB, bool WB>
+hipError_t launch_norm_grad_types(const NormGradArgs& a, void* workspace, hipStream_t stream) {
+    const int P = Piece<XB>::P;
+    const int pieces = (a.hidden + P - 1) / P;
+    if (a.num_tokens > 0) {
+        const int L = lanes_per_row(pieces, 8, a.num_tokens);
+        const int threads = L < 256 ? 256 : L;
+        const int rows = threads / L;
+        hipLaunchKernelGGL((norm_rows_kernel<XB, WB>),
+                           grid_of((a.num_tokens + rows - 1) / rows), dim3(threads), 0, stream, a, L);
+    }
+    if (a.d_weight == nullptr && a.d_bias == nullptr) return hipGetLastError();
+    float* parts = static_cast<float*>(workspace);
+    int n = 0;
+    if (a.num_tokens > 0) {
+        const int most = norm_parts(a.num_tokens, a.hidden);
+        const int run = (a.num_tokens + most - 1) / most;
+        n = (a.num_tokens + run - 1) / run;
+        hipLaunchKernelGGL((norm_columns_kernel<XB>), dim3((pieces + kWave - 1) / kWave, n),
+                           dim3(kColumnWaves * kWave), 0, stream, a, run, parts);
+    }
+    hipLaunchKernelGGL((norm_join_kernel<WB>), dim3((2 * a.hidden + kWave - 1) / kWave),
+                       dim3(kJoinWaves * kWave), 0, stream, parts, n, a.hidden, a.d_weight, a.d_bias);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// Partial sums of the gradients of weight and bias: at most one per CU, and at
+// most 2^21 channels of them.
+int norm_parts(int num_tokens, int hidden) {
+    int n = 256;
+    if (n > (1 << 21) / hidden) n = (1 << 21) / hidden;
+    return n < num_tokens ? n : num_tokens;
+}
+
+int64_t norm_workspace_bytes(int num_tokens, int hidden) {
+    const int64_t n = norm_parts(num_tokens, hidden);
+    return (n * 2 * hidden * 4 + 255) / 256 * 256;
+}
+
+hipError_t launch_norm(const NormArgs& a, bool x_bf16, bool w_bf16, hipStream_t stream) {
+    if (a.num_tokens == 0) return hipSuccess;
+    if (x_bf16 && w_bf16) launch_norm_types<true, true>(a, stream);
+    if (x_bf16 && !w_bf16) launch_norm_types<true, false>(a, stream);
+    if (!x_bf16 && w_bf16) launch_norm_types<false, true>(a, stream);
+    if (!x_bf16 && !w_bf16) launch_norm_types<false, false>(a, stream);
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_grad(const NormGradArgs& a, bool x_bf16, bool w_bf16, void* workspace,
+                            hipStream_t stream) {
+    if (x_bf16 && w_bf16) return launch_norm_grad_types<true, true>(a, workspace, stream);
+    if (x_bf16) return launch_norm_grad_types<true, false>(a, workspace, stream);
+    if (w_bf16) return launch_norm_grad_types<false, true>(a, workspace, stream);
+    return launch_norm_grad_types<false, false>(a, workspace, stream);
+}
+
+}  // namespace ep

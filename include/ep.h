@@ -13,6 +13,12 @@
  *   ep_expert_w4  receive rows -> the experts' products with 4-bit weights
  *   ep_combine  the k expert outputs of each token -> their routing-weighted
  *               sum in fp32, rounded to bf16
+ *   ep_layer_norm  token rows -> normalised rows, in front of the gate and the
+ *               dispatch; with ep_layer_norm_backward for training
+ *   ep_combine_dropout  the combine of a training step: dropout on the sum, then
+ *               the skip connection; with ep_combine_backward
+ *   ep_dispatch_i8, ep_expert_i8  dispatch and the experts' products in 8-bit
+ *               integers
  *
  * Source of the operations.  The pages this library follows are DeepEP issue
  * and pull-request threads about the multi-GPU version of this path.
@@ -360,6 +366,143 @@ typedef struct ep_expert_w4_t {
 int ep_expert_w4(const ep_problem* prob, const ep_expert_w4_t* mm, const void* rows,
                  const void* row_scales, const ep_layout_t* layout, const uint8_t* codes,
                  const uint8_t* scales, void* out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Layer norm of token rows: y = (x - m) * r * weight + bias with
+ * m = mean(x), r = 1 / sqrt(mean((x - m)^2) + eps) over the row's H channels.
+ * Statistics and sums are fp32 (m first, then the squares of x - m). */
+typedef struct ep_norm {
+    int32_t num_tokens;  /* T, 0 .. 2^25 */
+    int32_t hidden;      /* H, 1 .. 65536, any number */
+    float eps;           /* finite, >= 0 */
+} ep_norm;
+
+/*   x        [T, H], bf16 (x_bf16 = 1) or fp32 (0), device, at its own alignment (2 / 4 bytes,
+ *            as every tensor of these calls); row t starts x_stride >= H elements after row t - 1.
+ *   weight   [H], bf16 (w_bf16 = 1) or fp32 (0), device, or NULL (ones).
+ *   bias     [H], in the weight's type, device, or NULL (zeros).
+ *   y        [T, H] dense, in x's type, written; rounded once from fp32.
+ *   mean, rstd   fp32 [T], written, for the backward pass; both or neither (NULL).
+ * Outputs must not overlap inputs or each other.  T = 0 is valid and launches nothing. */
+int ep_layer_norm(const ep_norm* nm, const void* x, int x_bf16, int64_t x_stride,
+                  const void* weight, const void* bias, int w_bf16, void* y, float* mean,
+                  float* rstd, void* stream);
+
+/* Bytes of device workspace ep_layer_norm_backward needs, or -1 if the problem
+ * is invalid.  Needs no initialisation; scratch after the call.  Calls that may
+ * run at the same time, replayed graphs among them, need one each. */
+int64_t ep_layer_norm_workspace_bytes(const ep_norm* nm);
+
+/* Gradients of the rows, the weight and the bias.  With n = (x - mean) * rstd
+ * and a = dy * weight:
+ *   dx = rstd * (a - mean(a) - n * mean(a * n)) + d_skip
+ *   d_weight = sum_t dy * n,  d_bias = sum_t dy
+ *   dy        [T, H] in x's type, rows dy_stride >= H elements apart.
+ *   weight    as given to ep_layer_norm, or NULL (ones).
+ *   mean, rstd   as written by ep_layer_norm.
+ *   d_skip    [T, H] dense in x's type, or NULL: the gradient that reaches x past the norm.
+ *   dx        [T, H] dense in x's type, written.
+ *   d_weight, d_bias   [H] in the type that w_bf16 names, each written, or NULL.
+ *   workspace device scratch of at least ep_layer_norm_workspace_bytes bytes, 16-byte aligned;
+ *             may be NULL if d_weight and d_bias are.
+ * All sums are fp32 in a fixed order (equal calls give equal bits), outputs are
+ * rounded once.  Outputs must not overlap inputs or each other.  T = 0 writes zeros to d_weight
+ * and d_bias. */
+int ep_layer_norm_backward(const ep_norm* nm, const void* x, int x_bf16, int64_t x_stride,
+                           const void* dy, int64_t dy_stride, const void* weight, int w_bf16,
+                           const float* mean, const float* rstd, const void* d_skip, void* dx,
+                           void* d_weight, void* d_bias, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* ------------------------------------------------------------------------
+ * The combine of a training step: dropout on each token's combined row, then
+ * the skip connection.
+ *
+ * The mask is a function of (seed, offset, token, channel) and is never stored.
+ * Element (t, c) takes word c % 4 of Philox4x32 with ten rounds (Salmon, Moraes,
+ * Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011) at
+ * the counter {c / 4, t, low(offset), high(offset)} under the key
+ * {low(seed), high(seed)} (low and high 32-bit halves), and is kept where the
+ * word is at least p * 2^32, rounded to the nearest integer.
+ *   p     0 <= p < 1, the probability of a zero.  0: nothing is dropped.
+ *   rng   uint64 [2] {seed, offset}, device, 8-byte aligned; read when the kernel runs, so that
+ *         a replayed graph takes another mask once the program has written another offset.  NULL
+ *         only with p = 0. */
+
+/* y[t][c] = bf16_RNE( residual[t][c] + (kept ? s[t][c] * f : 0) ) with s the
+ * fp32 sum that ep_combine rounds and f = fp32(1 / (1 - p)).
+ *   residual   bf16 [T, H], device, or NULL (zeros).
+ * Other arguments as for ep_combine.  T at most 2^21.  y must not overlap the
+ * inputs. */
+int ep_combine_dropout(const ep_problem* prob, const void* expert_out, const ep_layout_t* layout,
+                       const float* topk_weights, const void* residual, double p,
+                       const uint64_t* rng, void* y, void* stream);
+
+/* Gradients of ep_combine_dropout (of ep_combine, with p = 0) in the expert rows
+ * and the routing weights; the residual's is dy itself.  With g = kept ? dy * f : 0,
+ * for every entry (t, j) with a slot:
+ *   d_expert_out[slot][c] = bf16_RNE(topk_weights[t, j] * g[t][c])
+ *   d_weights[t, j] = sum_c g[t][c] * expert_out[slot][c]      (fp32, a fixed order)
+ *   dy            bf16 [T, H], device.
+ *   expert_out    as given to ep_combine_dropout; may be NULL if d_weights is.
+ *   d_expert_out  bf16 [R, H], device.  Rows that no entry fills are not written.
+ *   d_weights     fp32 [T, k], device, written (0 for entries without a slot), or NULL.
+ * T at most 2^21.  Outputs must not overlap inputs or each other.  d_weights is what
+ * ep_route_backward takes. */
+int ep_combine_backward(const ep_problem* prob, const void* dy, const void* expert_out,
+                        const ep_layout_t* layout, const float* topk_weights, double p,
+                        const uint64_t* rng, void* d_expert_out, float* d_weights, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Dispatch and the experts' products in 8-bit integers: a row of codes q and one
+ * scale s stand for q * s.  scale = amax / 127 (one IEEE fp32 division) over the
+ * row, q = round-to-nearest-even of the fp32 quotient x / scale (another one);
+ * amax = 0 gives scale 0 and codes 0. */
+
+/* Dispatch as ep_dispatch, with 8-bit integer rows and one scale per token.
+ *   prob         use_fp8 is not read beyond the common checks.
+ *   recv_q       int8 [R, H], device.
+ *   recv_scales  fp32 [R], device, at its own alignment.
+ * Receive rows that no entry fills are not written.  x must be finite.  T at most 2^21.
+ * Outputs must not overlap inputs or each other. */
+int ep_dispatch_i8(const ep_problem* prob, const void* x, const ep_layout_t* layout, void* recv_q,
+                   float* recv_scales, void* stream);
+
+typedef struct ep_expert_i8_t {
+    int32_t in_features;   /* K, a multiple of 16, 16 .. 65536 */
+    int32_t out_features;  /* N, 1 .. 65536 */
+    int32_t in_format;     /* rows: 0 bf16 (finite), quantised by the call as above;
+                              1 int8 with one scale per row */
+    int32_t activation;    /* 0: out = y, weights [E, N, K].
+                              1: out = silu(gate) * up, weights [E, 2N, K], as ep_expert_w4_t */
+} ep_expert_i8_t;
+
+/* Bytes of device workspace ep_expert_i8 needs (0 for in_format 1), or -1 if the
+ * problem is invalid.  Needs no initialisation; scratch after the call.  Calls
+ * that may run at the same time, replayed graphs among them, need one each. */
+int64_t ep_expert_i8_workspace_bytes(const ep_problem* prob, const ep_expert_i8_t* mm);
+
+/* y[r, n] = fp32(sum_k q[r, k] * weight[e, n, k]) * row_scale[r] * scales[e, n] for
+ * every receive row r that an entry of expert e fills.  The sum is exact, in 32-bit
+ * integers; then two fp32 products, from the left, and one rounding to bf16.  Rows that
+ * no entry fills are neither read nor written.
+ *   prob        T, k, E and capacity of the layout; hidden and use_fp8 are not read beyond
+ *               the common checks.
+ *   rows        [R, K] bf16 or int8, in the receive-row layout (ep_dispatch_i8's recv_q, or
+ *               another product's out).
+ *   row_scales  fp32 [R] (in_format 1), at its own alignment; ignored for 0.
+ *   layout      as written by ep_layout for the same problem.
+ *   weights     int8 [E, N or 2N, K].
+ *   scales      fp32 [E, N or 2N], at its own alignment.
+ *   out         bf16 [R, N]; must not overlap the inputs or the workspace.
+ *   workspace   device scratch of at least ep_expert_i8_workspace_bytes bytes, 16-byte aligned;
+ *               may be NULL for in_format 1.
+ * The weights of an expert that no entry names are not read.  Data pointers
+ * are 16-byte aligned. */
+int ep_expert_i8(const ep_problem* prob, const ep_expert_i8_t* mm, const void* rows,
+                 const float* row_scales, const ep_layout_t* layout, const int8_t* weights,
+                 const float* scales, void* out, void* workspace, size_t workspace_bytes,
+                 void* stream);
 
 /* Static text for a status code. */
 const char* ep_strerror(int code);
