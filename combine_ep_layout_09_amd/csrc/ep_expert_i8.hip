@@ -14,6 +14,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ep_device.h"
 #include "ep_expert_dev.h"
 #include "ep_internal.h"
@@ -143,6 +145,166 @@ __global__ __launch_bounds__(WAVES* kWave, 4) void expert_i8_kernel(Args a) {
     }
 }
 
+// Many rows per expert: a workgroup of eight waves takes 256 weight rows (GATED: 128
+// of the gate and the 128 of up that belong to them) against up to 64 XT rows, a wave
+// 128 of the former against 16 XT of the latter.  Stages of 128 channels pass through LDS in turns of
+// two buffers, written by the loads themselves; a stage is loaded while the one
+// before it is multiplied.
+//
+// A stage's row is 128 bytes, eight pieces; piece q of row r lies at place
+// q ^ (r % 8), so that the 16 rows a fragment takes the same piece of are in
+// different banks.  A load instruction fills 1 KB of LDS in lane order, eight
+// rows, so its lanes fetch the pieces in that order.
+constexpr int kTileWaves = 8;
+constexpr int kTileW = 256;  // weight rows of a workgroup
+
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t from, u32x4* to, uint32_t at,
+                                         uint32_t step) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        from, reinterpret_cast<__attribute__((address_space(3))) void*>(reinterpret_cast<uintptr_t>(to)),
+        16, at, step, 0, 0);
+}
+
+template <int XT, bool GATED>
+__global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Args a) {
+    constexpr int MC = 64 * XT;
+    constexpr int kOut = GATED ? kTileW / 2 : kTileW;  // outputs of a workgroup
+    constexpr int WT = 8;                              // 16-row weight tiles of a wave
+    __shared__ u32x4 s_w[2][kTileW * 8];
+    __shared__ u32x4 s_x[2][MC * 8];
+
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int r16 = lane % 16, group = lane / 16;
+    const uint32_t K = a.K;
+    const int N = a.N;
+    // Workgroups go round the 8 XCDs in turn.  Each XCD takes a run of items
+    // (row tile, output block), so that its L2 serves one tile's rows to that
+    // tile's blocks, and one expert's weights to that expert's tiles.
+    const uint32_t n_blocks = (N + kOut - 1) / kOut;
+    const uint64_t id = static_cast<uint64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+    uint32_t block = 0;
+    const Found f = find_tile<MC>(a, [&](uint32_t tiles) {
+        const uint64_t items = static_cast<uint64_t>(tiles) * n_blocks;
+        const uint64_t run = (items + 7) / 8;
+        const uint64_t item = id % 8 * run + id / 8;
+        if (id / 8 >= run || item >= items) return 0xffffffffu;
+        block = static_cast<uint32_t>(item % n_blocks);
+        return static_cast<uint32_t>(item / n_blocks);
+    });
+    if (f.expert < 0) return;
+    const int n0 = block * kOut;
+    const int here = N - n0 < kOut ? N - n0 : kOut;
+    const int m0 = f.tile * MC;
+    const int rows_here = f.count - m0 < MC ? f.count - m0 : MC;
+    if (rows_here <= 0) return;
+    const int64_t row0 = f.start + m0;
+
+    // Loads: wave i fills weight rows 32 i .. 32 i + 31 and rows 8 XT i .. of the
+    // buffers.  GATED: of each 128 weight rows 64 are gate and 64 up.
+    const int64_t w_row = static_cast<int64_t>(f.expert) * (GATED ? 2 * N : N) + n0;
+    const bool up = GATED && wave % 4 >= 2;
+    const auto w_view = view(a.weights + (w_row + (up ? N : 0)) * K, here * K);
+    const auto x_view = view(a.rows + row0 * K, rows_here * K);
+    const uint32_t piece = (lane % 8 ^ lane / 8) * 16;
+    const uint32_t w_first = (GATED ? wave / 4 * 64 + wave % 2 * 32 : wave * 32) + lane / 8;
+    const uint32_t w_at = w_first * K + piece;
+    const uint32_t x_at = (wave * 8 * XT + lane / 8) * K + piece;
+    const auto load = [&](uint32_t c, int buf) {  // channels c .. c + 127; zeros past the end
+        const bool has = c + piece < K;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            load_lds(w_view, &s_w[buf][(wave * 32 + i * 8) * 8], has ? w_at + i * 8 * K : kNowhere, c);
+#pragma unroll
+        for (int i = 0; i < XT; ++i)
+            load_lds(x_view, &s_x[buf][(wave * 8 * XT + i * 8) * 8], has ? x_at + i * 8 * K : kNowhere,
+                     c);
+    };
+
+    // Products: waves 0-3 take the first half of the rows, so that a tile that
+    // is at most half full costs each SIMD half.
+    const int w_half = wave % 2, x_group = wave / 2;
+    const bool idle = rows_here <= x_group * 16 * XT;
+    const int place = r16 * 8 + (group ^ r16 % 8);  // of chunk 0; chunk 1: place ^ 4
+    i32x4 acc[WT][XT];
+#pragma unroll
+    for (int t = 0; t < WT; ++t)
+#pragma unroll
+        for (int m = 0; m < XT; ++m) acc[t][m] = i32x4{0, 0, 0, 0};
+    const auto multiply = [&](int buf) {
+        const u32x4* w = &s_w[buf][w_half * 128 * 8];
+        const u32x4* x = &s_x[buf][x_group * 16 * XT * 8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            u32x4 wf[WT], xf[XT];
+#pragma unroll
+            for (int m = 0; m < XT; ++m) xf[m] = x[m * 128 + (place ^ 4 * h)];
+#pragma unroll
+            for (int t = 0; t < WT; ++t) wf[t] = w[t * 128 + (place ^ 4 * h)];
+#pragma unroll
+            for (int t = 0; t < WT; ++t)
+#pragma unroll
+                for (int m = 0; m < XT; ++m) acc[t][m] = mfma(wf[t], xf[m], acc[t][m]);
+        }
+    };
+
+    load(0, 0);
+    for (uint32_t c = 0; c < K; c += 2 * kStep) {
+        __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+        __syncthreads();
+        if (c + kStep < K) load(c + kStep, 1);
+        if (!idle) multiply(0);
+        if (c + kStep >= K) break;
+        __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+        __syncthreads();
+        if (c + 2 * kStep < K) load(c + 2 * kStep, 0);
+        if (!idle) multiply(1);
+    }
+    if (idle) return;
+
+    // lane l holds outputs 4 * (l / 16) .. + 3 of a tile for row l % 16
+    constexpr int OT = GATED ? WT / 2 : WT;
+#pragma unroll
+    for (int m = 0; m < XT; ++m) {
+        const int r = (x_group * XT + m) * 16 + r16;
+        if (r >= rows_here) continue;
+        const float row_scale = a.row_scales[row0 + r];
+#pragma unroll
+        for (int t = 0; t < OT; ++t) {
+            const int n = (w_half * OT + t) * 16 + group * 4;
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = n + i < here ? n + i : 0;
+                float v = scaled(acc[t][m][i], row_scale, a.scales[w_row + at]);
+                if constexpr (GATED)
+                    v = v / (1.0f + expf(-v)) *
+                        scaled(acc[t + OT][m][i], row_scale, a.scales[w_row + N + at]);
+                y[i] = f32_to_bf16_rne(v);
+            }
+            uint16_t* to = a.out + (row0 + r) * N + n0 + n;
+            if (N % 4 == 0) {
+                if (n < here)
+                    *reinterpret_cast<uint2*>(to) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n + i < here) to[i] = static_cast<uint16_t>(y[i]);
+            }
+        }
+    }
+}
+
+template <int XT, bool GATED>
+void launch_many(const Args& a, int64_t tiles, hipStream_t stream) {
+    const int outs = GATED ? kTileW / 2 : kTileW;
+    const int64_t blocks = (a.N + outs - 1) / outs;
+    const int64_t items = (tiles * blocks + 7) / 8 * 8;  // a row of ids whose length 8 divides
+    const int64_t x = items < (1 << 20) ? items : 1 << 20;
+    const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>((items + x - 1) / x));
+    hipLaunchKernelGGL((expert_i8_tile_kernel<XT, GATED>), grid, dim3(kTileWaves * kWave), 0, stream, a);
+}
+
 template <int WAVES, bool GATED>
 void launch_few(const Args& a, int64_t tiles, hipStream_t stream) {
     const int outs = GATED ? kRows / 2 : kRows;
@@ -198,11 +360,23 @@ hipError_t launch_expert_i8(const ep_problem& p, const ep_expert_i8_t& mm, const
     // Row tiles: no more than one per expert that can have rows, plus one per
     // full tile.
     const int64_t experts = p.num_experts < filled ? p.num_experts : filled;
-    const int64_t tiles = experts + filled / 16;
+    const int64_t mean = filled / experts;
+    const auto tiles = [&](int mc) { return experts + filled / mc; };
+    const auto go = [&](auto gated) {
+        constexpr bool kGated = decltype(gated)::value;
+        if (mean > 128)
+            launch_many<4, kGated>(a, tiles(256), stream);
+        else if (mean > 64)
+            launch_many<2, kGated>(a, tiles(128), stream);
+        else if (mean > 16)
+            launch_many<1, kGated>(a, tiles(64), stream);
+        else
+            launch_few<4, kGated>(a, tiles(16), stream);
+    };
     if (mm.activation == 1)
-        launch_few<4, true>(a, tiles, stream);
+        go(std::true_type{});
     else
-        launch_few<4, false>(a, tiles, stream);
+        go(std::false_type{});
     return hipGetLastError();
 }
 
