@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
                     const float lo = bf16_lo(gi) * drop.factor, hi = bf16_hi(gi) * drop.factor;
                     sum = fmaf(lo, bf16_lo(e[i]), sum);
                     sum = fmaf(hi, bf16_hi(e[i]), sum);
-                    d[i] = norm::pack_bf16(lo * w, hi * w);
+                    d[i] = pack_bf16(lo * w, hi * w);
                 }
                 __builtin_nontemporal_store(d, deo + at);
             }

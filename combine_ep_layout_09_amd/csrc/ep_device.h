@@ -54,6 +54,15 @@ __device__ __forceinline__ uint32_t f32_to_bf16_rne(float f) {
     return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
 }
 
+// Two fp32 values -> bf16 bits (RNE), the first in the low half: one instruction.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    bf16x2 v;
+    v[0] = static_cast<__bf16>(a);
+    v[1] = static_cast<__bf16>(b);
+    return __builtin_bit_cast(uint32_t, v);
+}
+
 // fp32 -> OCP E4M3FN code, round to nearest even, saturating to +-448, sign
 // kept on zero.  Input must not be NaN.
 //   |v| >= 448            -> 0x7E (everything from 448 up rounds to 448 once

@@ -52,6 +52,13 @@ __device__ __forceinline__ float scaled(int32_t sum, float row, float channel) {
     return static_cast<float>(sum) * row * channel;
 }
 
+// silu(v) = v / (1 + exp(-v)) with the hardware's exponential and reciprocal, a step of
+// fp32 each, far below bf16's: a division and expf for each of a tile's outputs
+// took a sixth of the many-row kernel's time.
+__device__ __forceinline__ float silu(float v) {
+    return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504f));
+}
+
 // One step's operands of a wave.
 struct Stage {
     u32x4 w[2][kTiles];
@@ -140,7 +147,7 @@ __global__ __launch_bounds__(WAVES* kWave, 4) void expert_i8_kernel(Args a) {
         }
         const float row_scale = a.row_scales[row0 + m];
         float y = scaled(sum, row_scale, a.scales[w_row + n]);
-        if constexpr (GATED) y = y / (1.0f + expf(-y)) * scaled(up_sum, row_scale, a.scales[up_row + n]);
+        if constexpr (GATED) y = silu(y) * scaled(up_sum, row_scale, a.scales[up_row + n]);
         a.out[(row0 + m) * N + n0 + n] = static_cast<uint16_t>(f32_to_bf16_rne(y));
     }
 }
@@ -172,6 +179,8 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
     constexpr int WT = 8;                              // 16-row weight tiles of a wave
     __shared__ u32x4 s_w[2][kTileW * 8];
     __shared__ u32x4 s_x[2][MC * 8];
+    __shared__ float s_scale[kTileW];  // of the weight rows, in the buffers' order
+    __shared__ float s_row[MC];
 
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -249,6 +258,17 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
     };
 
     load(0, 0);
+    {
+        // the scales that the products take at the end
+        const int i = threadIdx.x % kTileW;
+        const int n = GATED ? i / 128 * 64 + i % 64 : i;
+        const int64_t from = w_row + (GATED && i % 128 >= 64 ? N : 0) + n;
+        if (threadIdx.x < kTileW) {
+            s_scale[i] = n < here ? a.scales[from] : 0.0f;
+        } else if (i < MC) {
+            s_row[i] = i < rows_here ? a.row_scales[row0 + i] : 0.0f;
+        }
+    }
     for (uint32_t c = 0; c < K; c += 2 * kStep) {
         __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
         __syncthreads();
@@ -264,32 +284,33 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
 
     // lane l holds outputs 4 * (l / 16) .. + 3 of a tile for row l % 16
     constexpr int OT = GATED ? WT / 2 : WT;
+    const float* scale = &s_scale[w_half * 128 + group * 4];
+    const bool whole = N % 4 == 0;
 #pragma unroll
     for (int m = 0; m < XT; ++m) {
         const int r = (x_group * XT + m) * 16 + r16;
         if (r >= rows_here) continue;
-        const float row_scale = a.row_scales[row0 + r];
+        const float row_scale = s_row[r];
+        uint16_t* row = a.out + (row0 + r) * N + n0;
 #pragma unroll
         for (int t = 0; t < OT; ++t) {
             const int n = (w_half * OT + t) * 16 + group * 4;
-            uint32_t y[4];
+            float y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int at = n + i < here ? n + i : 0;
-                float v = scaled(acc[t][m][i], row_scale, a.scales[w_row + at]);
+                y[i] = scaled(acc[t][m][i], row_scale, scale[t * 16 + i]);
                 if constexpr (GATED)
-                    v = v / (1.0f + expf(-v)) *
-                        scaled(acc[t + OT][m][i], row_scale, a.scales[w_row + N + at]);
-                y[i] = f32_to_bf16_rne(v);
+                    y[i] = silu(y[i]) *
+                           scaled(acc[t + OT][m][i], row_scale, scale[(t + OT) * 16 + i]);
             }
-            uint16_t* to = a.out + (row0 + r) * N + n0 + n;
-            if (N % 4 == 0) {
-                if (n < here)
-                    *reinterpret_cast<uint2*>(to) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
+            const uint32_t lo = pack_bf16(y[0], y[1]), hi = pack_bf16(y[2], y[3]);
+            if (whole) {
+                if (n < here) *reinterpret_cast<uint2*>(row + n) = make_uint2(lo, hi);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (n + i < here) to[i] = static_cast<uint16_t>(y[i]);
+                    if (n + i < here)
+                        row[n + i] = static_cast<uint16_t>((i < 2 ? lo : hi) >> (16 * (i & 1)));
             }
         }
     }

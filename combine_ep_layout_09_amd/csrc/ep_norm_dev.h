@@ -11,16 +11,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
 typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
-// Two fp32 values -> bf16 bits (RNE), the first in the low half.
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    bf16x2 v;
-    v[0] = static_cast<__bf16>(a);
-    v[1] = static_cast<__bf16>(b);
-    return __builtin_bit_cast(uint32_t, v);
-}
-
 // 16 bytes of a row: P channels from c on, 0 behind the row's end.
 template <bool BF16>
 struct Piece;
