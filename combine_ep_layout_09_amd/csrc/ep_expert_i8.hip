@@ -154,16 +154,21 @@ __global__ __launch_bounds__(WAVES* kWave, 4) void expert_i8_kernel(Args a) {
 
 // Many rows per expert: a workgroup of eight waves takes 256 weight rows (GATED: 128
 // of the gate and the 128 of up that belong to them) against up to 64 XT rows, a wave
-// 128 of the former against 16 XT of the latter.  Stages of 128 channels pass through LDS in turns of
-// two buffers, written by the loads themselves; a stage is loaded while the one
-// before it is multiplied.
+// 128 of the former against 16 XT of the latter.  Stages of 128 channels pass
+// through LDS, written by the loads themselves.
 //
 // A stage's row is 128 bytes, eight pieces; piece q of row r lies at place
 // q ^ (r % 8), so that the 16 rows a fragment takes the same piece of are in
 // different banks.  A load instruction fills 1 KB of LDS in lane order, eight
 // rows, so its lanes fetch the pieces in that order.
+//
+// What is in flight bounds the loads, so LDS holds as much as fits: three stages of
+// weights and, at XT = 4, two of rows, 160 KB in all.  Weights, which mostly come
+// from HBM, are loaded two stages ahead, rows, which other workgroups of the XCD
+// read as well, one.
 constexpr int kTileWaves = 8;
 constexpr int kTileW = 256;  // weight rows of a workgroup
+constexpr int kTileGroup = 8;
 
 __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t from, u32x4* to, uint32_t at,
                                          uint32_t step) {
@@ -177,10 +182,9 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
     constexpr int MC = 64 * XT;
     constexpr int kOut = GATED ? kTileW / 2 : kTileW;  // outputs of a workgroup
     constexpr int WT = 8;                              // 16-row weight tiles of a wave
-    __shared__ u32x4 s_w[2][kTileW * 8];
-    __shared__ u32x4 s_x[2][MC * 8];
-    __shared__ float s_scale[kTileW];  // of the weight rows, in the buffers' order
-    __shared__ float s_row[MC];
+    constexpr int WB = 3, XB = XT == 4 ? 2 : 3;        // stages held
+    __shared__ u32x4 s_w[WB * kTileW * 8];
+    __shared__ u32x4 s_x[XB * MC * 8];
 
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -188,12 +192,14 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
     const uint32_t K = a.K;
     const int N = a.N;
     // Workgroups go round the 8 XCDs in turn.  Each XCD takes a run of items
-    // (row tile, output block), so that its L2 serves one tile's rows to that
-    // tile's blocks, and one expert's weights to that expert's tiles.
+    // (row tile, output block), so that its L2 serves one expert's weights to that
+    // expert's tiles and one tile's rows to that tile's blocks.  Up to kTileGroup row
+    // tiles of an expert take a block in turn before the next block: the weights,
+    // the larger part, are then read by all of them at about the same time.
     const uint32_t n_blocks = (N + kOut - 1) / kOut;
     const uint64_t id = static_cast<uint64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
     uint32_t block = 0;
-    const Found f = find_tile<MC>(a, [&](uint32_t tiles) {
+    Found f = find_tile<MC>(a, [&](uint32_t tiles) {
         const uint64_t items = static_cast<uint64_t>(tiles) * n_blocks;
         const uint64_t run = (items + 7) / 8;
         const uint64_t item = id % 8 * run + id / 8;
@@ -202,6 +208,13 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
         return static_cast<uint32_t>(item / n_blocks);
     });
     if (f.expert < 0) return;
+    {
+        const int first = f.tile / kTileGroup * kTileGroup, left = (f.count + MC - 1) / MC - first;
+        const uint32_t held = left < kTileGroup ? left : kTileGroup;
+        const uint32_t item = (f.tile - first) * n_blocks + block;
+        f.tile = first + item % held;
+        block = item / held;
+    }
     const int n0 = block * kOut;
     const int here = N - n0 < kOut ? N - n0 : kOut;
     const int m0 = f.tile * MC;
@@ -209,8 +222,8 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
     if (rows_here <= 0) return;
     const int64_t row0 = f.start + m0;
 
-    // Loads: wave i fills weight rows 32 i .. 32 i + 31 and rows 8 XT i .. of the
-    // buffers.  GATED: of each 128 weight rows 64 are gate and 64 up.
+    // Loads: wave i fills weight rows 32 i .. 32 i + 31 and rows 8 XT i .. of a
+    // stage.  GATED: of each 128 weight rows 64 are gate and 64 up.
     const int64_t w_row = static_cast<int64_t>(f.expert) * (GATED ? 2 * N : N) + n0;
     const bool up = GATED && wave % 4 >= 2;
     const auto w_view = view(a.weights + (w_row + (up ? N : 0)) * K, here * K);
@@ -219,15 +232,20 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
     const uint32_t w_first = (GATED ? wave / 4 * 64 + wave % 2 * 32 : wave * 32) + lane / 8;
     const uint32_t w_at = w_first * K + piece;
     const uint32_t x_at = (wave * 8 * XT + lane / 8) * K + piece;
-    const auto load = [&](uint32_t c, int buf) {  // channels c .. c + 127; zeros past the end
+    // channels c .. c + 127; zeros past the end, where nothing is read
+    const auto load_w = [&](uint32_t c, int buf) {
         const bool has = c + piece < K;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            load_lds(w_view, &s_w[buf][(wave * 32 + i * 8) * 8], has ? w_at + i * 8 * K : kNowhere, c);
+            load_lds(w_view, &s_w[(buf * kTileW + wave * 32 + i * 8) * 8],
+                     has ? w_at + i * 8 * K : kNowhere, c);
+    };
+    const auto load_x = [&](uint32_t c, int buf) {
+        const bool has = c + piece < K;
 #pragma unroll
         for (int i = 0; i < XT; ++i)
-            load_lds(x_view, &s_x[buf][(wave * 8 * XT + i * 8) * 8], has ? x_at + i * 8 * K : kNowhere,
-                     c);
+            load_lds(x_view, &s_x[(buf * MC + wave * 8 * XT + i * 8) * 8],
+                     has ? x_at + i * 8 * K : kNowhere, c);
     };
 
     // Products: waves 0-3 take the first half of the rows, so that a tile that
@@ -240,57 +258,96 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
     for (int t = 0; t < WT; ++t)
 #pragma unroll
         for (int m = 0; m < XT; ++m) acc[t][m] = i32x4{0, 0, 0, 0};
-    const auto multiply = [&](int buf) {
-        const u32x4* w = &s_w[buf][w_half * 128 * 8];
-        const u32x4* x = &s_x[buf][x_group * 16 * XT * 8];
+    struct Frags {
+        u32x4 w[WT], x[XT];
+    };
+    const auto fetch = [&](Frags& f, int w_buf, int x_buf, int h) {  // chunk h of a stage
+        const u32x4* w = &s_w[(w_buf * kTileW + w_half * 128) * 8];
+        const u32x4* x = &s_x[(x_buf * MC + x_group * 16 * XT) * 8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            u32x4 wf[WT], xf[XT];
+        for (int m = 0; m < XT; ++m) f.x[m] = x[m * 128 + (place ^ 4 * h)];
 #pragma unroll
-            for (int m = 0; m < XT; ++m) xf[m] = x[m * 128 + (place ^ 4 * h)];
+        for (int t = 0; t < WT; ++t) f.w[t] = w[t * 128 + (place ^ 4 * h)];
+    };
+    const auto multiply = [&](const Frags& f) {
 #pragma unroll
-            for (int t = 0; t < WT; ++t) wf[t] = w[t * 128 + (place ^ 4 * h)];
+        for (int t = 0; t < WT; ++t)
 #pragma unroll
-            for (int t = 0; t < WT; ++t)
-#pragma unroll
-                for (int m = 0; m < XT; ++m) acc[t][m] = mfma(wf[t], xf[m], acc[t][m]);
-        }
+            for (int m = 0; m < XT; ++m) acc[t][m] = mfma(f.w[t], f.x[m], acc[t][m]);
     };
 
-    load(0, 0);
+    // The scales that the products take at the end, one per thread.
+    float scale = 0.0f;
     {
-        // the scales that the products take at the end
         const int i = threadIdx.x % kTileW;
         const int n = GATED ? i / 128 * 64 + i % 64 : i;
-        const int64_t from = w_row + (GATED && i % 128 >= 64 ? N : 0) + n;
         if (threadIdx.x < kTileW) {
-            s_scale[i] = n < here ? a.scales[from] : 0.0f;
-        } else if (i < MC) {
-            s_row[i] = i < rows_here ? a.row_scales[row0 + i] : 0.0f;
+            if (n < here) scale = a.scales[w_row + (GATED && i % 128 >= 64 ? N : 0) + n];
+        } else if (i < rows_here) {
+            scale = a.row_scales[row0 + i];
         }
     }
-    for (uint32_t c = 0; c < K; c += 2 * kStep) {
-        __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-        __syncthreads();
-        if (c + kStep < K) load(c + kStep, 1);
-        if (!idle) multiply(0);
-        if (c + kStep >= K) break;
-        __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-        __syncthreads();
-        if (c + 2 * kStep < K) load(c + 2 * kStep, 0);
-        if (!idle) multiply(1);
+    // A wave's loads end in order: waiting until only the newest are left waits for
+    // a stage's own.  Where every wave has waited, all of the stage is in LDS, and
+    // the buffers that the waves are done with are free.  (A barrier that does not wait
+    // for the loads behind it, which __syncthreads does.)
+    constexpr int kAhead = XB == 3 ? 4 + XT : 4;  // loads of the stage ahead
+    const auto stage_ready = [&] {
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(kAhead, 7, 0));
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    load_x(0, 0);
+    load_w(0, 0);
+    load_x(kStep, 1);
+    load_w(kStep, 1);
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(4 + XT, 7, 15));
+    if constexpr (XB == 3) load_x(2 * kStep, 2);
+    load_w(2 * kStep, 2);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    // Each chunk's fragments are fetched while the chunk before is multiplied.
+    int w_buf = 0, x_buf = 0;
+    Frags even, odd;
+    if (!idle) fetch(even, 0, 0, 0);
+    for (uint32_t c = 0; c < K; c += kStep) {
+        const int w_next = w_buf == WB - 1 ? 0 : w_buf + 1, x_next = x_buf == XB - 1 ? 0 : x_buf + 1;
+        if (!idle) {
+            fetch(odd, w_buf, x_buf, 1);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(even);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        stage_ready();  // the next one; this one's buffers are free
+        load_x(c + XB * kStep, x_buf);
+        load_w(c + WB * kStep, w_buf);
+        if (!idle) {
+            fetch(even, w_next, x_next, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(odd);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        w_buf = w_next;
+        x_buf = x_next;
     }
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // loads of nothing, but into LDS
+    __syncthreads();
+    float* s_scale = reinterpret_cast<float*>(s_w);  // of the weight rows, then of the rows
+    s_scale[threadIdx.x] = scale;
+    __syncthreads();
     if (idle) return;
 
     // lane l holds outputs 4 * (l / 16) .. + 3 of a tile for row l % 16
     constexpr int OT = GATED ? WT / 2 : WT;
-    const float* scale = &s_scale[w_half * 128 + group * 4];
+    const float* w_scale = &s_scale[w_half * 128 + group * 4];
     const bool whole = N % 4 == 0;
 #pragma unroll
     for (int m = 0; m < XT; ++m) {
         const int r = (x_group * XT + m) * 16 + r16;
         if (r >= rows_here) continue;
-        const float row_scale = s_row[r];
+        const float row_scale = s_scale[kTileW + r];
         uint16_t* row = a.out + (row0 + r) * N + n0;
 #pragma unroll
         for (int t = 0; t < OT; ++t) {
@@ -298,10 +355,10 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
             float y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                y[i] = scaled(acc[t][m][i], row_scale, scale[t * 16 + i]);
+                y[i] = scaled(acc[t][m][i], row_scale, w_scale[t * 16 + i]);
                 if constexpr (GATED)
                     y[i] = silu(y[i]) *
-                           scaled(acc[t + OT][m][i], row_scale, scale[(t + OT) * 16 + i]);
+                           scaled(acc[t + OT][m][i], row_scale, w_scale[(t + OT) * 16 + i]);
             }
             const uint32_t lo = pack_bf16(y[0], y[1]), hi = pack_bf16(y[2], y[3]);
             if (whole) {
