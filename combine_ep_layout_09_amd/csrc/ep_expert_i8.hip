@@ -165,16 +165,26 @@ __global__ __launch_bounds__(WAVES* kWave, 4) void expert_i8_kernel(Args a) {
 // What is in flight bounds the loads, so LDS holds as much as fits: three stages of
 // weights and, at XT = 4, two of rows, 160 KB in all.  Weights, which mostly come
 // from HBM, are loaded two stages ahead, rows, which other workgroups of the XCD
-// read as well, one.
+// read as well, one.  (Loads alone at XT 2, 8192 skewed tokens over 64 experts: 721 us one
+// stage ahead, 515 two.)  Up to XT 2 an expert mostly has one row tile, so its
+// weights are not kept in the caches (24 rows each: 140 us, kept 151).
+//
+// That batch, K 4096, N 1408 gated: 566 us, 2.0 POP/s of its own rows and 2.2 with the
+// tiles' empty ones; an 8192^3 int8 library product reaches 2.06.  The matrix cores are
+// busy for 47 % of the time, at 2.03 GHz; without loads it takes 435 us, without
+// products 449.  4096 tokens over 256 experts, K 7168, N 2048 gated: 1529 us, the
+// weights at 5.2 TB/s.  Matrix instructions of 32 x 32 x 32 were slower (625 us), and so
+// was a stage through registers (648 where this took 596).
 constexpr int kTileWaves = 8;
 constexpr int kTileW = 256;  // weight rows of a workgroup
 constexpr int kTileGroup = 8;
 
+template <bool ONCE>  // not kept in the caches
 __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t from, u32x4* to, uint32_t at,
                                          uint32_t step) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         from, reinterpret_cast<__attribute__((address_space(3))) void*>(reinterpret_cast<uintptr_t>(to)),
-        16, at, step, 0, 0);
+        16, at, step, 0, ONCE ? 2 : 0);
 }
 
 template <int XT, bool GATED>
@@ -237,14 +247,14 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
         const bool has = c + piece < K;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            load_lds(w_view, &s_w[(buf * kTileW + wave * 32 + i * 8) * 8],
+            load_lds<XT != 4>(w_view, &s_w[(buf * kTileW + wave * 32 + i * 8) * 8],
                      has ? w_at + i * 8 * K : kNowhere, c);
     };
     const auto load_x = [&](uint32_t c, int buf) {
         const bool has = c + piece < K;
 #pragma unroll
         for (int i = 0; i < XT; ++i)
-            load_lds(x_view, &s_x[(buf * MC + wave * 8 * XT + i * 8) * 8],
+            load_lds<false>(x_view, &s_x[(buf * MC + wave * 8 * XT + i * 8) * 8],
                      has ? x_at + i * 8 * K : kNowhere, c);
     };
 
@@ -440,16 +450,34 @@ hipError_t launch_expert_i8(const ep_problem& p, const ep_expert_i8_t& mm, const
     const int64_t experts = p.num_experts < filled ? p.num_experts : filled;
     const int64_t mean = filled / experts;
     const auto tiles = [&](int mc) { return experts + filled / mc; };
+    // By the mean rows of an expert, measured at 64 experts, K 4096, N 1408 gated (us):
+    //   rows   8    12   16   24   48   64   75   96   112  121  128
+    //   few    122  135  168  231  379
+    //   XT 1   127  137  128  140  139  163  192
+    //   XT 2   128  138  129  142  140  146  153  156  168  183  215
+    //   XT 4                                 162  162  177  172  180
+    // Larger row tiles and the many-row kernel's 256 weight rows make fewer
+    // workgroups.  Where they do not give nearly every CU one, the next smaller tile
+    // wins (8 experts, K 4096: N 704 gated, 250 rows each: 90 workgroups of XT 4 49 us,
+    // 138 of XT 2 35, 234 of XT 1 29; 1000 rows each: 234 of XT 4 53, XT 2 68), and the
+    // few-row kernel where the CUs hold all of its workgroups at once (32 experts of 25
+    // rows, N 167: 246 of them 14 us, XT 1 22; 8 of 16, K 2048, N 1024: 256, 9 and 15;
+    // 32 of 100, N 167: 696, 35 and 24).
+    const int64_t rows2 = static_cast<int64_t>(a.N) * (mm.activation == 1 ? 2 : 1);
+    const auto workgroups = [&](int mc, int w_rows) {
+        return tiles(mc) * ((rows2 + w_rows - 1) / w_rows);
+    };
+    constexpr int kEnough = 200;
     const auto go = [&](auto gated) {
         constexpr bool kGated = decltype(gated)::value;
-        if (mean > 128)
-            launch_many<4, kGated>(a, tiles(256), stream);
-        else if (mean > 64)
-            launch_many<2, kGated>(a, tiles(128), stream);
-        else if (mean > 16)
-            launch_many<1, kGated>(a, tiles(64), stream);
-        else
+        if (mean <= 12 || workgroups(16, kRows) <= 512)
             launch_few<4, kGated>(a, tiles(16), stream);
+        else if (mean > 116 && workgroups(256, kTileW) >= kEnough)
+            launch_many<4, kGated>(a, tiles(256), stream);
+        else if (mean > 48 && workgroups(128, kTileW) >= kEnough)
+            launch_many<2, kGated>(a, tiles(128), stream);
+        else
+            launch_many<1, kGated>(a, tiles(64), stream);
     };
     if (mm.activation == 1)
         go(std::true_type{});
