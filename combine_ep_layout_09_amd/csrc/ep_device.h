@@ -43,6 +43,19 @@ __device__ __forceinline__ uint64_t match_peers(uint32_t key, int nbits, uint64_
     return m;
 }
 
+// Bounded view of `bytes` bytes at p: loads past its end give 0 and touch
+// nothing.  A lane's own offset alone has to say so, since the step's offset,
+// the same in every lane, need not count in that check.  p and bytes are the same
+// in every lane, and said to be: a view in vector registers is loaded through in a
+// loop over its values.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t view(const void* p, uint32_t bytes) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint64_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+    const uint64_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(hi << 32 | (lo & 0xffffffffu)),
+                                             0, __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+}
+
 // bf16 bit patterns (two per 32-bit word, low half first) -> fp32, exact.
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }

@@ -1,6 +1,6 @@
-// ep_expert_dev.h -- what the experts' product kernels share: bounded views of
-// memory, the exchange of lanes that lets weights be loaded as whole cache
-// lines, and the search for a workgroup's expert and rows.
+// ep_expert_dev.h -- what the experts' product kernels share: loads through bounded
+// views, the exchange of lanes that lets weights be loaded as whole cache lines,
+// and the search for a workgroup's expert and rows.
 #pragma once
 
 #include "ep_device.h"
@@ -10,17 +10,6 @@ namespace expert {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// Bounded view of `bytes` bytes at p: loads past its end give 0 and touch
-// nothing.  A lane's own offset alone has to say so, since the step's offset,
-// the same in every lane, need not count in that check.  p and bytes are the same in every lane, and said to be: a view in
-// vector registers is loaded through in a loop over its values.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t view(const void* p, uint32_t bytes) {
-    const uint64_t v = reinterpret_cast<uint64_t>(p);
-    const uint64_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
-    const uint64_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
-    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(hi << 32 | (lo & 0xffffffffu)),
-                                             0, __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
-}
 constexpr uint32_t kNowhere = 0x7fffff00u;  // past the end of every view
 template <bool ONCE>  // not kept in the caches
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t step) {

@@ -84,8 +84,185 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a, int L) {
     }
 }
 
-// Gradient of the rows: a group of L lanes takes a row, reads it once for the
-// two means and once more for dx.
+// The whole backward pass in one reading of the rows.  A group of L lanes takes
+// B rows at a time, a lane V pieces of each at the same channels all along, so
+// that its sums for the gradients of weight and bias stay in registers: V P of each.
+// The next rows are loaded before these ones' sums are joined.  A workgroup's groups
+// join their sums in LDS and leave one part of both gradients (norm_join_kernel).
+
+// Sums of B pairs of values over the lanes of a group; parts: B pairs per wave.
+template <int B>
+__device__ __forceinline__ void pair_sums(float (&c1)[B], float (&c2)[B],
+                                          float (*parts)[2 * B], int wave0, int waves,
+                                          int wave) {
+    float v[2 * B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        v[2 * b] = wave_sum(c1[b]);
+        v[2 * b + 1] = wave_sum(c2[b]);
+    }
+    if (waves > 1) {
+        const int lane = threadIdx.x % kWave;
+        if (lane < 2 * B) {
+            float own = v[0];
+#pragma unroll
+            for (int i = 1; i < 2 * B; ++i) own = lane == i ? v[i] : own;
+            parts[wave][lane] = own;
+        }
+        __syncthreads();
+        // lane i of a row of 16 takes wave i's values
+        const bool has = lane % 16 < waves;
+#pragma unroll
+        for (int i = 0; i < 2 * B; ++i) v[i] = has ? parts[wave0 + lane % 16][i] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2 * B; ++i) v[i] = row16_sum(v[i]);
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        c1[b] = v[2 * b];
+        c2[b] = v[2 * b + 1];
+    }
+}
+
+// WHOLE: P divides H and rows start at whole words.
+template <bool XB, bool WB, int V, int B, bool WHOLE>
+__global__ __launch_bounds__(kMaxThreads) void norm_grad_kernel(NormGradArgs a, int L, float* out) {
+    typedef Piece<XB> X;
+    constexpr int P = X::P;
+    __shared__ float s_part[2][kMaxThreads / kWave][2 * B];
+    __shared__ float s_sum[V * P * kMaxThreads];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int waves = L / kWave, group = wave / waves, wave0 = group * waves;
+    const int l = threadIdx.x - group * L, groups = blockDim.x / L;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups * B;
+    float w[V][P], dw[V][P], db[V][P];
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        const int c = (l + u * L) * P;
+        load_params<P, WB>(a.weight, c, c < a.hidden ? a.hidden : 0, 1.0f, w[u]);
+#pragma unroll
+        for (int i = 0; i < P; ++i) dw[u][i] = db[u][i] = 0.0f;
+    }
+    struct Rows {
+        X x[B][V], g[B][V], s[B][V];
+        float m[B], r[B];
+    };
+    typedef typename X::T T;
+    const auto load = [&](Rows& q, int64_t t0) {
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const bool there = t0 + b < a.num_tokens;
+            const int64_t t = there ? t0 + b : 0;
+            q.m[b] = there ? a.mean[t] : 0.0f;
+            q.r[b] = there ? a.rstd[t] : 0.0f;
+            const int H = there ? a.hidden : 0;
+            const T* x = static_cast<const T*>(a.x) + t * a.x_stride;
+            const T* g = static_cast<const T*>(a.dy) + t * a.dy_stride;
+            const T* s = static_cast<const T*>(a.d_skip) + t * a.hidden;
+            const int skips = a.d_skip == nullptr ? 0 : H;
+            if constexpr (WHOLE) {
+                const auto xv = view(x, H * sizeof(T)), gv = view(g, H * sizeof(T));
+                const auto sv = view(s, skips * sizeof(T));
+#pragma unroll
+                for (int u = 0; u < V; ++u) {
+                    q.x[b][u].load(xv, (l + u * L) * P);
+                    q.g[b][u].load(gv, (l + u * L) * P);
+                    q.s[b][u].load(sv, (l + u * L) * P);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < V; ++u) {
+                    q.x[b][u].load(x, (l + u * L) * P, H);
+                    q.g[b][u].load(g, (l + u * L) * P, H);
+                    q.s[b][u].load(s, (l + u * L) * P, skips);
+                }
+            }
+        }
+    };
+    // Two pieces of bf16 rows leave no registers for rows ahead.
+    constexpr bool kAhead = !(XB && V == 2);
+    Rows now, next;
+    int64_t t0 = (static_cast<int64_t>(blockIdx.x) * groups + group) * B;
+    // every group of the workgroup takes as many turns, for the barriers
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * groups * B;
+    if constexpr (kAhead) load(now, t0);
+    int turn = 0;
+#pragma unroll 1
+    for (int64_t at = first; at < a.num_tokens; at += step, t0 += step, turn ^= 1) {
+        if constexpr (kAhead)
+            load(next, t0 + step);
+        else
+            load(now, t0);
+        float c1[B], c2[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            c1[b] = c2[b] = 0.0f;
+#pragma unroll
+            for (int u = 0; u < V; ++u)
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const float g = now.g[b][u].at(i), v = g * w[u][i];
+                    const float n = (now.x[b][u].at(i) - now.m[b]) * now.r[b];
+                    c1[b] += v;
+                    c2[b] = fmaf(v, n, c2[b]);
+                    db[u][i] += g;
+                    dw[u][i] = fmaf(g, n, dw[u][i]);
+                }
+            __builtin_amdgcn_sched_barrier(0);  // one row's values at a time: registers
+        }
+        pair_sums(c1, c2, s_part[turn], wave0, waves, wave);
+        // what was made of the rows is made again, not kept: registers
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+            for (int u = 0; u < V; ++u) asm volatile("" : "+v"(now.x[b][u].v), "+v"(now.g[b][u].v));
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (t0 + b >= a.num_tokens) continue;
+            const float a1 = c1[b] / a.hidden, a2 = c2[b] / a.hidden;
+            T* dx = static_cast<T*>(a.dx) + (t0 + b) * a.hidden;
+            const auto dv = view(dx, a.hidden * sizeof(T));
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                const int c = (l + u * L) * P;
+                float d[P];
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const float n = (now.x[b][u].at(i) - now.m[b]) * now.r[b];
+                    d[i] = fmaf(now.r[b], fmaf(-n, a2, now.g[b][u].at(i) * w[u][i] - a1),
+                                now.s[b][u].at(i));
+                }
+                if constexpr (WHOLE)
+                    X::store(dv, c, d);
+                else if (c < a.hidden)
+                    X::store(dx, c, a.hidden, d);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (kAhead) now = next;
+    }
+    if (out == nullptr) return;
+    out += static_cast<int64_t>(blockIdx.x) * 2 * a.hidden;
+    // one gradient after the other through LDS
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        if (which == 1) __syncthreads();
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                s_sum[group * L * V * P + (l + u * L) * P + i] = which == 0 ? dw[u][i] : db[u][i];
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.hidden; c += blockDim.x) {
+            float sum = 0.0f;
+            for (int q = 0; q < groups; ++q) sum += s_sum[q * L * V * P + c];
+            out[static_cast<int64_t>(which) * a.hidden + c] = sum;
+        }
+    }
+}
+
+// Longer rows.  Gradient of the rows: a group of L lanes takes a row, reads it
+// once for the two means and once more for dx.
 template <bool XB, bool WB>
 __global__ __launch_bounds__(kMaxThreads) void norm_rows_kernel(NormGradArgs a, int L) {
     typedef Piece<XB> X;
@@ -239,29 +416,59 @@ void launch_norm_types(const NormArgs& a, hipStream_t stream) {
     }
 }
 
+template <bool WB>
+void launch_join(const NormGradArgs& a, const float* parts, int n, hipStream_t stream) {
+    hipLaunchKernelGGL((norm_join_kernel<WB>), dim3((2 * a.hidden + kWave - 1) / kWave),
+                       dim3(kJoinWaves * kWave), 0, stream, parts, n, a.hidden, a.d_weight, a.d_bias);
+}
+
 template <bool XB, bool WB>
 hipError_t launch_norm_grad_types(const NormGradArgs& a, void* workspace, hipStream_t stream) {
     const int P = Piece<XB>::P;
     const int pieces = (a.hidden + P - 1) / P;
-    if (a.num_tokens > 0) {
-        const int L = lanes_per_row(pieces, 8, a.num_tokens);
-        const int threads = L < 256 ? 256 : L;
-        const int rows = threads / L;
-        hipLaunchKernelGGL((norm_rows_kernel<XB, WB>),
-                           grid_of((a.num_tokens + rows - 1) / rows), dim3(threads), 0, stream, a, L);
-    }
-    if (a.d_weight == nullptr && a.d_bias == nullptr) return hipGetLastError();
+    const bool params = a.d_weight != nullptr || a.d_bias != nullptr;
     float* parts = static_cast<float*>(workspace);
-    int n = 0;
-    if (a.num_tokens > 0) {
-        const int most = norm_parts(a.num_tokens, a.hidden);
-        const int run = (a.num_tokens + most - 1) / most;
-        n = (a.num_tokens + run - 1) / run;
-        hipLaunchKernelGGL((norm_columns_kernel<XB>), dim3((pieces + kWave - 1) / kWave, n),
-                           dim3(kColumnWaves * kWave), 0, stream, a, run, parts);
+    const int most = a.num_tokens > 0 ? norm_parts(a.num_tokens, a.hidden) : 0;
+    int n = 0;  // parts written
+    if (a.num_tokens > 0 && pieces <= 2 * kMaxThreads) {
+        const int lanes = (pieces <= kMaxThreads ? pieces : (pieces + 1) / 2);
+        const int L = (lanes + kWave - 1) / kWave * kWave;
+        const int groups = kMaxThreads / L;
+        // rows through views: whole pieces at addresses of whole words
+        const int el = 16 / P;
+        const auto words = [&](const void* p, int64_t stride) {
+            return reinterpret_cast<uintptr_t>(p) % 4 == 0 && stride * el % 4 == 0;
+        };
+        const bool whole = a.hidden % P == 0 && words(a.x, a.x_stride) && words(a.dy, a.dy_stride) &&
+                           words(a.d_skip, 0) && words(a.dx, 0);
+        const auto go = [&](auto kernel, int rows) {  // rows of a group's turn
+            const int each = groups * rows, turns = (a.num_tokens + each - 1) / each;
+            n = turns < most ? turns : most;
+            hipLaunchKernelGGL(kernel, dim3(n), dim3(groups * L), 0, stream, a, L,
+                               params ? parts : nullptr);
+        };
+        constexpr int kUneven = XB ? 1 : 2;  // registers
+        if (pieces <= kMaxThreads && whole)
+            go(norm_grad_kernel<XB, WB, 1, 2, true>, 2);
+        else if (pieces <= kMaxThreads)
+            go(norm_grad_kernel<XB, WB, 1, kUneven, false>, kUneven);
+        else if (whole)
+            go(norm_grad_kernel<XB, WB, 2, 1, true>, 1);
+        else
+            go(norm_grad_kernel<XB, WB, 2, 1, false>, 1);
+    } else if (a.num_tokens > 0) {
+        const int L = lanes_per_row(pieces, 8, a.num_tokens);
+        const int rows = L < 256 ? 256 / L : 1;
+        hipLaunchKernelGGL((norm_rows_kernel<XB, WB>), grid_of((a.num_tokens + rows - 1) / rows),
+                           dim3(rows * L), 0, stream, a, L);
+        if (params) {
+            const int run = (a.num_tokens + most - 1) / most;
+            n = (a.num_tokens + run - 1) / run;
+            hipLaunchKernelGGL((norm_columns_kernel<XB>), dim3((pieces + kWave - 1) / kWave, n),
+                               dim3(kColumnWaves * kWave), 0, stream, a, run, parts);
+        }
     }
-    hipLaunchKernelGGL((norm_join_kernel<WB>), dim3((2 * a.hidden + kWave - 1) / kWave),
-                       dim3(kJoinWaves * kWave), 0, stream, parts, n, a.hidden, a.d_weight, a.d_bias);
+    if (params) launch_join<WB>(a, parts, n, stream);
     return hipGetLastError();
 }
 

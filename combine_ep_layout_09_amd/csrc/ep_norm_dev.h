@@ -1,6 +1,8 @@
 // ep_norm_dev.h -- device-side helpers of the layer norm kernels.
 #pragma once
 
+#include <type_traits>
+
 #include "ep_device.h"
 
 namespace ep {
@@ -11,7 +13,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
 typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
-// 16 bytes of a row: P channels from c on, 0 behind the row's end.
+// 16 bytes of a row: P channels from c on, 0 behind the row's end.  Through a
+// bounded view of a row that P divides: no lane has to ask where the row ends.
 template <bool BF16>
 struct Piece;
 
@@ -19,12 +22,23 @@ template <>
 struct Piece<true> {
     typedef uint16_t T;
     static constexpr int P = 8;
+    static __device__ __forceinline__ u32x4 pack(const float (&f)[P]) {
+        return u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                     pack_bf16(f[6], f[7])};
+    }
     u32x4 v;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t row, int c) {
+        v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(row, c * sizeof(T), 0, 0));
+    }
+    static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t row, int c,
+                                                 const float (&f)[P]) {
+        __builtin_amdgcn_raw_buffer_store_b128(pack(f), row, c * sizeof(T), 0, 0);
+    }
     __device__ __forceinline__ void load(const T* row, int c, int H) {
+        v = u32x4{0, 0, 0, 0};
         if (c + P <= H) {
             v = *reinterpret_cast<const u32x4_at2*>(row + c);
         } else {
-            v = u32x4{0, 0, 0, 0};
             // a row of uneven length: at most one piece of it
             for (int i = 0; c + i < H; ++i) {
                 const uint32_t e = static_cast<uint32_t>(row[c + i]) << (16 * (i & 1));
@@ -37,8 +51,7 @@ struct Piece<true> {
         return i % 2 == 0 ? bf16_lo(v[i / 2]) : bf16_hi(v[i / 2]);
     }
     static __device__ __forceinline__ void store(T* row, int c, int H, const float (&f)[P]) {
-        const u32x4 o = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                         pack_bf16(f[6], f[7])};
+        const u32x4 o = pack(f);
         if (c + P <= H) {
             *reinterpret_cast<u32x4_at2*>(row + c) = o;
         } else {
@@ -54,8 +67,20 @@ struct Piece<false> {
     typedef float T;
     typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
     static constexpr int P = 4;
+    static __device__ __forceinline__ u32x4 pack(const float (&f)[P]) {
+        return u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                     __float_as_uint(f[3])};
+    }
     u32x4 v;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t row, int c) {
+        v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(row, c * sizeof(T), 0, 0));
+    }
+    static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t row, int c,
+                                                 const float (&f)[P]) {
+        __builtin_amdgcn_raw_buffer_store_b128(pack(f), row, c * sizeof(T), 0, 0);
+    }
     __device__ __forceinline__ void load(const T* row, int c, int H) {
+        v = u32x4{0, 0, 0, 0};
         if (c + P <= H) {
             v = *reinterpret_cast<const u32x4_at4*>(row + c);
         } else {
@@ -66,9 +91,7 @@ struct Piece<false> {
     __device__ __forceinline__ float at(int i) const { return __uint_as_float(v[i]); }
     static __device__ __forceinline__ void store(T* row, int c, int H, const float (&f)[P]) {
         if (c + P <= H) {
-            const u32x4 o = {__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                             __float_as_uint(f[3])};
-            *reinterpret_cast<u32x4_at4*>(row + c) = o;
+            *reinterpret_cast<u32x4_at4*>(row + c) = pack(f);
         } else {
 #pragma unroll
             for (int i = 0; i < P; ++i)
@@ -113,17 +136,22 @@ __device__ __forceinline__ void load_params(const void* p, int c, int H, float o
     }
 }
 
-// Sum over the lanes of a wave, in every lane: rows of 16 by rotation, then
-// across the four rows.
+// Sum over the lanes of a row of 16, in every lane, by rotation.
+__device__ __forceinline__ float row16_sum(float v) {
+    const auto turned = [&](auto i) {
+        return __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+            0, static_cast<int>(__float_as_uint(v)), 0x120 + decltype(i)::value, 0xf, 0xf, false)));
+    };
+    v += turned(std::integral_constant<int, 8>{});
+    v += turned(std::integral_constant<int, 4>{});
+    v += turned(std::integral_constant<int, 2>{});
+    v += turned(std::integral_constant<int, 1>{});
+    return v;
+}
+
+// Sum over the lanes of a wave, in every lane.
 __device__ __forceinline__ float wave_sum(float v) {
-    const auto moved = [&](auto i) { return __uint_as_float(static_cast<uint32_t>(i)); };
-#define EP_ROW_ROR(n) \
-    moved(__builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)), 0x120 + n, 0xf, 0xf, false))
-    v += EP_ROW_ROR(8);
-    v += EP_ROW_ROR(4);
-    v += EP_ROW_ROR(2);
-    v += EP_ROW_ROR(1);
-#undef EP_ROW_ROR
+    v = row16_sum(v);
     const auto lane = [&](int i) {
         return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), i));
     };
