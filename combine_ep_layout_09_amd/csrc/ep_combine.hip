@@ -40,12 +40,13 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kMaxThreads = 1024;
 
 // What follows a piece's sum, before it is rounded.  begin() is called where the
-// rows' loads are issued, its result goes to end() with the sum.  Plain: nothing
-// (ep_combine).
+// rows' loads are issued, under() while they are under way; the result goes to end()
+// with the sum.  Plain: nothing (ep_combine).
 struct Plain {
     struct Begun {};
     __device__ __forceinline__ Begun begin(int64_t, int, int) const { return {}; }
-    __device__ __forceinline__ void end(const Begun&, int, int, float (&)[8]) const {}
+    __device__ __forceinline__ void under(Begun&, int, int) const {}
+    __device__ __forceinline__ void end(const Begun&, float (&)[8]) const {}
 };
 
 // Dropout and the skip connection (ep_combine_dropout).  Eight channels of a piece
@@ -55,19 +56,22 @@ struct Dropped {
     const u32x4* residual;
     struct Begun {
         u32x4 residual;
+        uint32_t kept;
     };
     __device__ __forceinline__ Begun begin(int64_t t, int nvec, int v) const {
-        Begun b = {u32x4{0, 0, 0, 0}};
+        Begun b = {u32x4{0, 0, 0, 0}, 0};
         if (residual != nullptr) b.residual = __builtin_nontemporal_load(residual + t * nvec + v);
         return b;
     }
-    __device__ __forceinline__ void end(const Begun& b, int t, int v, float (&acc)[8]) const {
-        const uint32_t kept = dropout::keep8(drop, t, v);
+    __device__ __forceinline__ void under(Begun& b, int t, int v) const {
+        b.kept = dropout::keep8(drop, t, v);
+    }
+    __device__ __forceinline__ void end(const Begun& b, float (&acc)[8]) const {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t w = b.residual[i / 2];
             const float r = i % 2 == 0 ? bf16_lo(w) : bf16_hi(w);
-            acc[i] = r + (kept >> i & 1 ? acc[i] * drop.factor : 0.0f);
+            acc[i] = r + (b.kept >> i & 1 ? acc[i] * drop.factor : 0.0f);
         }
     }
 };
@@ -125,6 +129,10 @@ __global__ __launch_bounds__(kMaxThreads) void combine_kernel(
             for (int jj = 0; jj < KB; ++jj)
 #pragma unroll
                 for (int u = 0; u < VPL; ++u) buf[u][jj] = __builtin_nontemporal_load(src[jj] + v[u]);
+            if (j0 == 0) {
+#pragma unroll
+                for (int u = 0; u < VPL; ++u) fin.under(begun[u], t, v[u]);
+            }
 #pragma unroll
             for (int jj = 0; jj < KB; ++jj) {
 #pragma unroll
@@ -145,7 +153,7 @@ __global__ __launch_bounds__(kMaxThreads) void combine_kernel(
     u32x4* out = y + static_cast<int64_t>(t) * nvec;
 #pragma unroll
     for (int u = 0; u < VPL; ++u) {
-        fin.end(begun[u], t, v[u], acc[u]);
+        fin.end(begun[u], acc[u]);
         u32x4 r;
         r.x = f32_to_bf16_rne(acc[u][0]) | (f32_to_bf16_rne(acc[u][1]) << 16);
         r.y = f32_to_bf16_rne(acc[u][2]) | (f32_to_bf16_rne(acc[u][3]) << 16);
@@ -201,7 +209,7 @@ __device__ __forceinline__ u32x4 combine_piece(const u32x4* __restrict__ eo, int
                                                const float* __restrict__ w, int64_t R, int t, int v,
                                                const Fin& fin) {
     const int k = EXACT ? KB : k_arg;
-    const auto begun = fin.begin(t, nvec, v);
+    auto begun = fin.begin(t, nvec, v);
     float acc[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
@@ -219,6 +227,7 @@ __device__ __forceinline__ u32x4 combine_piece(const u32x4* __restrict__ eo, int
         }
         // all of the batch's loads are issued before the first is used
         __builtin_amdgcn_sched_barrier(0);
+        if (j0 == 0) fin.under(begun, t, v);
 #pragma unroll
         for (int jj = 0; jj < KB; ++jj) {
             const u32x4 p = buf[jj];
@@ -231,7 +240,7 @@ __device__ __forceinline__ u32x4 combine_piece(const u32x4* __restrict__ eo, int
             }
         }
     }
-    fin.end(begun, t, v, acc);
+    fin.end(begun, acc);
     u32x4 r;
     r.x = f32_to_bf16_rne(acc[0]) | (f32_to_bf16_rne(acc[1]) << 16);
     r.y = f32_to_bf16_rne(acc[2]) | (f32_to_bf16_rne(acc[3]) << 16);
@@ -267,7 +276,7 @@ template <int KB, typename Between, class Fin>
 __device__ __forceinline__ u32x4 reduce_rows(const u32x4* __restrict__ eo, int nvec, int64_t R,
                                              int t, int v, int32_t (&s)[KB], float (&w)[KB],
                                              Between between, const Fin& fin) {
-    const auto begun = fin.begin(t, nvec, v);
+    auto begun = fin.begin(t, nvec, v);
     bool ok[KB];
     u32x4 buf[KB];
 #pragma unroll
@@ -282,6 +291,7 @@ __device__ __forceinline__ u32x4 reduce_rows(const u32x4* __restrict__ eo, int n
     // all of the rows' loads (and the next entries' fetch) are issued before
     // the first row is used
     __builtin_amdgcn_sched_barrier(0);
+    fin.under(begun, t, v);
     float acc[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
@@ -296,7 +306,7 @@ __device__ __forceinline__ u32x4 reduce_rows(const u32x4* __restrict__ eo, int n
             acc[c] = ok[jj] ? a : acc[c];
         }
     }
-    fin.end(begun, t, v, acc);
+    fin.end(begun, acc);
     u32x4 r;
     r.x = f32_to_bf16_rne(acc[0]) | (f32_to_bf16_rne(acc[1]) << 16);
     r.y = f32_to_bf16_rne(acc[2]) | (f32_to_bf16_rne(acc[3]) << 16);

@@ -6,8 +6,10 @@
 //   d_weights[t, j] = <g[t], expert_out[s]>
 //
 // A workgroup takes a token.  A lane holds VPL 16-byte pieces of dy with the
-// dropped channels zeroed, made once for all k entries, and goes through the
-// entries: each expert row is read once, each gradient row written once.
+// dropped channels zeroed, made once for all k entries.  Entries are taken in batches of
+// KB: the loads of their expert rows are issued together, with no branches, and
+// the mask is made while they are under way.  Each expert row is read once,
+// each gradient row written once.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -22,7 +24,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxThreads = 1024;
 
-template <int VPL>
+template <int VPL, int KB>
 __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
         const u32x4* __restrict__ dy, const u32x4* __restrict__ eo, int nvec, int k,
         const int32_t* __restrict__ slot_of, int64_t R, const float* __restrict__ weights,
@@ -30,45 +32,75 @@ __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
     __shared__ float s_part[kMaxThreads / kWave][kMaxTopk];
     const int t = blockIdx.x;
     const int32_t* slots = slot_of + static_cast<int64_t>(t) * k;
+    const float* w = weights + static_cast<int64_t>(t) * k;
     const int wave = threadIdx.x / kWave;
+    int v[VPL];  // lanes past the end redo the last piece, and add and store nothing
+    bool here[VPL];
     u32x4 g[VPL];
 #pragma unroll
     for (int u = 0; u < VPL; ++u) {
-        const int v = threadIdx.x + u * blockDim.x;
-        g[u] = u32x4{0, 0, 0, 0};
-        if (v >= nvec) continue;
-        g[u] = __builtin_nontemporal_load(dy + static_cast<int64_t>(t) * nvec + v);
-        const uint32_t kept = dropout::keep8(drop, t, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            g[u][i] &= (kept >> (2 * i) & 1 ? 0xffffu : 0u) | (kept >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
+        const int at = threadIdx.x + u * blockDim.x;
+        here[u] = at < nvec;
+        v[u] = min(at, nvec - 1);
+        g[u] = __builtin_nontemporal_load(dy + static_cast<int64_t>(t) * nvec + v[u]);
     }
-    for (int j = 0; j < k; ++j) {
-        const int32_t slot = slots[j];
-        float sum = 0.0f;
-        if (slot >= 0 && slot < R) {
-            const float w = weights[static_cast<int64_t>(t) * k + j];
+    for (int j0 = 0; j0 < k; j0 += KB) {
+        bool ok[KB];
+        float wj[KB];
+        int64_t row[KB];
+        u32x4 e[KB][VPL];
 #pragma unroll
-            for (int u = 0; u < VPL; ++u) {
-                const int v = threadIdx.x + u * blockDim.x;
-                if (v >= nvec) continue;
-                const int64_t at = static_cast<int64_t>(slot) * nvec + v;
-                u32x4 e = u32x4{0, 0, 0, 0}, d;
-                if (dw != nullptr) e = __builtin_nontemporal_load(eo + at);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t gi = g[u][i];
-                    const float lo = bf16_lo(gi) * drop.factor, hi = bf16_hi(gi) * drop.factor;
-                    sum = fmaf(lo, bf16_lo(e[i]), sum);
-                    sum = fmaf(hi, bf16_hi(e[i]), sum);
-                    d[i] = pack_bf16(lo * w, hi * w);
-                }
-                __builtin_nontemporal_store(d, deo + at);
-            }
+        for (int jj = 0; jj < KB; ++jj) {
+            const int j = j0 + jj;
+            const int32_t slot = j < k ? slots[j] : -1;
+            ok[jj] = slot >= 0 && slot < R;
+            wj[jj] = ok[jj] ? w[j] : 0.0f;
+            // an entry without a slot loads row 0, whose products are dropped
+            row[jj] = static_cast<int64_t>(ok[jj] ? slot : 0) * nvec;
         }
         if (dw != nullptr) {
-            sum = norm::wave_sum(sum);
-            if (threadIdx.x % kWave == 0) s_part[wave][j] = sum;
+#pragma unroll
+            for (int jj = 0; jj < KB; ++jj)
+#pragma unroll
+                for (int u = 0; u < VPL; ++u)
+                    e[jj][u] = __builtin_nontemporal_load(eo + row[jj] + v[u]);
+        } else {
+#pragma unroll
+            for (int jj = 0; jj < KB; ++jj)
+#pragma unroll
+                for (int u = 0; u < VPL; ++u) e[jj][u] = u32x4{0, 0, 0, 0};
+        }
+        __builtin_amdgcn_sched_barrier(0);  // all loads first
+        if (j0 == 0) {
+#pragma unroll
+            for (int u = 0; u < VPL; ++u) {
+                const uint32_t kept = here[u] ? dropout::keep8(drop, t, v[u]) : 0u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    g[u][i] &= (kept >> (2 * i) & 1 ? 0xffffu : 0u) |
+                               (kept >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
+            }
+        }
+#pragma unroll
+        for (int jj = 0; jj < KB; ++jj) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int u = 0; u < VPL; ++u) {
+                u32x4 d;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float lo = bf16_lo(g[u][i]) * drop.factor;
+                    const float hi = bf16_hi(g[u][i]) * drop.factor;
+                    sum = fmaf(lo, bf16_lo(e[jj][u][i]), sum);
+                    sum = fmaf(hi, bf16_hi(e[jj][u][i]), sum);
+                    d[i] = pack_bf16(lo * wj[jj], hi * wj[jj]);
+                }
+                if (ok[jj] && here[u]) __builtin_nontemporal_store(d, deo + row[jj] + v[u]);
+            }
+            if (dw != nullptr && j0 + jj < k) {
+                sum = norm::wave_sum(sum);
+                if (threadIdx.x % kWave == 0) s_part[wave][j0 + jj] = ok[jj] ? sum : 0.0f;
+            }
         }
     }
     if (dw == nullptr) return;
@@ -91,22 +123,26 @@ hipError_t launch_combine_backward(const ep_problem& p, const void* dy, const vo
     const int64_t R = p.capacity == 0 ? static_cast<int64_t>(T) * p.num_topk
                                       : static_cast<int64_t>(p.num_experts) * p.capacity;
     const int nvec = p.hidden / 8;
-    int threads = kWave;
-    while (threads < kMaxThreads && nvec > 4 * threads) threads *= 2;
+    const int vpl = (nvec + kMaxThreads - 1) / kMaxThreads;
+    const int lanes = (nvec + vpl - 1) / vpl;
+    const int threads = (lanes + kWave - 1) / kWave * kWave;
     const auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3(T), dim3(threads), 0, stream, static_cast<const u32x4*>(dy),
                            static_cast<const u32x4*>(expert_out), nvec, p.num_topk, slot_of, R,
                            topk_weights, drop, static_cast<u32x4*>(d_expert_out), d_weights);
     };
-    const int vpl = (nvec + threads - 1) / threads;
-    if (vpl == 1)
-        go(combine_backward_kernel<1>);
+    if (vpl > 2)
+        go(combine_backward_kernel<8, 1>);
     else if (vpl == 2)
-        go(combine_backward_kernel<2>);
-    else if (vpl <= 4)
-        go(combine_backward_kernel<4>);
+        go(combine_backward_kernel<2, 4>);
+    else if (p.num_topk <= 2)
+        go(combine_backward_kernel<1, 2>);
+    else if (p.num_topk <= 4)
+        go(combine_backward_kernel<1, 4>);
+    else if (p.num_topk <= 6)
+        go(combine_backward_kernel<1, 6>);
     else
-        go(combine_backward_kernel<8>);
+        go(combine_backward_kernel<1, 8>);
     return hipGetLastError();
 }
 
