@@ -15,33 +15,41 @@
 namespace ep {
 namespace dropout {
 
-__device__ __forceinline__ void philox(uint32_t (&c)[4], uint32_t k0, uint32_t k1) {
-#pragma unroll
-    for (int i = 0; i < 10; ++i) {
-        const uint64_t p0 = static_cast<uint64_t>(c[0]) * 0xD2511F53u;
-        const uint64_t p1 = static_cast<uint64_t>(c[2]) * 0xCD9E8D57u;
-        c[0] = static_cast<uint32_t>(p1 >> 32) ^ c[1] ^ k0;
-        c[2] = static_cast<uint32_t>(p0 >> 32) ^ c[3] ^ k1;
-        c[1] = static_cast<uint32_t>(p1);
-        c[3] = static_cast<uint32_t>(p0);
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
-    }
-}
-
-// Bit i: channel 8 v + i of token t is kept.
+// Bit i: channel 8 v + i of token t is kept.  Two counters at a time, the rounds as
+// a loop: unrolled they make the combine's own loop over its pieces too long to be
+// unrolled, and its pieces leave the registers (4096 tokens, H 7168, top-8: 114 us instead of
+// 85, with no dropout in either).
 __device__ __forceinline__ uint32_t keep8(const DropArgs& d, int t, int v) {
     if (d.border == 0) return 0xffu;
     const uint64_t seed = d.rng[0], offset = d.rng[1];
-    uint32_t kept = 0;
+    uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+    uint32_t c[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        uint32_t c[4] = {static_cast<uint32_t>(2 * v + h), static_cast<uint32_t>(t),
-                         static_cast<uint32_t>(offset), static_cast<uint32_t>(offset >> 32)};
-        philox(c, static_cast<uint32_t>(seed), static_cast<uint32_t>(seed >> 32));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) kept |= c[i] >= d.border ? 1u << (4 * h + i) : 0u;
+        c[h][0] = static_cast<uint32_t>(2 * v + h);
+        c[h][1] = static_cast<uint32_t>(t);
+        c[h][2] = static_cast<uint32_t>(offset);
+        c[h][3] = static_cast<uint32_t>(offset >> 32);
     }
+#pragma unroll 1
+    for (int i = 0; i < 10; ++i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint64_t p0 = static_cast<uint64_t>(c[h][0]) * 0xD2511F53u;
+            const uint64_t p1 = static_cast<uint64_t>(c[h][2]) * 0xCD9E8D57u;
+            c[h][0] = static_cast<uint32_t>(p1 >> 32) ^ c[h][1] ^ k0;
+            c[h][2] = static_cast<uint32_t>(p0 >> 32) ^ c[h][3] ^ k1;
+            c[h][1] = static_cast<uint32_t>(p1);
+            c[h][3] = static_cast<uint32_t>(p0);
+        }
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    uint32_t kept = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kept |= c[h][i] >= d.border ? 1u << (4 * h + i) : 0u;
     return kept;
 }
 
