@@ -42,7 +42,10 @@ constexpr int kMaxThreads = 1024;
 // What follows a piece's sum, before it is rounded.  begin() is called where the
 // rows' loads are issued, under() while they are under way; the result goes to end()
 // with the sum.  Plain: nothing (ep_combine).
+// kPersistRows: expert rows that a wave has to read in the mean for the persistent form to
+// be taken (besides what that form needs).
 struct Plain {
+    static constexpr int kPersistRows = 0;
     struct Begun {};
     __device__ __forceinline__ Begun begin(int64_t, int, int) const { return {}; }
     __device__ __forceinline__ void under(Begun&, int, int) const {}
@@ -50,8 +53,12 @@ struct Plain {
 };
 
 // Dropout and the skip connection (ep_combine_dropout).  Eight channels of a piece
-// are two counters of the generator.
+// are two counters of the generator.  Persistent and per-token form, with the skip
+// connection: H 4096, top-6, 2600 tokens (30 rows per wave): 28.6 us and 27.2, 3500 (41) 38.8
+// and 39.9; H 7168, top-8, 1200 (33): 30.3 both, 4096 94.2 and 102.5; 517 tokens of H 4096 12.1
+// and 8.1.
 struct Dropped {
+    static constexpr int kPersistRows = 36;
     DropArgs drop;
     const u32x4* residual;
     struct Begun {
@@ -451,7 +458,8 @@ hipError_t launch_forms(const ep_problem& p, const void* expert_out, const int32
         per = (T + launches - 1) / launches;
         if ((per * C + nw - 1) / nw <= kHold) break;
     }
-    if (all_chunks >= nw && launches <= kMaxPersistLaunches) {
+    if (all_chunks >= nw && launches <= kMaxPersistLaunches &&
+        all_chunks * k >= nw * Fin::kPersistRows) {
         for (int64_t t0 = 0; t0 < T; t0 += per) {
             PersistShape ps;
             ps.C = C;

@@ -5,8 +5,7 @@
 //   dw = sum_t dy n,   db = sum_t dy
 //
 // Rows are moved in 16-byte pieces of P channels (8 bf16 or 4 fp32), at any
-// alignment that the element type allows; the last piece of a row whose length P
-// does not divide is moved channel by channel.
+// alignment that the element type allows.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -42,10 +41,10 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a, int L) {
     const int waves = L / kWave, wave0 = group * waves, wave = threadIdx.x / kWave;
     const int64_t t = block_number() * (blockDim.x / L) + group;
     const bool there = t < a.num_tokens;
-    const typename X::T* row = static_cast<const typename X::T*>(a.x) + (there ? t : 0) * a.x_stride;
+    const auto row = row_view<typename X::T>(a.x, t, a.x_stride, a.hidden, there);
     X x[VPL];
 #pragma unroll
-    for (int u = 0; u < VPL; ++u) x[u].load(row, (l + u * L) * P, there ? a.hidden : 0);
+    for (int u = 0; u < VPL; ++u) x[u].load(row, (l + u * L) * P, a.hidden);
 
     float sum = 0.0f;
 #pragma unroll
@@ -70,7 +69,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a, int L) {
         a.mean[t] = m;
         a.rstd[t] = r;
     }
-    typename X::T* out = static_cast<typename X::T*>(a.y) + t * a.hidden;
+    const auto out = row_view<typename X::T>(a.y, t, a.hidden, a.hidden, true);
 #pragma unroll
     for (int u = 0; u < VPL; ++u) {
         const int c = (l + u * L) * P;
@@ -124,8 +123,7 @@ __device__ __forceinline__ void pair_sums(float (&c1)[B], float (&c2)[B],
     }
 }
 
-// WHOLE: P divides H and rows start at whole words.
-template <bool XB, bool WB, int V, int B, bool WHOLE>
+template <bool XB, bool WB, int V, int B>
 __global__ __launch_bounds__(kMaxThreads) void norm_grad_kernel(NormGradArgs a, int L, float* out) {
     typedef Piece<XB> X;
     constexpr int P = X::P;
@@ -139,7 +137,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_grad_kernel(NormGradArgs a, 
 #pragma unroll
     for (int u = 0; u < V; ++u) {
         const int c = (l + u * L) * P;
-        load_params<P, WB>(a.weight, c, c < a.hidden ? a.hidden : 0, 1.0f, w[u]);
+        load_params<P, WB>(a.weight, c, a.hidden, 1.0f, w[u]);
 #pragma unroll
         for (int i = 0; i < P; ++i) dw[u][i] = db[u][i] = 0.0f;
     }
@@ -155,27 +153,14 @@ __global__ __launch_bounds__(kMaxThreads) void norm_grad_kernel(NormGradArgs a, 
             const int64_t t = there ? t0 + b : 0;
             q.m[b] = there ? a.mean[t] : 0.0f;
             q.r[b] = there ? a.rstd[t] : 0.0f;
-            const int H = there ? a.hidden : 0;
-            const T* x = static_cast<const T*>(a.x) + t * a.x_stride;
-            const T* g = static_cast<const T*>(a.dy) + t * a.dy_stride;
-            const T* s = static_cast<const T*>(a.d_skip) + t * a.hidden;
-            const int skips = a.d_skip == nullptr ? 0 : H;
-            if constexpr (WHOLE) {
-                const auto xv = view(x, H * sizeof(T)), gv = view(g, H * sizeof(T));
-                const auto sv = view(s, skips * sizeof(T));
+            const auto xv = row_view<T>(a.x, t, a.x_stride, a.hidden, there);
+            const auto gv = row_view<T>(a.dy, t, a.dy_stride, a.hidden, there);
+            const auto sv = row_view<T>(a.d_skip, t, a.hidden, a.hidden, there);
 #pragma unroll
-                for (int u = 0; u < V; ++u) {
-                    q.x[b][u].load(xv, (l + u * L) * P);
-                    q.g[b][u].load(gv, (l + u * L) * P);
-                    q.s[b][u].load(sv, (l + u * L) * P);
-                }
-            } else {
-#pragma unroll
-                for (int u = 0; u < V; ++u) {
-                    q.x[b][u].load(x, (l + u * L) * P, H);
-                    q.g[b][u].load(g, (l + u * L) * P, H);
-                    q.s[b][u].load(s, (l + u * L) * P, skips);
-                }
+            for (int u = 0; u < V; ++u) {
+                q.x[b][u].load(xv, (l + u * L) * P, a.hidden);
+                q.g[b][u].load(gv, (l + u * L) * P, a.hidden);
+                q.s[b][u].load(sv, (l + u * L) * P, a.hidden);
             }
         }
     };
@@ -220,8 +205,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_grad_kernel(NormGradArgs a, 
         for (int b = 0; b < B; ++b) {
             if (t0 + b >= a.num_tokens) continue;
             const float a1 = c1[b] / a.hidden, a2 = c2[b] / a.hidden;
-            T* dx = static_cast<T*>(a.dx) + (t0 + b) * a.hidden;
-            const auto dv = view(dx, a.hidden * sizeof(T));
+            const auto dx = row_view<T>(a.dx, t0 + b, a.hidden, a.hidden, true);
 #pragma unroll
             for (int u = 0; u < V; ++u) {
                 const int c = (l + u * L) * P;
@@ -232,10 +216,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_grad_kernel(NormGradArgs a, 
                     d[i] = fmaf(now.r[b], fmaf(-n, a2, now.g[b][u].at(i) * w[u][i] - a1),
                                 now.s[b][u].at(i));
                 }
-                if constexpr (WHOLE)
-                    X::store(dv, c, d);
-                else if (c < a.hidden)
-                    X::store(dx, c, a.hidden, d);
+                X::store(dx, c, a.hidden, d);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -272,16 +253,17 @@ __global__ __launch_bounds__(kMaxThreads) void norm_rows_kernel(NormGradArgs a, 
     const int waves = L / kWave, wave0 = group * waves, wave = threadIdx.x / kWave;
     const int64_t t = block_number() * (blockDim.x / L) + group;
     const bool there = t < a.num_tokens;
-    const int H = there ? a.hidden : 0;
+    typedef typename X::T T;
+    const int H = a.hidden;
     const int64_t at = there ? t : 0;
-    const typename X::T* xr = static_cast<const typename X::T*>(a.x) + at * a.x_stride;
-    const typename X::T* gr = static_cast<const typename X::T*>(a.dy) + at * a.dy_stride;
+    const auto xr = row_view<T>(a.x, t, a.x_stride, H, there);
+    const auto gr = row_view<T>(a.dy, t, a.dy_stride, H, there);
     const float m = a.mean[at], r = a.rstd[at];
     float c1 = 0.0f, c2 = 0.0f;
     for (int c = l * P; c < H; c += L * P) {
         X x, g;
-        x.load(xr, c, H);
-        g.load(gr, c, H);
+        x.template load<0>(xr, c, H);
+        g.template load<0>(gr, c, H);
         float w[P];
         load_params<P, WB>(a.weight, c, H, 1.0f, w);
 #pragma unroll
@@ -293,14 +275,13 @@ __global__ __launch_bounds__(kMaxThreads) void norm_rows_kernel(NormGradArgs a, 
     }
     c1 = group_sum(c1, s_part[0], wave0, waves, wave) / a.hidden;
     c2 = group_sum(c2, s_part[1], wave0, waves, wave) / a.hidden;
-    typename X::T* out = static_cast<typename X::T*>(a.dx) + at * a.hidden;
-    const typename X::T* skip =
-        a.d_skip == nullptr ? nullptr : static_cast<const typename X::T*>(a.d_skip) + at * a.hidden;
+    const auto out = row_view<T>(a.dx, t, H, H, there);
+    const auto skip = row_view<T>(a.d_skip, t, H, H, there);
     for (int c = l * P; c < H; c += L * P) {
         X x, g, s;
         x.load(xr, c, H);
         g.load(gr, c, H);
-        s.load(skip, c, skip == nullptr ? 0 : H);
+        s.load(skip, c, H);
         float w[P], d[P];
         load_params<P, WB>(a.weight, c, H, 1.0f, w);
 #pragma unroll
@@ -331,8 +312,8 @@ __global__ __launch_bounds__(kColumnWaves* kWave) void norm_columns_kernel(NormG
     for (int i = 0; i < P; ++i) dw[i] = db[i] = 0.0f;
     for (int64_t t = first + wave; t < end; t += kColumnWaves) {
         X x, g;
-        x.load(static_cast<const typename X::T*>(a.x) + t * a.x_stride, c, a.hidden);
-        g.load(static_cast<const typename X::T*>(a.dy) + t * a.dy_stride, c, a.hidden);
+        x.load(row_view<typename X::T>(a.x, t, a.x_stride, a.hidden, true), c, a.hidden);
+        g.load(row_view<typename X::T>(a.dy, t, a.dy_stride, a.hidden, true), c, a.hidden);
         const float m = a.mean[t], r = a.rstd[t];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -434,28 +415,16 @@ hipError_t launch_norm_grad_types(const NormGradArgs& a, void* workspace, hipStr
         const int lanes = (pieces <= kMaxThreads ? pieces : (pieces + 1) / 2);
         const int L = (lanes + kWave - 1) / kWave * kWave;
         const int groups = kMaxThreads / L;
-        // rows through views: whole pieces at addresses of whole words
-        const int el = 16 / P;
-        const auto words = [&](const void* p, int64_t stride) {
-            return reinterpret_cast<uintptr_t>(p) % 4 == 0 && stride * el % 4 == 0;
-        };
-        const bool whole = a.hidden % P == 0 && words(a.x, a.x_stride) && words(a.dy, a.dy_stride) &&
-                           words(a.d_skip, 0) && words(a.dx, 0);
         const auto go = [&](auto kernel, int rows) {  // rows of a group's turn
             const int each = groups * rows, turns = (a.num_tokens + each - 1) / each;
             n = turns < most ? turns : most;
             hipLaunchKernelGGL(kernel, dim3(n), dim3(groups * L), 0, stream, a, L,
                                params ? parts : nullptr);
         };
-        constexpr int kUneven = XB ? 1 : 2;  // registers
-        if (pieces <= kMaxThreads && whole)
-            go(norm_grad_kernel<XB, WB, 1, 2, true>, 2);
-        else if (pieces <= kMaxThreads)
-            go(norm_grad_kernel<XB, WB, 1, kUneven, false>, kUneven);
-        else if (whole)
-            go(norm_grad_kernel<XB, WB, 2, 1, true>, 1);
+        if (pieces <= kMaxThreads)
+            go(norm_grad_kernel<XB, WB, 1, 2>, 2);
         else
-            go(norm_grad_kernel<XB, WB, 2, 1, false>, 1);
+            go(norm_grad_kernel<XB, WB, 2, 1>, 1);
     } else if (a.num_tokens > 0) {
         const int L = lanes_per_row(pieces, 8, a.num_tokens);
         const int rows = L < 256 ? 256 / L : 1;

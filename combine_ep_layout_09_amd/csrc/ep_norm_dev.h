@@ -8,13 +8,23 @@
 namespace ep {
 namespace norm {
 
-// Sixteen and eight bytes at any address that two-byte elements may have.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
-typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
-// 16 bytes of a row: P channels from c on, 0 behind the row's end.  Through a
-// bounded view of a row that P divides: no lane has to ask where the row ends.
+
+// Rows are accessed through bounded views (any alignment): words past the end of
+// the row read as 0 and are not written.  A row of an odd number of bf16 channels
+// ends within a word, which counts as past the end: its last channel is moved by
+// itself.  kOnce: not kept in the caches.
+constexpr int kOnce = 2;
+
+// The last of H channels, for the piece of P from channel c on that holds it:
+// its word of the piece, or -1 (also where H is even).
+__device__ __forceinline__ int odd_word(int c, int H, int P) {
+    const int at = H - 1 - c;
+    return H % 2 == 1 && at >= 0 && at < P ? at / 2 : -1;
+}
+
+// 16 bytes of a row: P channels from c on, 0 behind the row's end.
 template <bool BF16>
 struct Piece;
 
@@ -22,42 +32,32 @@ template <>
 struct Piece<true> {
     typedef uint16_t T;
     static constexpr int P = 8;
-    static __device__ __forceinline__ u32x4 pack(const float (&f)[P]) {
-        return u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                     pack_bf16(f[6], f[7])};
-    }
     u32x4 v;
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t row, int c) {
-        v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(row, c * sizeof(T), 0, 0));
-    }
-    static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t row, int c,
-                                                 const float (&f)[P]) {
-        __builtin_amdgcn_raw_buffer_store_b128(pack(f), row, c * sizeof(T), 0, 0);
-    }
-    __device__ __forceinline__ void load(const T* row, int c, int H) {
-        v = u32x4{0, 0, 0, 0};
-        if (c + P <= H) {
-            v = *reinterpret_cast<const u32x4_at2*>(row + c);
-        } else {
-            // a row of uneven length: at most one piece of it
-            for (int i = 0; c + i < H; ++i) {
-                const uint32_t e = static_cast<uint32_t>(row[c + i]) << (16 * (i & 1));
+    template <int AUX = kOnce>
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t row, int c, int H) {
+        v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(row, c * 2, 0, AUX));
+        if (H % 2 == 1) {
+            const uint32_t last = __builtin_amdgcn_raw_buffer_load_b16(row, (H - 1) * 2, 0, 0);
+            const int word = odd_word(c, H, P);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] |= q == i / 2 ? e : 0u;
-            }
+            for (int i = 0; i < 4; ++i) v[i] = word == i ? last : v[i];
         }
     }
     __device__ __forceinline__ float at(int i) const {
         return i % 2 == 0 ? bf16_lo(v[i / 2]) : bf16_hi(v[i / 2]);
     }
-    static __device__ __forceinline__ void store(T* row, int c, int H, const float (&f)[P]) {
-        const u32x4 o = pack(f);
-        if (c + P <= H) {
-            *reinterpret_cast<u32x4_at2*>(row + c) = o;
-        } else {
+    static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t row, int c, int H,
+                                                 const float (&f)[P]) {
+        const u32x4 o = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                         pack_bf16(f[6], f[7])};
+        __builtin_amdgcn_raw_buffer_store_b128(o, row, c * 2, 0, kOnce);
+        if (H % 2 == 1) {
+            const int word = odd_word(c, H, P);
+            uint32_t last = 0;
 #pragma unroll
-            for (int i = 0; i < P; ++i)
-                if (c + i < H) row[c + i] = static_cast<T>(o[i / 2] >> (16 * (i & 1)));
+            for (int i = 0; i < 4; ++i) last = word == i ? o[i] : last;
+            if (word >= 0)
+                __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(last), row, (H - 1) * 2, 0, 0);
         }
     }
 };
@@ -65,73 +65,58 @@ struct Piece<true> {
 template <>
 struct Piece<false> {
     typedef float T;
-    typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
     static constexpr int P = 4;
-    static __device__ __forceinline__ u32x4 pack(const float (&f)[P]) {
-        return u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                     __float_as_uint(f[3])};
-    }
     u32x4 v;
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t row, int c) {
-        v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(row, c * sizeof(T), 0, 0));
-    }
-    static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t row, int c,
-                                                 const float (&f)[P]) {
-        __builtin_amdgcn_raw_buffer_store_b128(pack(f), row, c * sizeof(T), 0, 0);
-    }
-    __device__ __forceinline__ void load(const T* row, int c, int H) {
-        v = u32x4{0, 0, 0, 0};
-        if (c + P <= H) {
-            v = *reinterpret_cast<const u32x4_at4*>(row + c);
-        } else {
-#pragma unroll
-            for (int i = 0; i < P; ++i) v[i] = c + i < H ? __float_as_uint(row[c + i]) : 0u;
-        }
+    template <int AUX = kOnce>
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t row, int c, int) {
+        v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(row, c * 4, 0, AUX));
     }
     __device__ __forceinline__ float at(int i) const { return __uint_as_float(v[i]); }
-    static __device__ __forceinline__ void store(T* row, int c, int H, const float (&f)[P]) {
-        if (c + P <= H) {
-            *reinterpret_cast<u32x4_at4*>(row + c) = pack(f);
-        } else {
-#pragma unroll
-            for (int i = 0; i < P; ++i)
-                if (c + i < H) row[c + i] = f[i];
-        }
+    static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t row, int c, int,
+                                                 const float (&f)[P]) {
+        const u32x4 o = {__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                         __float_as_uint(f[3])};
+        __builtin_amdgcn_raw_buffer_store_b128(o, row, c * 4, 0, kOnce);
     }
 };
 
-// P channels of a per-channel parameter, `otherwise` where there is none.
+// View of row t of [T, H] rows `stride` elements apart; empty where there is no such
+// row or no such tensor.
+template <class T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_view(const void* p, int64_t t, int64_t stride,
+                                                           int H, bool there) {
+    return view(static_cast<const T*>(p) + (there ? t * stride : 0),
+                there && p != nullptr ? H * sizeof(T) : 0);
+}
+
+// P channels of a per-channel parameter; `otherwise` where there is no such tensor.
 template <int P, bool BF16>
 __device__ __forceinline__ void load_params(const void* p, int c, int H, float otherwise,
                                             float (&f)[P]) {
+    if (p == nullptr) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) f[i] = otherwise;
-    if (p == nullptr) return;
-    if constexpr (BF16) {
-        const uint16_t* from = static_cast<const uint16_t*>(p) + c;
-        if (c + P <= H) {
-            if constexpr (P == 8) {
-                const u32x4 v = *reinterpret_cast<const u32x4_at2*>(from);
+        for (int i = 0; i < P; ++i) f[i] = otherwise;
+        return;
+    }
+    const auto v = view(p, H * (BF16 ? 2 : 4));
+    if constexpr (BF16 && P == 4) {
+        u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(v, c * 2, 0, 0));
+        if (H % 2 == 1) {
+            const uint32_t last = __builtin_amdgcn_raw_buffer_load_b16(v, (H - 1) * 2, 0, 0);
+            const int word = odd_word(c, H, P);
 #pragma unroll
-                for (int i = 0; i < P; ++i) f[i] = i % 2 == 0 ? bf16_lo(v[i / 2]) : bf16_hi(v[i / 2]);
-            } else {
-                const u32x2 v = *reinterpret_cast<const u32x2_at2*>(from);
-#pragma unroll
-                for (int i = 0; i < P; ++i) f[i] = i % 2 == 0 ? bf16_lo(v[i / 2]) : bf16_hi(v[i / 2]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < P; ++i)
-                if (c + i < H) f[i] = bf16_lo(from[i]);
+            for (int i = 0; i < 2; ++i) w[i] = word == i ? last : w[i];
         }
+#pragma unroll
+        for (int i = 0; i < P; ++i) f[i] = i % 2 == 0 ? bf16_lo(w[i / 2]) : bf16_hi(w[i / 2]);
     } else {
-        const float* from = static_cast<const float*>(p);
-        Piece<false> v;
+        constexpr int Q = Piece<BF16>::P;
+        Piece<BF16> q;
 #pragma unroll
-        for (int q = 0; q < P / 4; ++q) {
-            v.load(from, c + 4 * q, H);
+        for (int k = 0; k < P / Q; ++k) {
+            q.template load<0>(v, c + k * Q, H);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[4 * q + i] = v.at(i);
+            for (int i = 0; i < Q; ++i) f[k * Q + i] = q.at(i);
         }
     }
 }
