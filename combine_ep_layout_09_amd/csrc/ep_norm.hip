@@ -347,8 +347,20 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void norm_join_kernel(const floa
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int i = blockIdx.x * kWave + lane;  // of 2 H
     float s = 0.0f;
-    if (i < 2 * H)
-        for (int p = wave; p < n; p += kJoinWaves) s += parts[static_cast<int64_t>(p) * 2 * H + i];
+    if (i < 2 * H) {
+        const float* from = parts + i;
+        int p = wave;
+        // eight parts on their way at a time
+        for (; p + 7 * kJoinWaves < n; p += 8 * kJoinWaves) {
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                v[q] = from[static_cast<int64_t>(p + q * kJoinWaves) * 2 * H];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) s += v[q];
+        }
+        for (; p < n; p += kJoinWaves) s += from[static_cast<int64_t>(p) * 2 * H];
+    }
     s_sum[wave][lane] = s;
     __syncthreads();
     if (wave != 0 || i >= 2 * H) return;
