@@ -29,57 +29,82 @@ dim3 grid_of(int64_t blocks) {
     return dim3(static_cast<unsigned>(x), static_cast<unsigned>((blocks + x - 1) / x));
 }
 
-// A group of L lanes (a multiple of 64 that divides the workgroup) takes a row,
+// A group of L lanes (a multiple of 64 that divides the workgroup) takes B rows,
 // which it holds in registers between the statistics and the output: x is read
-// once, and m is known before the squares of x - m are added.
-template <bool XB, bool WB, int VPL>
+// once, and m is known before the squares of x - m are added.  B rows share each
+// load of weight and bias, which as fp32 are four times the bytes of a bf16 row.
+template <bool XB, bool WB, int VPL, int B>
 __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a, int L) {
     typedef Piece<XB> X;
+    typedef typename X::T T;
     constexpr int P = X::P;
-    __shared__ float s_part[2][kMaxThreads / kWave];
-    const int group = threadIdx.x / L, l = threadIdx.x % L;
-    const int waves = L / kWave, wave0 = group * waves, wave = threadIdx.x / kWave;
-    const int64_t t = block_number() * (blockDim.x / L) + group;
-    const bool there = t < a.num_tokens;
-    const auto row = row_view<typename X::T>(a.x, t, a.x_stride, a.hidden, there);
-    X x[VPL];
+    __shared__ float s_part[2][B][kMaxThreads / kWave];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int waves = L / kWave, group = wave / waves, wave0 = group * waves;
+    const int l = threadIdx.x - group * L;
+    const int64_t t0 = (block_number() * (blockDim.x / L) + group) * B;
+    X x[B][VPL];
 #pragma unroll
-    for (int u = 0; u < VPL; ++u) x[u].load(row, (l + u * L) * P, a.hidden);
-
-    float sum = 0.0f;
+    for (int b = 0; b < B; ++b) {
+        const auto row = row_view<T>(a.x, t0 + b, a.x_stride, a.hidden, t0 + b < a.num_tokens);
 #pragma unroll
-    for (int u = 0; u < VPL; ++u)
+        for (int u = 0; u < VPL; ++u) x[b][u].load(row, (l + u * L) * P, a.hidden);
+    }
+    // Registers: between its uses a row is kept as it came, not as fp32 values.
+    const auto as_it_came = [&] {
 #pragma unroll
-        for (int i = 0; i < P; ++i) sum += x[u].at(i);
-    const float m = group_sum(sum, s_part[0], wave0, waves, wave) / a.hidden;
-    float squares = 0.0f;
+        for (int b = 0; b < B; ++b)
 #pragma unroll
-    for (int u = 0; u < VPL; ++u) {
-        const int left = a.hidden - (l + u * L) * P;  // channels from this piece on
+            for (int u = 0; u < VPL; ++u) asm volatile("" : "+v"(x[b][u].v));
+    };
+    float m[B], r[B];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const float d = i < left ? x[u].at(i) - m : 0.0f;
-            squares = fmaf(d, d, squares);
+    for (int b = 0; b < B; ++b) {
+        m[b] = 0.0f;
+#pragma unroll
+        for (int u = 0; u < VPL; ++u)
+#pragma unroll
+            for (int i = 0; i < P; ++i) m[b] += x[b][u].at(i);
+    }
+    group_sums(m, s_part[0], wave0, waves, wave);
+    as_it_came();
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        m[b] /= a.hidden;
+        r[b] = 0.0f;
+#pragma unroll
+        for (int u = 0; u < VPL; ++u) {
+            const int left = a.hidden - (l + u * L) * P;  // channels from this piece on
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float d = i < left ? x[b][u].at(i) - m[b] : 0.0f;
+                r[b] = fmaf(d, d, r[b]);
+            }
         }
     }
-    const float var = group_sum(squares, s_part[1], wave0, waves, wave) / a.hidden;
-    const float r = 1.0f / sqrtf(var + a.eps);
-    if (!there) return;
-    if (l == 0 && a.mean != nullptr) {
-        a.mean[t] = m;
-        a.rstd[t] = r;
+    group_sums(r, s_part[1], wave0, waves, wave);
+    as_it_came();
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        r[b] = 1.0f / sqrtf(r[b] / a.hidden + a.eps);
+        if (l == 0 && a.mean != nullptr && t0 + b < a.num_tokens) {
+            a.mean[t0 + b] = m[b];
+            a.rstd[t0 + b] = r[b];
+        }
     }
-    const auto out = row_view<typename X::T>(a.y, t, a.hidden, a.hidden, true);
 #pragma unroll
     for (int u = 0; u < VPL; ++u) {
         const int c = (l + u * L) * P;
-        if (c >= a.hidden) continue;
-        float w[P], b[P], y[P];
+        float w[P], p[P], y[P];
         load_params<P, WB>(a.weight, c, a.hidden, 1.0f, w);
-        load_params<P, WB>(a.bias, c, a.hidden, 0.0f, b);
+        load_params<P, WB>(a.bias, c, a.hidden, 0.0f, p);
 #pragma unroll
-        for (int i = 0; i < P; ++i) y[i] = fmaf((x[u].at(i) - m) * r, w[i], b[i]);
-        X::store(out, c, a.hidden, y);
+        for (int b = 0; b < B; ++b) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) y[i] = fmaf((x[b][u].at(i) - m[b]) * r[b], w[i], p[i]);
+            X::store(row_view<T>(a.y, t0 + b, a.hidden, a.hidden, t0 + b < a.num_tokens), c, a.hidden,
+                     y);
+        }
     }
 }
 
@@ -385,28 +410,36 @@ int lanes_per_row(int pieces, int most, int64_t tokens) {
     return L;
 }
 
-template <bool XB, bool WB>
-void launch_norm_types(const NormArgs& a, hipStream_t stream) {
-    const int pieces = (a.hidden + Piece<XB>::P - 1) / Piece<XB>::P;
-    const int L = lanes_per_row(pieces, 8, a.num_tokens);
+template <bool XB, bool WB, int B>
+void launch_norm_rows(const NormArgs& a, int pieces, int L, hipStream_t stream) {
     const int threads = L < 256 ? 256 : L;
-    const int rows = threads / L;
+    const int rows = threads / L * B;
     const dim3 grid = grid_of((a.num_tokens + rows - 1) / rows);
     const auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, stream, a, L);
     };
     switch ((pieces + L - 1) / L) {
-        case 1: go(norm_kernel<XB, WB, 1>); break;
-        case 2: go(norm_kernel<XB, WB, 2>); break;
-        case 3: go(norm_kernel<XB, WB, 3>); break;
-        case 4: go(norm_kernel<XB, WB, 4>); break;
-        case 5: go(norm_kernel<XB, WB, 5>); break;
-        case 6: go(norm_kernel<XB, WB, 6>); break;
-        case 7: go(norm_kernel<XB, WB, 7>); break;
-        case 8: go(norm_kernel<XB, WB, 8>); break;
+        case 1: go(norm_kernel<XB, WB, 1, B>); break;
+        case 2: go(norm_kernel<XB, WB, 2, B>); break;
+        case 3: go(norm_kernel<XB, WB, 3, B>); break;
+        case 4: go(norm_kernel<XB, WB, 4, B>); break;
+        case 5: go(norm_kernel<XB, WB, 5, B>); break;
+        case 6: go(norm_kernel<XB, WB, 6, B>); break;
+        case 7: go(norm_kernel<XB, WB, 7, B>); break;
+        case 8: go(norm_kernel<XB, WB, 8, B>); break;
         default:  // fp32 rows of more than 32768 channels
-            if constexpr (!XB) go(norm_kernel<XB, WB, 16>);
+            if constexpr (!XB && B == 1) go(norm_kernel<XB, WB, 16, 1>);
     }
+}
+
+template <bool XB, bool WB>
+void launch_norm_types(const NormArgs& a, hipStream_t stream) {
+    const int pieces = (a.hidden + Piece<XB>::P - 1) / Piece<XB>::P;
+    const int L = lanes_per_row(pieces, 8, a.num_tokens);
+    if (a.num_tokens >= 4096 && pieces <= 8 * L)
+        launch_norm_rows<XB, WB, 2>(a, pieces, L, stream);
+    else
+        launch_norm_rows<XB, WB, 1>(a, pieces, L, stream);
 }
 
 template <bool WB>

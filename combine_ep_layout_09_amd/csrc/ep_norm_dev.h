@@ -156,5 +156,24 @@ __device__ __forceinline__ float group_sum(float v, float* parts, int wave0, int
     return s;
 }
 
+// The same for B values; parts: B floats per wave.
+template <int B>
+__device__ __forceinline__ void group_sums(float (&v)[B], float (*parts)[16], int wave0, int waves,
+                                           int wave) {
+#pragma unroll
+    for (int b = 0; b < B; ++b) v[b] = wave_sum(v[b]);
+    if (waves == 1) return;
+    if (threadIdx.x % kWave == 0) {
+#pragma unroll
+        for (int b = 0; b < B; ++b) parts[b][wave] = v[b];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        v[b] = 0.0f;
+        for (int i = 0; i < waves; ++i) v[b] += parts[b][wave0 + i];
+    }
+}
+
 }  // namespace norm
 }  // namespace ep
