@@ -15,7 +15,6 @@
 
 #include "ep_dropout_dev.h"
 #include "ep_internal.h"
-#include "ep_norm_dev.h"
 
 namespace ep {
 namespace {
@@ -23,6 +22,36 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxThreads = 1024;
+
+template <int CTRL>
+__device__ __forceinline__ float moved(float v) {
+    return __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+        0, static_cast<int>(__float_as_uint(v)), CTRL, 0xf, 0xf, false)));
+}
+
+// One step of wave_sums: each lane keeps one value of a pair, by bit BIT of its
+// number, and gives the other to the lane across, which keeps that.
+template <int N, int BIT, int CTRL>
+__device__ __forceinline__ void halve(float (&v)[8], int lane) {
+    const bool odd = lane >> BIT & 1;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float keep = odd ? v[2 * i + 1] : v[2 * i], give = odd ? v[2 * i] : v[2 * i + 1];
+        v[i] = keep + moved<CTRL>(give);
+    }
+}
+
+// Sums over a wave of eight values per lane, in a third of the instructions that eight
+// sums take: lane l returns the sum of value (l / 8 & 1) + 2 (l / 4 & 1) + 4 (l / 2 & 1).
+__device__ __forceinline__ float wave_sums(float (&v)[8]) {
+    const int lane = threadIdx.x % kWave;
+    halve<8, 3, 0x140>(v, lane);  // lane ^ 15
+    halve<4, 2, 0x141>(v, lane);  // lane ^ 7
+    halve<2, 1, 0x1b>(v, lane);   // lane ^ 3
+    float s = v[0] + moved<0xb1>(v[0]);  // lane ^ 1
+    s += __shfl_xor(s, 16, kWave);
+    return s + __shfl_xor(s, 32, kWave);
+}
 
 template <int VPL, int KB>
 __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
@@ -36,13 +65,14 @@ __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
     const int wave = threadIdx.x / kWave;
     int v[VPL];  // lanes past the end redo the last piece, and add and store nothing
     bool here[VPL];
-    u32x4 g[VPL];
+    u32x4 dyv[VPL];
+    float g[VPL][8];
 #pragma unroll
     for (int u = 0; u < VPL; ++u) {
         const int at = threadIdx.x + u * blockDim.x;
         here[u] = at < nvec;
         v[u] = min(at, nvec - 1);
-        g[u] = __builtin_nontemporal_load(dy + static_cast<int64_t>(t) * nvec + v[u]);
+        dyv[u] = __builtin_nontemporal_load(dy + static_cast<int64_t>(t) * nvec + v[u]);
     }
     for (int j0 = 0; j0 < k; j0 += KB) {
         bool ok[KB];
@@ -76,31 +106,37 @@ __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
             for (int u = 0; u < VPL; ++u) {
                 const uint32_t kept = here[u] ? dropout::keep8(drop, t, v[u]) : 0u;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    g[u][i] &= (kept >> (2 * i) & 1 ? 0xffffu : 0u) |
-                               (kept >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t word = dyv[u][i / 2];
+                    const float f = (i % 2 == 0 ? bf16_lo(word) : bf16_hi(word)) * drop.factor;
+                    g[u][i] = kept >> i & 1 ? f : 0.0f;
+                }
             }
         }
+        float sums[8];
+#pragma unroll
+        for (int jj = 0; jj < 8; ++jj) sums[jj] = 0.0f;
 #pragma unroll
         for (int jj = 0; jj < KB; ++jj) {
-            float sum = 0.0f;
 #pragma unroll
             for (int u = 0; u < VPL; ++u) {
                 u32x4 d;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float lo = bf16_lo(g[u][i]) * drop.factor;
-                    const float hi = bf16_hi(g[u][i]) * drop.factor;
-                    sum = fmaf(lo, bf16_lo(e[jj][u][i]), sum);
-                    sum = fmaf(hi, bf16_hi(e[jj][u][i]), sum);
+                    const float lo = g[u][2 * i], hi = g[u][2 * i + 1];
+                    sums[jj] = fmaf(lo, bf16_lo(e[jj][u][i]), sums[jj]);
+                    sums[jj] = fmaf(hi, bf16_hi(e[jj][u][i]), sums[jj]);
                     d[i] = pack_bf16(lo * wj[jj], hi * wj[jj]);
                 }
                 if (ok[jj] && here[u]) __builtin_nontemporal_store(d, deo + row[jj] + v[u]);
             }
-            if (dw != nullptr && j0 + jj < k) {
-                sum = norm::wave_sum(sum);
-                if (threadIdx.x % kWave == 0) s_part[wave][j0 + jj] = ok[jj] ? sum : 0.0f;
-            }
+            if (!ok[jj]) sums[jj] = 0.0f;
+        }
+        if (dw != nullptr) {
+            const float sum = wave_sums(sums);
+            const int lane = threadIdx.x % kWave;
+            const int j = j0 + (lane >> 3 & 1) + (lane >> 1 & 2) + (lane << 1 & 4);
+            if (lane < 16 && lane % 2 == 0 && j < k && j - j0 < KB) s_part[wave][j] = sum;
         }
     }
     if (dw == nullptr) return;
