@@ -784,12 +784,18 @@ def prepare_expert_w4(prob, mm, rows, layout, codes, scales, out, row_scales=Non
 
 def _rows_arg(t, name, nm, dtype, dev):
     """Pointer and row pitch of a [T, H] tensor, rows of any pitch."""
+    T, H = nm.num_tokens, nm.hidden
+    try:  # what nearly every call passes
+        if (t.dtype is dtype and t.shape == (T, H) and t.is_contiguous()
+                and t.get_device() == dev):
+            return t.data_ptr(), H
+    except AttributeError:
+        pass
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    T, H = nm.num_tokens, nm.hidden
     if t.shape != (T, H):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, H)}")
     if t.get_device() != dev:
@@ -804,36 +810,35 @@ def _rows_arg(t, name, nm, dtype, dev):
     return t.data_ptr(), stride
 
 
-def _norm_types(x, params):
-    """Whether x and the parameters are bf16 (1) or fp32 (0), and their types."""
+def _is_bf16(t, name):
+    """1 for a bf16 tensor, 0 for an fp32 one."""
     torch = _torch()
-    kinds = {torch.float32: 0, torch.bfloat16: 1}
-    x_dtype = getattr(x, "dtype", None)
-    if x_dtype not in kinds:
-        raise TypeError(f"x has dtype {x_dtype}, expected float32 or bfloat16")
-    w_dtype = None
-    for p in params:
-        if p is not None:
-            w_dtype = getattr(p, "dtype", None)
-            break
-    else:
-        w_dtype = torch.float32
-    if w_dtype not in kinds:
-        raise TypeError(f"weight has dtype {w_dtype}, expected float32 or bfloat16")
-    return x_dtype, kinds[x_dtype], w_dtype, kinds[w_dtype]
+    dtype = getattr(t, "dtype", None)
+    if dtype is torch.bfloat16:
+        return 1
+    if dtype is torch.float32:
+        return 0
+    raise TypeError(f"{name} has dtype {dtype}, expected float32 or bfloat16")
 
 
 def _layer_norm_args(nm, x, weight, bias, y, mean, rstd):
     torch = _torch()
     dev = _device_of(x, "x")
-    x_dtype, x_bf16, w_dtype, w_bf16 = _norm_types(x, (weight, bias))
     T, H = nm.num_tokens, nm.hidden
-    xp, stride = _rows_arg(x, "x", nm, x_dtype, dev)
-    wp = _arg(weight, "weight", w_dtype, (H,), dev, allow_none=True)
-    bp = _arg(bias, "bias", w_dtype, (H,), dev, allow_none=True)
-    yp = _arg(y, "y", x_dtype, (T, H), dev)
-    mp = _arg(mean, "mean", torch.float32, (T,), dev, allow_none=True)
-    rp = _arg(rstd, "rstd", torch.float32, (T,), dev, allow_none=True)
+    x_bf16, w_bf16, wp, bp, mp, rp = _is_bf16(x, "x"), 0, None, None, None, None
+    xp, stride = _rows_arg(x, "x", nm, x.dtype, dev)
+    param = weight if weight is not None else bias
+    if param is not None:
+        w_bf16 = _is_bf16(param, "weight")
+        if weight is not None:
+            wp = _arg(weight, "weight", param.dtype, (H,), dev)
+        if bias is not None:
+            bp = _arg(bias, "bias", param.dtype, (H,), dev)
+    yp = _arg(y, "y", x.dtype, (T, H), dev)
+    if mean is not None:
+        mp = _arg(mean, "mean", torch.float32, (T,), dev)
+    if rstd is not None:
+        rp = _arg(rstd, "rstd", torch.float32, (T,), dev)
     return dev, (ctypes.byref(nm), xp, x_bf16, stride, wp, bp, w_bf16, yp, mp, rp)
 
 
@@ -868,8 +873,12 @@ def _layer_norm_backward_args(nm, x, dy, weight, mean, rstd, dx, d_weight, d_bia
                               d_skip):
     torch = _torch()
     dev = _device_of(x, "x")
-    x_dtype, x_bf16, w_dtype, w_bf16 = _norm_types(x, (weight, d_weight, d_bias))
     T, H = nm.num_tokens, nm.hidden
+    x_bf16, x_dtype, w_bf16, w_dtype = _is_bf16(x, "x"), x.dtype, 0, torch.float32
+    for param in (weight, d_weight, d_bias):
+        if param is not None:
+            w_bf16, w_dtype = _is_bf16(param, "weight"), param.dtype
+            break
     xp, x_stride = _rows_arg(x, "x", nm, x_dtype, dev)
     gp, g_stride = _rows_arg(dy, "dy", nm, x_dtype, dev)
     wp = _arg(weight, "weight", w_dtype, (H,), dev, allow_none=True)

@@ -159,23 +159,33 @@ hipError_t launch_combine_backward(const ep_problem& p, const void* dy, const vo
     const int64_t R = p.capacity == 0 ? static_cast<int64_t>(T) * p.num_topk
                                       : static_cast<int64_t>(p.num_experts) * p.capacity;
     const int nvec = p.hidden / 8;
-    const int vpl = (nvec + kMaxThreads - 1) / kMaxThreads;
+    // Two pieces per lane where a row is more than two waves' and there are fewer than
+    // 2048 tokens, from five entries on: half the waves, each with twice as much in flight (517 tokens,
+    // H 4096, top-6: 12.7 us with one piece, 10.2 with two; 1000, H 2048: 11.4 and
+    // 10.0; 1000, H 4096, top-8: 26.9 and 25.8; but 2000, H 4096, top-6: 42.3 and 43.5).
+    const int k = p.num_topk;
+    int vpl = (nvec + kMaxThreads - 1) / kMaxThreads;
+    if (vpl == 1 && T < 2048 && nvec > 2 * kWave && k >= 5) vpl = 2;
     const int lanes = (nvec + vpl - 1) / vpl;
     const int threads = (lanes + kWave - 1) / kWave * kWave;
     const auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3(T), dim3(threads), 0, stream, static_cast<const u32x4*>(dy),
-                           static_cast<const u32x4*>(expert_out), nvec, p.num_topk, slot_of, R,
+                           static_cast<const u32x4*>(expert_out), nvec, k, slot_of, R,
                            topk_weights, drop, static_cast<u32x4*>(d_expert_out), d_weights);
     };
     if (vpl > 2)
         go(combine_backward_kernel<8, 1>);
-    else if (vpl == 2)
+    else if (vpl == 2 && k <= 4)
         go(combine_backward_kernel<2, 4>);
-    else if (p.num_topk <= 2)
+    else if (vpl == 2 && k <= 6)
+        go(combine_backward_kernel<2, 6>);
+    else if (vpl == 2)
+        go(combine_backward_kernel<2, 8>);
+    else if (k <= 2)
         go(combine_backward_kernel<1, 2>);
-    else if (p.num_topk <= 4)
+    else if (k <= 4)
         go(combine_backward_kernel<1, 4>);
-    else if (p.num_topk <= 6)
+    else if (k <= 6)
         go(combine_backward_kernel<1, 6>);
     else
         go(combine_backward_kernel<1, 8>);
