@@ -258,10 +258,10 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
                      has ? x_at + i * 8 * K : kNowhere, c);
     };
 
-    // Products: waves 0-3 take the first half of the rows, so that a tile that
-    // is at most half full costs each SIMD half.
+    // Products.  A wave multiplies those of its 16-row tiles that hold rows; waves
+    // 0-3 take the first half of the rows, so that every SIMD has one wave of each half.
     const int w_half = wave % 2, x_group = wave / 2;
-    const bool idle = rows_here <= x_group * 16 * XT;
+    const int tiles_here = (rows_here + 15) / 16 - x_group * XT;  // not positive: none
     const int place = r16 * 8 + (group ^ r16 % 8);  // of chunk 0; chunk 1: place ^ 4
     i32x4 acc[WT][XT];
 #pragma unroll
@@ -271,19 +271,21 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
     struct Frags {
         u32x4 w[WT], x[XT];
     };
-    const auto fetch = [&](Frags& f, int w_buf, int x_buf, int h) {  // chunk h of a stage
+    const auto fetch = [&](auto active, Frags& f, int w_buf, int x_buf, int h) {  // chunk h of a stage
+        constexpr int M = decltype(active)::value;
+        if constexpr (M == 0) return;
         const u32x4* w = &s_w[(w_buf * kTileW + w_half * 128) * 8];
         const u32x4* x = &s_x[(x_buf * MC + x_group * 16 * XT) * 8];
 #pragma unroll
-        for (int m = 0; m < XT; ++m) f.x[m] = x[m * 128 + (place ^ 4 * h)];
+        for (int m = 0; m < M; ++m) f.x[m] = x[m * 128 + (place ^ 4 * h)];
 #pragma unroll
         for (int t = 0; t < WT; ++t) f.w[t] = w[t * 128 + (place ^ 4 * h)];
     };
-    const auto multiply = [&](const Frags& f) {
+    const auto multiply = [&](auto active, const Frags& f) {
 #pragma unroll
         for (int t = 0; t < WT; ++t)
 #pragma unroll
-            for (int m = 0; m < XT; ++m) acc[t][m] = mfma(f.w[t], f.x[m], acc[t][m]);
+            for (int m = 0; m < decltype(active)::value; ++m) acc[t][m] = mfma(f.w[t], f.x[m], acc[t][m]);
     };
 
     // The scales that the products take at the end, one per thread.
@@ -318,36 +320,46 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    // Each chunk's fragments are fetched while the chunk before is multiplied.
-    int w_buf = 0, x_buf = 0;
-    Frags even, odd;
-    if (!idle) fetch(even, 0, 0, 0);
-    for (uint32_t c = 0; c < K; c += kStep) {
-        const int w_next = w_buf == WB - 1 ? 0 : w_buf + 1, x_next = x_buf == XB - 1 ? 0 : x_buf + 1;
-        if (!idle) {
-            fetch(odd, w_buf, x_buf, 1);
+    // Each chunk's fragments are fetched while the chunk before is multiplied.  One
+    // loop for each number of a wave's tiles, with the same barriers.
+    const auto all_stages = [&](auto active) {
+        int w_buf = 0, x_buf = 0;
+        Frags even, odd;
+        fetch(active, even, 0, 0, 0);
+        for (uint32_t c = 0; c < K; c += kStep) {
+            const int w_next = w_buf == WB - 1 ? 0 : w_buf + 1;
+            const int x_next = x_buf == XB - 1 ? 0 : x_buf + 1;
+            fetch(active, odd, w_buf, x_buf, 1);
             __builtin_amdgcn_sched_barrier(0);
-            multiply(even);
+            multiply(active, even);
             __builtin_amdgcn_sched_barrier(0);
+            stage_ready();  // the next one; this one's buffers are free
+            load_x(c + XB * kStep, x_buf);
+            load_w(c + WB * kStep, w_buf);
+            fetch(active, even, w_next, x_next, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(active, odd);
+            __builtin_amdgcn_sched_barrier(0);
+            w_buf = w_next;
+            x_buf = x_next;
         }
-        stage_ready();  // the next one; this one's buffers are free
-        load_x(c + XB * kStep, x_buf);
-        load_w(c + WB * kStep, w_buf);
-        if (!idle) {
-            fetch(even, w_next, x_next, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(odd);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        w_buf = w_next;
-        x_buf = x_next;
-    }
+    };
+    if (tiles_here >= XT)
+        all_stages(std::integral_constant<int, XT>{});
+    else if (XT > 3 && tiles_here == 3)
+        all_stages(std::integral_constant<int, XT < 3 ? XT : 3>{});
+    else if (XT > 2 && tiles_here == 2)
+        all_stages(std::integral_constant<int, XT < 2 ? XT : 2>{});
+    else if (XT > 1 && tiles_here == 1)
+        all_stages(std::integral_constant<int, 1>{});
+    else
+        all_stages(std::integral_constant<int, 0>{});
     __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // loads of nothing, but into LDS
     __syncthreads();
     float* s_scale = reinterpret_cast<float*>(s_w);  // of the weight rows, then of the rows
     s_scale[threadIdx.x] = scale;
     __syncthreads();
-    if (idle) return;
+    if (tiles_here <= 0) return;
 
     // lane l holds outputs 4 * (l / 16) .. + 3 of a tile for row l % 16
     constexpr int OT = GATED ? WT / 2 : WT;
