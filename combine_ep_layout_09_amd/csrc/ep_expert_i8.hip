@@ -26,6 +26,7 @@ namespace {
 using namespace expert;
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
 
 constexpr int kTiles = 4;            // 16-row weight tiles of a wave
 constexpr int kRows = 16 * kTiles;   // weight rows of a wave
@@ -356,40 +357,57 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
         all_stages(std::integral_constant<int, 0>{});
     __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // loads of nothing, but into LDS
     __syncthreads();
-    float* s_scale = reinterpret_cast<float*>(s_w);  // of the weight rows, then of the rows
+    float* s_scale = reinterpret_cast<float*>(s_x);  // of the weight rows, then of the rows
     s_scale[threadIdx.x] = scale;
     __syncthreads();
-    if (tiles_here <= 0) return;
 
-    // lane l holds outputs 4 * (l / 16) .. + 3 of a tile for row l % 16
+    // Outputs change places in LDS, so that a row's leave together, 16 bytes a lane, at
+    // whatever address: an odd N has rows of any alignment.  Lane l holds outputs 4 * (l / 16) .. + 3
+    // of a tile for row l % 16; piece q (8 outputs) of row r lies at place q ^ (r % 16).
+    // All rows at once, or those of waves 0-3 and of 4-7 in turn where they do not fit.
     constexpr int OT = GATED ? WT / 2 : WT;
+    constexpr int kPieces = kOut / 8;
+    constexpr int kTurns = MC * kOut * 2 > static_cast<int>(sizeof(s_w)) ? 2 : 1;
+    constexpr int kTurnRows = MC / kTurns;
+    uint2* s_out = reinterpret_cast<uint2*>(s_w);
     const float* w_scale = &s_scale[w_half * 128 + group * 4];
-    const bool whole = N % 4 == 0;
 #pragma unroll
-    for (int m = 0; m < XT; ++m) {
-        const int r = (x_group * XT + m) * 16 + r16;
-        if (r >= rows_here) continue;
-        const float row_scale = s_scale[kTileW + r];
-        uint16_t* row = a.out + (row0 + r) * N + n0;
+    for (int turn = 0; turn < kTurns; ++turn) {
+        if (turn > 0) __syncthreads();
+        if (x_group / (4 / kTurns) == turn) {
 #pragma unroll
-        for (int t = 0; t < OT; ++t) {
-            const int n = (w_half * OT + t) * 16 + group * 4;
-            float y[4];
+            for (int m = 0; m < XT; ++m) {
+                if (m >= tiles_here) break;
+                const int r = (x_group * XT + m) * 16 + r16;
+                const float row_scale = s_scale[kTileW + r];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                y[i] = scaled(acc[t][m][i], row_scale, w_scale[t * 16 + i]);
-                if constexpr (GATED)
-                    y[i] = silu(y[i]) *
-                           scaled(acc[t + OT][m][i], row_scale, w_scale[(t + OT) * 16 + i]);
+                for (int t = 0; t < OT; ++t) {
+                    const int n = (w_half * OT + t) * 16 + group * 4;
+                    float y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        y[i] = scaled(acc[t][m][i], row_scale, w_scale[t * 16 + i]);
+                        if constexpr (GATED)
+                            y[i] = silu(y[i]) *
+                                   scaled(acc[t + OT][m][i], row_scale, w_scale[(t + OT) * 16 + i]);
+                    }
+                    const int at = (r - turn * kTurnRows) * kPieces + (n / 8 ^ r16);
+                    s_out[at * 2 + n / 4 % 2] = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+                }
             }
-            const uint32_t lo = pack_bf16(y[0], y[1]), hi = pack_bf16(y[2], y[3]);
-            if (whole) {
-                if (n < here) *reinterpret_cast<uint2*>(row + n) = make_uint2(lo, hi);
+        }
+        __syncthreads();
+        const int rows_now = rows_here - turn * kTurnRows < kTurnRows ? rows_here - turn * kTurnRows : kTurnRows;
+        for (int i = threadIdx.x; i < rows_now * kPieces; i += kTileWaves * kWave) {
+            const int r = i / kPieces, q = i % kPieces;
+            const u32x4 v = reinterpret_cast<const u32x4*>(s_w)[r * kPieces + (q ^ r % 16)];
+            uint16_t* to = a.out + (row0 + turn * kTurnRows + r) * N + n0 + q * 8;
+            if (q * 8 + 8 <= here) {
+                *reinterpret_cast<u32x4_at2*>(to) = v;
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (n + i < here)
-                        row[n + i] = static_cast<uint16_t>((i < 2 ? lo : hi) >> (16 * (i & 1)));
+                for (int k = 0; k < 8; ++k)
+                    if (q * 8 + k < here) to[k] = static_cast<uint16_t>(v[k / 2] >> (16 * (k % 2)));
             }
         }
     }

@@ -149,7 +149,7 @@ __device__ __forceinline__ void pair_sums(float (&c1)[B], float (&c2)[B],
 }
 
 template <bool XB, bool WB, int V, int B>
-__global__ __launch_bounds__(kMaxThreads) void norm_grad_kernel(NormGradArgs a, int L, float* out) {
+__global__ __launch_bounds__(kMaxThreads) void norm_grad_kernel(NormGradArgs a, int L, float* parts) {
     typedef Piece<XB> X;
     constexpr int P = X::P;
     __shared__ float s_part[2][kMaxThreads / kWave][2 * B];
@@ -247,9 +247,9 @@ __global__ __launch_bounds__(kMaxThreads) void norm_grad_kernel(NormGradArgs a, 
         }
         if constexpr (kAhead) now = next;
     }
-    if (out == nullptr) return;
-    out += static_cast<int64_t>(blockIdx.x) * 2 * a.hidden;
-    // one gradient after the other through LDS
+    if (a.d_weight == nullptr && a.d_bias == nullptr) return;
+    // one gradient after the other through LDS, to this workgroup's part, or, where it
+    // is the only one, to the gradient itself
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         if (which == 1) __syncthreads();
@@ -262,7 +262,10 @@ __global__ __launch_bounds__(kMaxThreads) void norm_grad_kernel(NormGradArgs a, 
         for (int c = threadIdx.x; c < a.hidden; c += blockDim.x) {
             float sum = 0.0f;
             for (int q = 0; q < groups; ++q) sum += s_sum[q * L * V * P + c];
-            out[static_cast<int64_t>(which) * a.hidden + c] = sum;
+            if (gridDim.x == 1)
+                store_param<WB>(which == 0 ? a.d_weight : a.d_bias, c, sum);
+            else
+                parts[(static_cast<int64_t>(blockIdx.x) * 2 + which) * a.hidden + c] = sum;
         }
     }
 }
@@ -392,13 +395,7 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void norm_join_kernel(const floa
     s = 0.0f;
 #pragma unroll
     for (int w = 0; w < kJoinWaves; ++w) s += s_sum[w][lane];
-    void* out = i < H ? dw : db;
-    const int c = i < H ? i : i - H;
-    if (out == nullptr) return;
-    if (WB)
-        static_cast<__bf16*>(out)[c] = static_cast<__bf16>(s);
-    else
-        static_cast<float*>(out)[c] = s;
+    store_param<WB>(i < H ? dw : db, i < H ? i : i - H, s);
 }
 
 // Lanes per row: as few as hold the row with at most `most` pieces each, more
@@ -456,15 +453,18 @@ hipError_t launch_norm_grad_types(const NormGradArgs& a, void* workspace, hipStr
     float* parts = static_cast<float*>(workspace);
     const int most = a.num_tokens > 0 ? norm_parts(a.num_tokens, a.hidden) : 0;
     int n = 0;  // parts written
+    bool joined = false;
     if (a.num_tokens > 0 && pieces <= 2 * kMaxThreads) {
         const int lanes = (pieces <= kMaxThreads ? pieces : (pieces + 1) / 2);
         const int L = (lanes + kWave - 1) / kWave * kWave;
         const int groups = kMaxThreads / L;
         const auto go = [&](auto kernel, int rows) {  // rows of a group's turn
             const int each = groups * rows, turns = (a.num_tokens + each - 1) / each;
-            n = turns < most ? turns : most;
-            hipLaunchKernelGGL(kernel, dim3(n), dim3(groups * L), 0, stream, a, L,
-                               params ? parts : nullptr);
+            // Few rows: one workgroup, whose sums are the gradients; a second launch
+            // takes longer than its few turns.
+            n = turns <= 2 ? 1 : turns < most ? turns : most;
+            hipLaunchKernelGGL(kernel, dim3(n), dim3(groups * L), 0, stream, a, L, parts);
+            if (n == 1) joined = true;
         };
         if (pieces <= kMaxThreads)
             go(norm_grad_kernel<XB, WB, 1, 2>, 2);
@@ -482,7 +482,7 @@ hipError_t launch_norm_grad_types(const NormGradArgs& a, void* workspace, hipStr
                                dim3(kColumnWaves * kWave), 0, stream, a, run, parts);
         }
     }
-    if (params) launch_join<WB>(a, parts, n, stream);
+    if (params && !joined) launch_join<WB>(a, parts, n, stream);
     return hipGetLastError();
 }
 

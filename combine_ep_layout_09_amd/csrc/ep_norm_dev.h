@@ -121,6 +121,15 @@ __device__ __forceinline__ void load_params(const void* p, int c, int H, float o
     }
 }
 
+template <bool BF16>
+__device__ __forceinline__ void store_param(void* p, int c, float v) {
+    if (p == nullptr) return;
+    if (BF16)
+        static_cast<__bf16*>(p)[c] = static_cast<__bf16>(v);
+    else
+        static_cast<float*>(p)[c] = v;
+}
+
 // Sum over the lanes of a row of 16, in every lane, by rotation.
 __device__ __forceinline__ float row16_sum(float v) {
     const auto turned = [&](auto i) {
