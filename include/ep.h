@@ -423,7 +423,8 @@ int ep_layer_norm_backward(const ep_norm* nm, const void* x, int x_bf16, int64_t
  * Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011) at
  * the counter {c / 4, t, low(offset), high(offset)} under the key
  * {low(seed), high(seed)} (low and high 32-bit halves), and is kept where the
- * word is at least p * 2^32, rounded to the nearest integer.
+ * word is at least p * 2^32, rounded to the nearest integer and at most 2^32 - 1.  Calls
+ * on parts of a batch count their tokens from 0 each: they take an offset each.
  *   p     0 <= p < 1, the probability of a zero.  0: nothing is dropped.
  *   rng   uint64 [2] {seed, offset}, device, 8-byte aligned; read when the kernel runs, so that
  *         a replayed graph takes another mask once the program has written another offset.  NULL

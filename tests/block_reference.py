@@ -140,7 +140,7 @@ def quant(x):
 
 def i8_products(q, row_scale, w, scale, gated):
     """(y, bound) of rows q int8 [M, K] with weights int8 [n2, K]."""
-    s = (q.astype(np.int64) @ w.astype(np.int64).T).astype(np.float64)
+    s = q.astype(np.float64) @ w.astype(np.float64).T  # whole numbers below 2^53: exact
     y = s * row_scale.astype(np.float64)[:, None] * scale.astype(np.float64)[None]
     e = 4 * U * np.abs(y)
     if gated:

@@ -193,3 +193,50 @@ def served_layer(T, cap, captured):
 @pytest.mark.parametrize("captured", [False, True])
 def test_served_layer(T, cap, captured):
     served_layer(T, cap, captured)
+
+
+def test_no_tokens():
+    """Batches without a token launch nothing."""
+    prob = ep.Problem(0, 64, 2, 4)
+    lay = ep.Layout(*(torch.zeros(n, dtype=I32, device=DEV) for n in (4, 5, 0, 0, 2)))
+    x, w = torch.empty((0, 64), dtype=BF16, device=DEV), torch.empty((0, 2), device=DEV)
+    rng = torch.zeros(2, dtype=torch.int64, device=DEV)
+    ep.ep_combine_dropout(prob, x, lay, w, 0.5, rng, x.clone(), residual=x.clone())
+    ep.ep_combine_backward(prob, x, x, lay, w, 0.5, rng, x.clone(), w.clone())
+    ep.ep_dispatch_i8(prob, x, lay, torch.empty((0, 64), dtype=torch.int8, device=DEV),
+                      torch.empty(0, device=DEV))
+    torch.cuda.synchronize()
+
+
+def test_prepared_calls():
+    """The calls checked and marshalled once give what the plain ones give."""
+    s = Step(T=50, H=264)
+    s.run()
+    torch.cuda.synchronize()
+    want = {n: getattr(s, n).clone() for n in ("n", "mean", "rstd", "y", "deo", "dw", "dx", "dnw", "dnb")}
+    q, qs = torch.zeros((100, 264), dtype=torch.int8, device=DEV), torch.zeros(100, device=DEV)
+    mm = ep.ExpertI8(264 // 16 * 16, 40, 0)
+    rows = torch.randn(100, mm.in_features, device=DEV).to(BF16)
+    weights = torch.randint(-128, 128, (8, 40, mm.in_features), device=DEV, dtype=torch.int8)
+    scales, out = torch.rand((8, 40), device=DEV), torch.zeros((100, 40), dtype=BF16, device=DEV)
+    space = torch.empty(ep.ep_expert_i8_workspace_bytes(s.prob, mm), dtype=torch.uint8, device=DEV)
+    ep.ep_dispatch_i8(s.prob, s.x, s.lay, q, qs)
+    ep.ep_expert_i8(s.prob, mm, rows, s.lay, weights, scales, out, workspace=space)
+    want.update(q=q.clone(), qs=qs.clone(), out=out.clone())
+    calls = [
+        ep.prepare_layer_norm(s.nm, s.x, s.nw, s.nb, s.n, mean=s.mean, rstd=s.rstd),
+        ep.prepare_combine_dropout(s.prob, s.eo, s.lay, s.w, s.p, s.rng, s.y, residual=s.x),
+        ep.prepare_combine_backward(s.prob, s.dy, s.eo, s.lay, s.w, s.p, s.rng, s.deo, s.dw),
+        ep.prepare_layer_norm_backward(s.nm, s.x, s.dn, s.nw, s.mean, s.rstd, s.dx, d_weight=s.dnw,
+                                       d_bias=s.dnb, workspace=s.space, d_skip=s.dy),
+        ep.prepare_dispatch_i8(s.prob, s.x, s.lay, q, qs),
+        ep.prepare_expert_i8(s.prob, mm, rows, s.lay, weights, scales, out, workspace=space),
+    ]
+    got = dict({n: getattr(s, n) for n in want if hasattr(s, n)}, q=q, qs=qs, out=out)
+    for t in got.values():
+        t.fill_(1)
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    for n, t in want.items():
+        assert torch.equal(got[n], t), n

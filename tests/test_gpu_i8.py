@@ -204,6 +204,41 @@ def test_skewed_and_empty_experts(gated):
     Case(idx, E, 64, 272, 130, 0, gated).check()
 
 
+def filled(counts):
+    """One entry per token; experts with these numbers of rows, in any order."""
+    idx = np.repeat(np.arange(len(counts), dtype=np.int32), counts)[:, None]
+    np.random.default_rng(len(idx)).shuffle(idx)
+    return idx
+
+
+# rows of the experts: for row tiles of 256, of 128 and of 64 rows
+MANY = {
+    "256": [300, 1, 512, 0, 257, 700, 31, 240, 255, 129, 65, 900, 400, 128, 333, 177],
+    "128": [80] * 30 + list(range(97, 129)) + [129, 256, 0, 1, 17, 63],
+    "64": [20] * 40 + list(range(0, 66)) + [128, 129],
+}
+
+
+@pytest.mark.parametrize("K", [16, 80, 128, 272, 400, 512])
+@pytest.mark.parametrize("N,gated", [(4100, False), (2049, True), (4097, False), (4352, False)])
+@pytest.mark.parametrize("rows", MANY)
+def test_many_rows(rows, N, gated, K):
+    """Workgroups enough for each form of the many-row kernel: every filling of a row
+    tile, channels that end inside a chunk, outputs that end inside a block, odd ones."""
+    if rows != "256":
+        N = N // 4 + N % 2
+    counts = MANY[rows]
+    c = Case(filled(counts), len(counts), 0, K, N, 1, gated)
+    c.check()
+
+
+def test_many_rows_in_the_fixed_capacity_layout():
+    counts = MANY["256"]
+    for cap in (300, 1000):
+        Case(filled(counts), len(counts), cap, 208, 3600, 0, False).check()
+    Case(filled(MANY["128"]), len(MANY["128"]), 120, 336, 1100, 0, True).check()
+
+
 @pytest.mark.parametrize("T", [3, 400])
 def test_largest_sums(T):
     """65536 products of -128 and -128: 2^30."""
@@ -245,11 +280,11 @@ def test_layout_of_another_problem_stays_inside():
     assert (c.run().view(torch.int16) == SENTINEL).all()
 
 
-def test_rows_and_weights_beyond_32_bit_offsets():
+@pytest.mark.parametrize("T", [20, 40])  # each kernel
+def test_rows_and_weights_beyond_32_bit_offsets(T):
     """Weights of 4.5 GB and receive rows of 2.3 GB; the last expert's, at the end
     of both."""
     E, K, N, cap = 3, 65536, 23000, 12000
-    T = 40
     idx = np.full((T, 1), 2, np.int32)
     idx[0] = 0
     r, lay = make_layout(idx, E, cap)
@@ -332,6 +367,30 @@ def test_replayed_graph_and_streams():
         torch.cuda.synchronize()
         for o, w in zip(outs, want):
             assert torch.equal(o, w), i
+
+
+def test_layout_of_another_problem_dispatch():
+    """Slots outside the receive rows are not followed."""
+    T, H, k, E = 30, 128, 3, 8
+    prob = ep.Problem(T, H, k, E)
+    r, lay = make_layout(uniform(T, E, k), E, 0)
+    lay.slot_of[::2] += T * k
+    lay.slot_of[1::4] = -3
+    x = torch.randn(T, H, device=DEV).bfloat16()
+    q = torch.full((T * k, H), 0x5A, dtype=torch.int8, device=DEV)
+    s = torch.full((T * k,), 77.0, device=DEV)
+    ep.ep_dispatch_i8(prob, x, lay, q, s)
+    torch.cuda.synchronize()
+    want, scale = ref.quant(x.float().cpu().numpy())
+    slot = lay.slot_of.cpu().numpy()
+    there = np.zeros(T * k, bool)
+    for t in range(T):
+        for j in range(k):
+            if 0 <= slot[t, j] < T * k:
+                there[slot[t, j]] = True
+                assert np.array_equal(q[slot[t, j]].cpu().numpy(), want[t])
+                assert float(s[slot[t, j]]) == float(scale[t])
+    assert (q.cpu().numpy()[~there] == 0x5A).all() and (s.cpu().numpy()[~there] == 77.0).all()
 
 
 def test_binding_refuses():
