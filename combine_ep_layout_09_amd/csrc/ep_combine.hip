@@ -53,8 +53,9 @@ struct Plain {
 };
 
 // Dropout and the skip connection (ep_combine_dropout).  Eight channels of a piece
-// are two counters of the generator.  Persistent and per-token form, with the skip
-// connection: H 4096, top-6, 2600 tokens (30 rows per wave): 28.6 us and 27.2, 3500 (41) 38.8
+// are two counters of the generator.  4096 tokens, H 7168, top-8 with the skip connection:
+// 94 us, 6.2 TB/s, as long with p = 0: the mask is made under the loads.  Persistent and
+// per-token form: H 4096, top-6, 2600 tokens (30 rows per wave): 28.6 us and 27.2, 3500 (41) 38.8
 // and 39.9; H 7168, top-8, 1200 (33): 30.3 both, 4096 94.2 and 102.5; 517 tokens of H 4096 12.1
 // and 8.1.
 struct Dropped {

@@ -72,6 +72,12 @@ struct Stage {
 // covers 8 weight rows x 128 bytes, whole cache lines that are not kept; two
 // chunks change places across lanes afterwards (pair_chunks).  GATED: tiles 0, 1 are
 // rows n of the gate half and tiles 2, 3 rows N + n.
+//
+// Reading the weights bounds it.  128 tokens over 256 experts, top-8: K 7168, N 2048
+// gated 1065 to 1070 us, 6.9 TB/s; K 2048, N 7168 560 to 572, 6.5 TB/s, 16 steps for
+// four waves; one token, K 7168, N 2048 gated: 40 us, 5.9 TB/s.  Two waves take 37 there but
+// 141 where four take 123 (64 experts of 8 rows, K 4096, N 1408 gated), and 18
+// where four take 12 (32 of 6, K 4096, N 167).
 template <int WAVES, bool GATED>
 __global__ __launch_bounds__(WAVES* kWave, 4) void expert_i8_kernel(Args a) {
     constexpr int kThreads = WAVES * kWave;
@@ -170,12 +176,14 @@ __global__ __launch_bounds__(WAVES* kWave, 4) void expert_i8_kernel(Args a) {
 // stage ahead, 515 two.)  Up to XT 2 an expert mostly has one row tile, so its
 // weights are not kept in the caches (24 rows each: 140 us, kept 151).
 //
-// That batch, K 4096, N 1408 gated: 566 us, 2.0 POP/s of its own rows and 2.2 with the
-// tiles' empty ones; an 8192^3 int8 library product reaches 2.06.  The matrix cores are
-// busy for 47 % of the time, at 2.03 GHz; without loads it takes 435 us, without
-// products 449.  4096 tokens over 256 experts, K 7168, N 2048 gated: 1529 us, the
-// weights at 5.2 TB/s.  Matrix instructions of 32 x 32 x 32 were slower (625 us), and so
-// was a stage through registers (648 where this took 596).
+// That batch, K 4096, N 1408 gated: 559 to 573 us, 2.0 POP/s; 49152 rows of one expert
+// 2.35 POP/s; an 8192^3 int8 library product 2.06.  LDS and the matrix cores bound it
+// together: fragments and stages take LDS as many cycles as the products take them, which
+// are busy for 47 % of the time, at 2.0 to 2.1 GHz (435 us without loads, 449 without
+// products).  4096 tokens over 256 experts, K 7168, N 2048 gated: 1483 us, the
+// weights at 5.3 TB/s.  Slower were matrix instructions of 32 x 32 x 32 (625 where this
+// took 566), a stage through registers (648 where this took 596) and four waves of
+// 128 x 128 (637 where this took 600).
 constexpr int kTileWaves = 8;
 constexpr int kTileW = 256;  // weight rows of a workgroup
 constexpr int kTileGroup = 8;
