@@ -93,11 +93,11 @@ def test_dispatch_of_unrouted_tokens():
 def test_every_quotient_of_a_scale():
     """All bf16 magnitudes up to the row's largest, for scales of every mantissa
     that bf16 rows can have, positive and negative."""
-    H = 2 * 128 * 12
+    H = 2 * 128 * 13
     rows = []
     for top in range(128):
         amax = (1 + top / 128) * 2.0 ** 3
-        steps = np.exp2(np.arange(-8, 4)[:, None]) * (1 + np.arange(128) / 128)[None]
+        steps = np.exp2(np.arange(-9, 4)[:, None]) * (1 + np.arange(128) / 128)[None]
         v = steps.reshape(-1)
         v = np.where(v <= amax, v, amax)
         rows.append(np.concatenate([v, -v]))
