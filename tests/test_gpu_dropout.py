@@ -129,6 +129,16 @@ def test_tokens_without_a_row():
     assert not c.forward()[7].any()
 
 
+def test_an_expert_twice():
+    """A token that names an expert twice has two rows there."""
+    idx = uniform(60, 8, 4, seed=9)
+    idx[:, 2] = idx[:, 0]
+    idx[::3, 1] = idx[::3, 0]
+    c = Case(idx, 8, 0, 520, 0.2)
+    c.check_forward()
+    c.check_backward()
+
+
 @pytest.mark.parametrize("T", [40, 2100])
 def test_without_dropout_it_is_the_combine(T):
     """p = 0 and no skip connection: the bits of ep_combine, in both launch forms."""
