@@ -2,8 +2,11 @@
 // rows and the routing weights.
 //
 //   g[t]            = kept ? dy[t] * f : 0          (f = 1 / (1 - p))
-//   d_expert_out[s] = w[t, j] g[t]                  s the receive row of entry (t, j)
-//   d_weights[t, j] = <g[t], expert_out[s]>
+//   d_expert_out[s] = kept ? w[t, j] g[t] : 0       s the receive row of entry (t, j)
+//   d_weights[t, j] = <g[t], expert_out[s]>         over the kept channels
+//
+// Dropped channels are selected out of all three: the output does not depend on what
+// is there, so that an infinite weight or expert row there leaves no 0 * inf.
 //
 // A workgroup takes a token.  A lane holds VPL 16-byte pieces of dy with the
 // dropped channels zeroed, made once for all k entries.  Entries are taken in batches of
@@ -72,6 +75,7 @@ __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
     bool here[VPL];
     u32x4 dyv[VPL];
     float g[VPL][8];
+    uint32_t pass[VPL][4];  // ones at the kept channels' halves of a piece's words
 #pragma unroll
     for (int u = 0; u < VPL; ++u) {
         const int at = threadIdx.x + u * blockDim.x;
@@ -116,6 +120,9 @@ __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
                     const float f = (i % 2 == 0 ? bf16_lo(word) : bf16_hi(word)) * drop.factor;
                     g[u][i] = kept >> i & 1 ? f : 0.0f;
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    pass[u][i] = (kept >> 2 * i & 1 ? 0xffffu : 0u) | (kept >> 2 * i & 2 ? 0xffff0000u : 0u);
             }
         }
         float sums[8];
@@ -129,9 +136,10 @@ __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float lo = g[u][2 * i], hi = g[u][2 * i + 1];
-                    sums[jj] = fmaf(lo, bf16_lo(e[jj][u][i]), sums[jj]);
-                    sums[jj] = fmaf(hi, bf16_hi(e[jj][u][i]), sums[jj]);
-                    d[i] = pack_bf16(lo * wj[jj], hi * wj[jj]);
+                    const uint32_t word = e[jj][u][i] & pass[u][i];
+                    sums[jj] = fmaf(lo, bf16_lo(word), sums[jj]);
+                    sums[jj] = fmaf(hi, bf16_hi(word), sums[jj]);
+                    d[i] = pack_bf16(lo * wj[jj], hi * wj[jj]) & pass[u][i];
                 }
                 if (ok[jj] && here[u]) __builtin_nontemporal_store(d, deo + row[jj] + v[u]);
             }

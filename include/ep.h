@@ -442,8 +442,8 @@ int ep_combine_dropout(const ep_problem* prob, const void* expert_out, const ep_
 /* Gradients of ep_combine_dropout (of ep_combine, with p = 0) in the expert rows
  * and the routing weights; the residual's is dy itself.  With g = kept ? dy * f : 0,
  * for every entry (t, j) with a slot:
- *   d_expert_out[slot][c] = bf16_RNE(topk_weights[t, j] * g[t][c])
- *   d_weights[t, j] = sum_c g[t][c] * expert_out[slot][c]      (fp32, a fixed order)
+ *   d_expert_out[slot][c] = kept ? bf16_RNE(topk_weights[t, j] * g[t][c]) : 0
+ *   d_weights[t, j] = sum over kept c of g[t][c] * expert_out[slot][c]  (fp32, a fixed order)
  *   dy            bf16 [T, H], device.
  *   expert_out    as given to ep_combine_dropout; may be NULL if d_weights is.
  *   d_expert_out  bf16 [R, H], device.  Rows that no entry fills are not written.

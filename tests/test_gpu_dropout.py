@@ -189,6 +189,26 @@ def test_dropped_elements_do_not_pass_on_what_is_not_finite():
     assert not rows[~keep].any() and torch.isnan(rows[keep]).all()
 
 
+@pytest.mark.parametrize("T,k,H", [(12, 2, 512), (30, 6, 4096), (9, 7, 16392), (2100, 8, 520)])
+def test_gradients_do_not_take_what_is_not_finite_from_dropped_channels(T, k, H):
+    """Infinities and NaN in the expert rows' and the gradient's dropped channels and
+    an infinite weight: the output does not depend on any of them there."""
+    c = Case(uniform(T, 8, k), 8, 0, H, 0.5)
+    keep = torch.from_numpy(c.keep()).to(DEV)
+    slot = c.lay.slot_of.long()
+    clean, want = c.backward()
+    for j in range(k):
+        c.eo[slot[:, j]] = torch.where(keep, c.eo[slot[:, j]], float("inf") if j % 2 else float("nan"))
+    c.dy = torch.where(keep, c.dy, float("-inf"))
+    deo, dw = c.backward()
+    assert torch.equal(dw, want) and torch.equal(deo, clean)
+    c.w[:, 0] = float("inf")
+    deo, dw = c.backward()
+    assert torch.equal(dw, want)
+    rows = deo[slot[:, 0]]
+    assert not rows[~keep].any() and not torch.isfinite(rows[keep]).any()
+
+
 def test_without_the_weights_gradient():
     c = Case(uniform(70, 16, 4), 16, 20, 1288, 0.2)
     deo, dw = c.backward()
