@@ -15,7 +15,7 @@
 // each gradient row written once.
 //
 // Memory bounds it, as many bytes written as read: 4096 tokens, H 7168, top-8, p 0.1:
-// 197 to 205 us, 5.0 TB/s; the loads alone take 111, the stores alone 116.  Fewer lanes
+// 184 to 205 us by box, 5.0 to 5.4 TB/s; the loads alone take 111, the stores alone 116.  Fewer lanes
 // with more pieces each (VPL 2 to 7: 199 to 208), batches of 512 to 2048 tokens a launch
 // (203 to 225) and stores that stay in the caches (207) were slower.
 #include <hip/hip_runtime.h>
@@ -61,7 +61,7 @@ __device__ __forceinline__ float wave_sums(float (&v)[8]) {
     return s + __shfl_xor(s, 32, kWave);
 }
 
-template <int VPL, int KB>
+template <int VPL, int KB, bool WIDE>
 __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
         const u32x4* __restrict__ dy, const u32x4* __restrict__ eo, int nvec, int k,
         const int32_t* __restrict__ slot_of, int64_t R, const float* __restrict__ weights,
@@ -71,86 +71,93 @@ __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
     const int32_t* slots = slot_of + static_cast<int64_t>(t) * k;
     const float* w = weights + static_cast<int64_t>(t) * k;
     const int wave = threadIdx.x / kWave;
-    int v[VPL];  // lanes past the end redo the last piece, and add and store nothing
-    bool here[VPL];
-    u32x4 dyv[VPL];
-    float g[VPL][8];
-    uint32_t pass[VPL][4];  // ones at the kept channels' halves of a piece's words
+    // WIDE: rows of more than two pieces per lane, a part after the other.  (512 tokens, H 16392,
+    // top-8: 61 us; a lane with eight pieces, which do not fit its registers, 203; H 65536, top-4
+    // 118 and 232; eight entries at a time 63 and 129.)
+    for (int v0 = 0; v0 < nvec; v0 += VPL * blockDim.x) {
+        int v[VPL];  // lanes past the end redo the last piece, and add and store nothing
+        bool here[VPL];
+        u32x4 dyv[VPL];
+        float g[VPL][8];
+        uint32_t pass[VPL][4];  // ones at the kept channels' halves of a piece's words
 #pragma unroll
-    for (int u = 0; u < VPL; ++u) {
-        const int at = threadIdx.x + u * blockDim.x;
-        here[u] = at < nvec;
-        v[u] = min(at, nvec - 1);
-        dyv[u] = __builtin_nontemporal_load(dy + static_cast<int64_t>(t) * nvec + v[u]);
-    }
-    for (int j0 = 0; j0 < k; j0 += KB) {
-        bool ok[KB];
-        float wj[KB];
-        int64_t row[KB];
-        u32x4 e[KB][VPL];
-#pragma unroll
-        for (int jj = 0; jj < KB; ++jj) {
-            const int j = j0 + jj;
-            const int32_t slot = j < k ? slots[j] : -1;
-            ok[jj] = slot >= 0 && slot < R;
-            wj[jj] = ok[jj] ? w[j] : 0.0f;
-            // an entry without a slot loads row 0, whose products are dropped
-            row[jj] = static_cast<int64_t>(ok[jj] ? slot : 0) * nvec;
+        for (int u = 0; u < VPL; ++u) {
+            const int at = v0 + threadIdx.x + u * blockDim.x;
+            here[u] = at < nvec;
+            v[u] = min(at, nvec - 1);
+            dyv[u] = __builtin_nontemporal_load(dy + static_cast<int64_t>(t) * nvec + v[u]);
         }
-        if (dw != nullptr) {
+        for (int j0 = 0; j0 < k; j0 += KB) {
+            bool ok[KB];
+            float wj[KB];
+            int64_t row[KB];
+            u32x4 e[KB][VPL];
 #pragma unroll
-            for (int jj = 0; jj < KB; ++jj)
+            for (int jj = 0; jj < KB; ++jj) {
+                const int j = j0 + jj;
+                const int32_t slot = j < k ? slots[j] : -1;
+                ok[jj] = slot >= 0 && slot < R;
+                wj[jj] = ok[jj] ? w[j] : 0.0f;
+                // an entry without a slot loads row 0, whose products are dropped
+                row[jj] = static_cast<int64_t>(ok[jj] ? slot : 0) * nvec;
+            }
+            if (dw != nullptr) {
 #pragma unroll
-                for (int u = 0; u < VPL; ++u)
-                    e[jj][u] = __builtin_nontemporal_load(eo + row[jj] + v[u]);
-        } else {
+                for (int jj = 0; jj < KB; ++jj)
 #pragma unroll
-            for (int jj = 0; jj < KB; ++jj)
+                    for (int u = 0; u < VPL; ++u)
+                        e[jj][u] = __builtin_nontemporal_load(eo + row[jj] + v[u]);
+            } else {
 #pragma unroll
-                for (int u = 0; u < VPL; ++u) e[jj][u] = u32x4{0, 0, 0, 0};
-        }
-        __builtin_amdgcn_sched_barrier(0);  // all loads first
-        if (j0 == 0) {
+                for (int jj = 0; jj < KB; ++jj)
 #pragma unroll
-            for (int u = 0; u < VPL; ++u) {
-                const uint32_t kept = here[u] ? dropout::keep8(drop, t, v[u]) : 0u;
+                    for (int u = 0; u < VPL; ++u) e[jj][u] = u32x4{0, 0, 0, 0};
+            }
+            __builtin_amdgcn_sched_barrier(0);  // all loads first
+            if (j0 == 0) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t word = dyv[u][i / 2];
-                    const float f = (i % 2 == 0 ? bf16_lo(word) : bf16_hi(word)) * drop.factor;
-                    g[u][i] = kept >> i & 1 ? f : 0.0f;
+                for (int u = 0; u < VPL; ++u) {
+                    const uint32_t kept = here[u] ? dropout::keep8(drop, t, v[u]) : 0u;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t word = dyv[u][i / 2];
+                        const float f = (i % 2 == 0 ? bf16_lo(word) : bf16_hi(word)) * drop.factor;
+                        g[u][i] = kept >> i & 1 ? f : 0.0f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        pass[u][i] = (kept >> 2 * i & 1 ? 0xffffu : 0u) | (kept >> 2 * i & 2 ? 0xffff0000u : 0u);
                 }
+            }
+            float sums[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    pass[u][i] = (kept >> 2 * i & 1 ? 0xffffu : 0u) | (kept >> 2 * i & 2 ? 0xffff0000u : 0u);
+            for (int jj = 0; jj < 8; ++jj) sums[jj] = 0.0f;
+#pragma unroll
+            for (int jj = 0; jj < KB; ++jj) {
+#pragma unroll
+                for (int u = 0; u < VPL; ++u) {
+                    u32x4 d;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float lo = g[u][2 * i], hi = g[u][2 * i + 1];
+                        const uint32_t word = e[jj][u][i] & pass[u][i];
+                        sums[jj] = fmaf(lo, bf16_lo(word), sums[jj]);
+                        sums[jj] = fmaf(hi, bf16_hi(word), sums[jj]);
+                        d[i] = pack_bf16(lo * wj[jj], hi * wj[jj]) & pass[u][i];
+                    }
+                    if (ok[jj] && here[u]) __builtin_nontemporal_store(d, deo + row[jj] + v[u]);
+                }
+                if (!ok[jj]) sums[jj] = 0.0f;
+            }
+            if (dw != nullptr) {
+                const float sum = wave_sums(sums);
+                const int lane = threadIdx.x % kWave;
+                const int j = j0 + (lane >> 3 & 1) + (lane >> 1 & 2) + (lane << 1 & 4);
+                if (lane < 16 && lane % 2 == 0 && j < k && j - j0 < KB)
+                    s_part[wave][j] = WIDE && v0 > 0 ? s_part[wave][j] + sum : sum;
             }
         }
-        float sums[8];
-#pragma unroll
-        for (int jj = 0; jj < 8; ++jj) sums[jj] = 0.0f;
-#pragma unroll
-        for (int jj = 0; jj < KB; ++jj) {
-#pragma unroll
-            for (int u = 0; u < VPL; ++u) {
-                u32x4 d;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float lo = g[u][2 * i], hi = g[u][2 * i + 1];
-                    const uint32_t word = e[jj][u][i] & pass[u][i];
-                    sums[jj] = fmaf(lo, bf16_lo(word), sums[jj]);
-                    sums[jj] = fmaf(hi, bf16_hi(word), sums[jj]);
-                    d[i] = pack_bf16(lo * wj[jj], hi * wj[jj]) & pass[u][i];
-                }
-                if (ok[jj] && here[u]) __builtin_nontemporal_store(d, deo + row[jj] + v[u]);
-            }
-            if (!ok[jj]) sums[jj] = 0.0f;
-        }
-        if (dw != nullptr) {
-            const float sum = wave_sums(sums);
-            const int lane = threadIdx.x % kWave;
-            const int j = j0 + (lane >> 3 & 1) + (lane >> 1 & 2) + (lane << 1 & 4);
-            if (lane < 16 && lane % 2 == 0 && j < k && j - j0 < KB) s_part[wave][j] = sum;
-        }
+        if (!WIDE) break;
     }
     if (dw == nullptr) return;
     __syncthreads();
@@ -177,31 +184,31 @@ hipError_t launch_combine_backward(const ep_problem& p, const void* dy, const vo
     // H 4096, top-6: 12.7 us with one piece, 10.2 with two; 1000, H 2048: 11.4 and
     // 10.0; 1000, H 4096, top-8: 26.9 and 25.8; but 2000, H 4096, top-6: 42.3 and 43.5).
     const int k = p.num_topk;
-    int vpl = (nvec + kMaxThreads - 1) / kMaxThreads;
-    if (vpl == 1 && T < 2048 && nvec > 2 * kWave && k >= 5) vpl = 2;
-    const int lanes = (nvec + vpl - 1) / vpl;
+    const int parts = (nvec + 2 * kMaxThreads - 1) / (2 * kMaxThreads);
+    const int vpl = nvec > kMaxThreads || (T < 2048 && nvec > 2 * kWave && k >= 5) ? 2 : 1;
+    const int lanes = (nvec + vpl * parts - 1) / (vpl * parts);
     const int threads = (lanes + kWave - 1) / kWave * kWave;
     const auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3(T), dim3(threads), 0, stream, static_cast<const u32x4*>(dy),
                            static_cast<const u32x4*>(expert_out), nvec, k, slot_of, R,
                            topk_weights, drop, static_cast<u32x4*>(d_expert_out), d_weights);
     };
-    if (vpl > 2)
-        go(combine_backward_kernel<8, 1>);
+    if (parts > 1)
+        go(combine_backward_kernel<2, 4, true>);
     else if (vpl == 2 && k <= 4)
-        go(combine_backward_kernel<2, 4>);
+        go(combine_backward_kernel<2, 4, false>);
     else if (vpl == 2 && k <= 6)
-        go(combine_backward_kernel<2, 6>);
+        go(combine_backward_kernel<2, 6, false>);
     else if (vpl == 2)
-        go(combine_backward_kernel<2, 8>);
+        go(combine_backward_kernel<2, 8, false>);
     else if (k <= 2)
-        go(combine_backward_kernel<1, 2>);
+        go(combine_backward_kernel<1, 2, false>);
     else if (k <= 4)
-        go(combine_backward_kernel<1, 4>);
+        go(combine_backward_kernel<1, 4, false>);
     else if (k <= 6)
-        go(combine_backward_kernel<1, 6>);
+        go(combine_backward_kernel<1, 6, false>);
     else
-        go(combine_backward_kernel<1, 8>);
+        go(combine_backward_kernel<1, 8, false>);
     return hipGetLastError();
 }
 

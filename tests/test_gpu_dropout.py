@@ -129,6 +129,13 @@ def test_tokens_without_a_row():
     assert not c.forward()[7].any()
 
 
+@pytest.mark.parametrize("H,k", [(16384, 3), (20480, 12), (33000, 4), (49160, 9)])
+def test_rows_longer_than_a_workgroup_holds(H, k):
+    c = Case(uniform(6, 32, k, seed=k), 32, 2, H, 0.1)
+    c.check_forward()
+    c.check_backward()
+
+
 def test_an_expert_twice():
     """A token that names an expert twice has two rows there."""
     idx = uniform(60, 8, 4, seed=9)
