@@ -472,8 +472,9 @@ hipError_t launch_norm_grad_types(const NormGradArgs& a, void* workspace, hipStr
         const auto go = [&](auto kernel, int rows) {  // rows of a group's turn
             const int each = groups * rows, turns = (a.num_tokens + each - 1) / each;
             // Few rows: one workgroup, whose sums are the gradients (one row of 7168: 9.7 us,
-            // 12.3 with a second launch; four turns of two rows: 19 and 11.5).
-            n = turns <= 2 ? 1 : turns < most ? turns : most;
+            // 12.3 with a second launch; four turns of two rows: 19 and 11.5).  Without them there is no
+            // second launch to save (four rows: 6.5, by one workgroup 9.6).
+            n = turns <= 2 && params ? 1 : turns < most ? turns : most;
             hipLaunchKernelGGL(kernel, dim3(n), dim3(groups * L), 0, stream, a, L, parts);
             if (n == 1) joined = true;
         };

@@ -185,6 +185,25 @@ def test_rows_that_are_not_finite_stay_by_themselves():
     assert torch.isnan(y[3]).all() and torch.isnan(y[5]).all()
 
 
+@pytest.mark.parametrize("T,H", [(1, 7168), (2, 7168), (4, 7168), (16, 1024)])
+def test_few_rows_without_the_parameters_gradients(T, H):
+    """The rows' gradient is the same with and without the sums over tokens."""
+    print(f"[gpu] {T} x {H}", flush=True)
+    r = np.random.default_rng(T)
+    x, dy = (torch.from_numpy(r.standard_normal((T, H)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+             for _ in range(2))
+    w = torch.from_numpy(r.standard_normal(H).astype(np.float32)).to(DEV)
+    nm = ep.Norm(T, H)
+    y, mean, rstd = torch.empty_like(x), torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    ep.ep_layer_norm(nm, x, w, None, y, mean, rstd)
+    dx, only = torch.empty_like(x), torch.empty_like(x)
+    space = torch.empty(ep.ep_layer_norm_workspace_bytes(nm), dtype=torch.uint8, device=DEV)
+    ep.ep_layer_norm_backward(nm, x, dy, w, mean, rstd, dx, torch.empty_like(w),
+                              torch.empty_like(w), space)
+    ep.ep_layer_norm_backward(nm, x, dy, w, mean, rstd, only)
+    assert torch.equal(dx, only)
+
+
 def test_no_tokens():
     nm = ep.Norm(0, 48)
     x = torch.empty((0, 48), dtype=torch.bfloat16, device=DEV)
