@@ -118,11 +118,13 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a, int L) {
 // B rows at a time, a lane V pieces of each at the same channels all along, so
 // that its sums for the gradients of weight and bias stay in registers: V P of each.
 // The next rows are loaded before these ones' sums are joined.  A workgroup's groups
-// join their sums in LDS and leave one part of both gradients (norm_join_kernel).
+// join their sums in LDS, a single group's leave as they are: one part of both gradients
+// (norm_join_kernel).
 //
-// Memory bounds it: 4096 x 7168 bf16 with d_skip 52 us for both kernels, 4.5 TB/s of what the call
-// has to move and 7 % more in parts; 86 with the rows read a second time for the sums
-// over tokens.  1999 x 1409 fp32: 12.9 us, of which the host's two launches are 12.
+// Memory bounds it: 4096 x 7168 bf16 with d_skip 49.5 us for both kernels, 4.75 TB/s of what the
+// call has to move and 7 % more in parts (a single group's sums through LDS as well: 52); 86 with
+// the rows read a second time for the sums over tokens.  1999 x 1409 fp32: 12.9 us, of which the
+// host's two launches are 12.
 
 // Sums of B pairs of values over the lanes of a group; parts: B pairs per wave.
 template <int B>
@@ -163,7 +165,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_grad_kernel(NormGradArgs a, 
     typedef Piece<XB> X;
     constexpr int P = X::P;
     __shared__ float s_part[2][kMaxThreads / kWave][2 * B];
-    __shared__ float s_sum[V * P * kMaxThreads];
+    __shared__ __attribute__((aligned(16))) float s_sum[2][V][P / 4][kMaxThreads][4];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int waves = L / kWave, group = wave / waves, wave0 = group * waves;
     const int l = threadIdx.x - group * L, groups = blockDim.x / L;
@@ -258,24 +260,47 @@ __global__ __launch_bounds__(kMaxThreads) void norm_grad_kernel(NormGradArgs a, 
         if constexpr (kAhead) now = next;
     }
     if (a.d_weight == nullptr && a.d_bias == nullptr) return;
-    // one gradient after the other through LDS, to this workgroup's part, or, where it
-    // is the only one, to the gradient itself
+    if (groups == 1 && gridDim.x > 1) {  // the lanes' sums are the part
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        if (which == 1) __syncthreads();
+        for (int which = 0; which < 2; ++which) {
+            const auto part = view(parts + (static_cast<int64_t>(blockIdx.x) * 2 + which) * a.hidden,
+                                   a.hidden * 4);
+#pragma unroll
+            for (int u = 0; u < V; ++u)
+#pragma unroll
+                for (int i = 0; i < P; i += 4) {
+                    const auto word = [&](int j) {
+                        return __float_as_uint(which == 0 ? dw[u][i + j] : db[u][i + j]);
+                    };
+                    __builtin_amdgcn_raw_buffer_store_b128(u32x4{word(0), word(1), word(2), word(3)},
+                                                           part, ((l + u * L) * P + i) * 4, 0, 0);
+                }
+        }
+        return;
+    }
+    // Through LDS, to this workgroup's part, or, where it is the only one, to the gradient
+    // itself.
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
 #pragma unroll
         for (int u = 0; u < V; ++u)
 #pragma unroll
             for (int i = 0; i < P; ++i)
-                s_sum[group * L * V * P + (l + u * L) * P + i] = which == 0 ? dw[u][i] : db[u][i];
-        __syncthreads();
-        for (int c = threadIdx.x; c < a.hidden; c += blockDim.x) {
-            float sum = 0.0f;
-            for (int q = 0; q < groups; ++q) sum += s_sum[q * L * V * P + c];
-            if (gridDim.x == 1)
-                store_param<WB>(which == 0 ? a.d_weight : a.d_bias, c, sum);
-            else
-                parts[(static_cast<int64_t>(blockIdx.x) * 2 + which) * a.hidden + c] = sum;
+                s_sum[which][u][i / 4][threadIdx.x][i % 4] = which == 0 ? dw[u][i] : db[u][i];
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        const int c0 = u * L * P, end = min(L * P, a.hidden - c0);
+        for (int c = threadIdx.x; c < end; c += blockDim.x) {
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                float sum = 0.0f;
+                for (int q = 0; q < groups; ++q) sum += s_sum[which][u][c % P / 4][q * L + c / P][c % 4];
+                if (gridDim.x == 1)
+                    store_param<WB>(which == 0 ? a.d_weight : a.d_bias, c0 + c, sum);
+                else
+                    parts[(static_cast<int64_t>(blockIdx.x) * 2 + which) * a.hidden + c0 + c] = sum;
+            }
         }
     }
 }
@@ -388,17 +413,17 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void norm_join_kernel(const floa
     float s = 0.0f;
     if (i < 2 * H) {
         const float* from = parts + i;
-        int p = wave;
         // eight parts on their way at a time
-        for (; p + 7 * kJoinWaves < n; p += 8 * kJoinWaves) {
+        for (int p = wave; p < n; p += 8 * kJoinWaves) {
             float v[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                v[q] = from[static_cast<int64_t>(p + q * kJoinWaves) * 2 * H];
+            for (int q = 0; q < 8; ++q) {
+                const int at = p + q * kJoinWaves;
+                v[q] = at < n ? from[static_cast<int64_t>(at) * 2 * H] : 0.0f;
+            }
 #pragma unroll
             for (int q = 0; q < 8; ++q) s += v[q];
         }
-        for (; p < n; p += kJoinWaves) s += from[static_cast<int64_t>(p) * 2 * H];
     }
     s_sum[wave][lane] = s;
     __syncthreads();
@@ -474,7 +499,11 @@ hipError_t launch_norm_grad_types(const NormGradArgs& a, void* workspace, hipStr
             // Few rows: one workgroup, whose sums are the gradients (one row of 7168: 9.7 us,
             // 12.3 with a second launch; four turns of two rows: 19 and 11.5).  Without them there is no
             // second launch to save (four rows: 6.5, by one workgroup 9.6).
-            n = turns <= 2 && params ? 1 : turns < most ? turns : most;
+            // Otherwise as many workgroups as take their turns in the time of the fullest: a last turn
+            // of a few would leave as many parts (264 x 6712 fp32: 132 workgroups 16.2 us, 256 19.3;
+            // 6278 x 4096 bf16: 242 45.1, 256 48.0).
+            const int rounds = (turns + most - 1) / most;
+            n = turns <= 2 && params ? 1 : (turns + rounds - 1) / rounds;
             hipLaunchKernelGGL(kernel, dim3(n), dim3(groups * L), 0, stream, a, L, parts);
             if (n == 1) joined = true;
         };
