@@ -69,8 +69,11 @@ struct Stage {
 // Few rows per expert: the weights are the traffic and are read once.  A
 // workgroup takes 64 weight rows of one expert against up to 16 rows; its WAVES
 // waves take steps of 128 channels in turns and add their sums in LDS.  A load
-// covers 8 weight rows x 128 bytes, whole cache lines that are not kept; two
-// chunks change places across lanes afterwards (pair_chunks).  GATED: tiles 0, 1 are
+// covers 8 weight rows x 128 bytes; two chunks change places across lanes afterwards
+// (pair_chunks).  ONCE: K is a multiple of 128, so that these are whole cache lines, which
+// are not kept; else two steps share lines, and not keeping them would read
+// those twice (17 tokens over 32 experts, K 2672, N 7117: 86 us, not kept 101; decode batch, K 2048,
+// N 7168: 568, kept 628).  GATED: tiles 0, 1 are
 // rows n of the gate half and tiles 2, 3 rows N + n.
 //
 // Reading the weights bounds it.  128 tokens over 256 experts, top-8: K 7168, N 2048
@@ -78,7 +81,7 @@ struct Stage {
 // four waves; one token, K 7168, N 2048 gated: 40 us, 5.9 TB/s.  Two waves take 37 there but
 // 141 where four take 123 (64 experts of 8 rows, K 4096, N 1408 gated), and 18
 // where four take 12 (32 of 6, K 4096, N 167).
-template <int WAVES, bool GATED>
+template <int WAVES, bool GATED, bool ONCE>
 __global__ __launch_bounds__(WAVES* kWave, 4) void expert_i8_kernel(Args a) {
     constexpr int kThreads = WAVES * kWave;
     constexpr int MC = 16;
@@ -117,7 +120,7 @@ __global__ __launch_bounds__(WAVES* kWave, 4) void expert_i8_kernel(Args a) {
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                s.w[i][t] = load16<true>(t * 16 < kOut ? w_view : up_view,
+                s.w[i][t] = load16<ONCE>(t * 16 < kOut ? w_view : up_view,
                                          at + (t * 16 % kOut + i * 8) * K, c);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -173,8 +176,10 @@ __global__ __launch_bounds__(WAVES* kWave, 4) void expert_i8_kernel(Args a) {
 // weights and, at XT = 4, two of rows, 160 KB in all.  Weights, which mostly come
 // from HBM, are loaded two stages ahead, rows, which other workgroups of the XCD
 // read as well, one.  (Loads alone at XT 2, 8192 skewed tokens over 64 experts: 721 us one
-// stage ahead, 515 two.)  Up to XT 2 an expert mostly has one row tile, so its
-// weights are not kept in the caches (24 rows each: 140 us, kept 151).
+// stage ahead, 515 two.)  ONCE: up to XT 2 an expert mostly has one row tile, so its
+// weights are not kept in the caches (24 rows each: 140 us, kept 151), unless two stages share
+// cache lines (K 3872, no multiple of 128, N 535 gated, 21 rows each of 256 experts: 233,
+// not kept 271).
 //
 // That batch, K 4096, N 1408 gated: 559 to 573 us, 2.0 POP/s; 49152 rows of one expert
 // 2.35 POP/s; an 8192^3 int8 library product 2.06.  LDS and the matrix cores bound it
@@ -196,7 +201,7 @@ __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t from, u32x4* to,
         16, at, step, 0, ONCE ? 2 : 0);
 }
 
-template <int XT, bool GATED>
+template <int XT, bool GATED, bool ONCE>
 __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Args a) {
     constexpr int MC = 64 * XT;
     constexpr int kOut = GATED ? kTileW / 2 : kTileW;  // outputs of a workgroup
@@ -256,7 +261,7 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
         const bool has = c + piece < K;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            load_lds<XT != 4>(w_view, &s_w[(buf * kTileW + wave * 32 + i * 8) * 8],
+            load_lds<ONCE>(w_view, &s_w[(buf * kTileW + wave * 32 + i * 8) * 8],
                      has ? w_at + i * 8 * K : kNowhere, c);
     };
     const auto load_x = [&](uint32_t c, int buf) {
@@ -421,23 +426,24 @@ __global__ __launch_bounds__(kTileWaves* kWave, 2) void expert_i8_tile_kernel(Ar
     }
 }
 
-template <int XT, bool GATED>
+template <int XT, bool GATED, bool ONCE>
 void launch_many(const Args& a, int64_t tiles, hipStream_t stream) {
     const int outs = GATED ? kTileW / 2 : kTileW;
     const int64_t blocks = (a.N + outs - 1) / outs;
     const int64_t items = (tiles * blocks + 7) / 8 * 8;  // a row of ids whose length 8 divides
     const int64_t x = items < (1 << 20) ? items : 1 << 20;
     const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>((items + x - 1) / x));
-    hipLaunchKernelGGL((expert_i8_tile_kernel<XT, GATED>), grid, dim3(kTileWaves * kWave), 0, stream, a);
+    hipLaunchKernelGGL((expert_i8_tile_kernel<XT, GATED, ONCE>), grid, dim3(kTileWaves * kWave), 0,
+                       stream, a);
 }
 
-template <int WAVES, bool GATED>
+template <int WAVES, bool GATED, bool ONCE>
 void launch_few(const Args& a, int64_t tiles, hipStream_t stream) {
     const int outs = GATED ? kRows / 2 : kRows;
     const int64_t y = tiles < 32768 ? tiles : 32768;
     const dim3 grid((a.N + outs - 1) / outs, static_cast<unsigned>(y),
                     static_cast<unsigned>((tiles + y - 1) / y));
-    hipLaunchKernelGGL((expert_i8_kernel<WAVES, GATED>), grid, dim3(WAVES * kWave), 0, stream, a);
+    hipLaunchKernelGGL((expert_i8_kernel<WAVES, GATED, ONCE>), grid, dim3(WAVES * kWave), 0, stream, a);
 }
 
 int64_t padded(int64_t bytes) { return (bytes + 255) / 256 * 256; }
@@ -487,40 +493,54 @@ hipError_t launch_expert_i8(const ep_problem& p, const ep_expert_i8_t& mm, const
     // full tile.
     const int64_t experts = p.num_experts < filled ? p.num_experts : filled;
     const int64_t mean = filled / experts;
-    const auto tiles = [&](int mc) { return experts + filled / mc; };
-    // By the mean rows of an expert, measured at 64 experts, K 4096, N 1408 gated (us):
+    const auto tiles = [&](int64_t mc) {
+        const int64_t most = experts + filled / mc;
+        const int64_t held_tiles = p.num_experts * ((p.capacity + mc - 1) / mc);
+        return p.capacity > 0 && held_tiles < most ? held_tiles : most;
+    };
+    // Few rows: up to a mean of 12 (64 experts, K 4096, N 1408 gated, rows each, us:
     //   rows   8    12   16   24   48   64   75   96   112  121  128
     //   few    122  135  168  231  379
     //   XT 1   127  137  128  140  139  163  192
     //   XT 2   128  138  129  142  140  146  153  156  168  183  215
-    //   XT 4                                 162  162  177  172  180
-    // Larger row tiles and the many-row kernel's 256 weight rows make fewer
-    // workgroups.  Where they do not give nearly every CU one, the next smaller tile
-    // wins (8 experts, K 4096: N 704 gated, 250 rows each: 90 workgroups of XT 4 49 us,
-    // 138 of XT 2 35, 234 of XT 1 29; 1000 rows each: 234 of XT 4 53, XT 2 68), and the
-    // few-row kernel where the CUs hold all of its workgroups at once (32 experts of 25
+    //   XT 4                                 162  162  177  172  180),
+    // and where the CUs hold all of the few-row kernel's workgroups at once (32 experts of 25
     // rows, N 167: 246 of them 14 us, XT 1 22; 8 of 16, K 2048, N 1024: 256, 9 and 15;
     // 32 of 100, N 167: 696, 35 and 24).
+    // Of the many-row kernel's tiles those whose rounds over 256 CUs cost the least; a
+    // workgroup of XT 1, 2, 4 takes as 10, 12, 16 do (8 experts of 250 rows, K 4096, N 704 gated, one
+    // round each: 29, 35 and 49 us; of 1000 rows two rounds of XT 2 68, one of XT 4 53; 32 of 237,
+    // K 7120, N 946: two rounds of XT 1 169, one of XT 2 121, of XT 4 148, half of its CUs idle).
+    // Half a tile per expert is taken to be empty.
     const int64_t rows2 = static_cast<int64_t>(a.N) * (mm.activation == 1 ? 2 : 1);
-    const auto workgroups = [&](int mc, int w_rows) {
-        return tiles(mc) * ((rows2 + w_rows - 1) / w_rows);
+    const auto rounds = [&](int64_t mc) {
+        int64_t n = experts / 2 + filled / mc;
+        if (n < experts) n = experts;
+        if (n > tiles(mc)) n = tiles(mc);
+        return (n * ((rows2 + kTileW - 1) / kTileW) + 255) / 256;
     };
-    constexpr int kEnough = 200;
-    const auto go = [&](auto gated) {
-        constexpr bool kGated = decltype(gated)::value;
-        if (mean <= 12 || workgroups(16, kRows) <= 512)
-            launch_few<4, kGated>(a, tiles(16), stream);
-        else if (mean > 116 && workgroups(256, kTileW) >= kEnough)
-            launch_many<4, kGated>(a, tiles(256), stream);
-        else if (mean > 48 && workgroups(128, kTileW) >= kEnough)
-            launch_many<2, kGated>(a, tiles(128), stream);
+    const int64_t cost1 = 10 * rounds(64), cost2 = 12 * rounds(128), cost4 = 16 * rounds(256);
+    const auto go = [&](auto gated, auto once) {
+        constexpr bool kGated = decltype(gated)::value, kOnce = decltype(once)::value;
+        if (mean <= 12 || tiles(16) * ((rows2 + kRows - 1) / kRows) <= 512)
+            launch_few<4, kGated, kOnce>(a, tiles(16), stream);
+        else if (cost1 <= cost2 && cost1 <= cost4)
+            launch_many<1, kGated, kOnce>(a, tiles(64), stream);
+        else if (cost2 <= cost4)
+            launch_many<2, kGated, kOnce>(a, tiles(128), stream);
         else
-            launch_many<1, kGated>(a, tiles(64), stream);
+            launch_many<4, kGated, false>(a, tiles(256), stream);
     };
-    if (mm.activation == 1)
-        go(std::true_type{});
+    const auto go_once = [&](auto once) {
+        if (mm.activation == 1)
+            go(std::true_type{}, once);
+        else
+            go(std::false_type{}, once);
+    };
+    if (a.K % kStep == 0)
+        go_once(std::true_type{});
     else
-        go(std::false_type{});
+        go_once(std::false_type{});
     return hipGetLastError();
 }
 
