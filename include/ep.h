@@ -475,7 +475,8 @@ typedef struct ep_expert_i8_t {
     int32_t in_format;     /* rows: 0 bf16 (finite), quantised by the call as above;
                               1 int8 with one scale per row */
     int32_t activation;    /* 0: out = y, weights [E, N, K].
-                              1: out = silu(gate) * up, weights [E, 2N, K], as ep_expert_w4_t */
+                              1: out = silu(gate) * up, weights [E, 2N, K], as ep_expert_w4_t;
+                              silu is rounded to fp32, its subnormal values among them */
 } ep_expert_i8_t;
 
 /* Bytes of device workspace ep_expert_i8 needs (0 for in_format 1), or -1 if the
