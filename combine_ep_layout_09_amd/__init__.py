@@ -829,7 +829,7 @@ def _layer_norm_args(nm, x, weight, bias, y, mean, rstd):
     xp, stride = _rows_arg(x, "x", nm, x.dtype, dev)
     param = weight if weight is not None else bias
     if param is not None:
-        w_bf16 = _is_bf16(param, "weight")
+        w_bf16 = _is_bf16(param, "weight" if weight is not None else "bias")
         if weight is not None:
             wp = _arg(weight, "weight", param.dtype, (H,), dev)
         if bias is not None:
@@ -875,9 +875,9 @@ def _layer_norm_backward_args(nm, x, dy, weight, mean, rstd, dx, d_weight, d_bia
     dev = _device_of(x, "x")
     T, H = nm.num_tokens, nm.hidden
     x_bf16, x_dtype, w_bf16, w_dtype = _is_bf16(x, "x"), x.dtype, 0, torch.float32
-    for param in (weight, d_weight, d_bias):
+    for param, name in ((weight, "weight"), (d_weight, "d_weight"), (d_bias, "d_bias")):
         if param is not None:
-            w_bf16, w_dtype = _is_bf16(param, "weight"), param.dtype
+            w_bf16, w_dtype = _is_bf16(param, name), param.dtype
             break
     xp, x_stride = _rows_arg(x, "x", nm, x_dtype, dev)
     gp, g_stride = _rows_arg(dy, "dy", nm, x_dtype, dev)
