@@ -306,16 +306,15 @@ __global__ __launch_bounds__(kMaxThreads) void norm_grad_kernel(NormGradArgs a, 
 }
 
 // Rows longer than 2048 pieces, whose sums over tokens do not fit the registers.
-// Gradient of the rows: a group of L lanes takes a row, reads it once for the two means
-// and once more for dx.
+// Gradient of the rows: a workgroup, of 512 or 1024 lanes at these lengths, takes a row,
+// reads it once for the two means and once more for dx.
 template <bool XB, bool WB>
-__global__ __launch_bounds__(kMaxThreads) void norm_rows_kernel(NormGradArgs a, int L) {
+__global__ __launch_bounds__(kMaxThreads) void norm_rows_kernel(NormGradArgs a) {
     typedef Piece<XB> X;
     constexpr int P = X::P;
     __shared__ float s_part[2][kMaxThreads / kWave];
-    const int group = threadIdx.x / L, l = threadIdx.x % L;
-    const int waves = L / kWave, wave0 = group * waves, wave = threadIdx.x / kWave;
-    const int64_t t = block_number() * (blockDim.x / L) + group;
+    const int l = threadIdx.x, L = blockDim.x;
+    const int64_t t = block_number();
     const bool there = t < a.num_tokens;
     typedef typename X::T T;
     const int H = a.hidden;
@@ -337,8 +336,8 @@ __global__ __launch_bounds__(kMaxThreads) void norm_rows_kernel(NormGradArgs a, 
             c2 = fmaf(v, (x.at(i) - m) * r, c2);
         }
     }
-    c1 = group_sum(c1, s_part[0], wave0, waves, wave) / a.hidden;
-    c2 = group_sum(c2, s_part[1], wave0, waves, wave) / a.hidden;
+    c1 = workgroup_sum(c1, s_part[0]) / a.hidden;
+    c2 = workgroup_sum(c2, s_part[1]) / a.hidden;
     const auto out = row_view<T>(a.dx, t, H, H, there);
     const auto skip = row_view<T>(a.d_skip, t, H, H, there);
     for (int c = l * P; c < H; c += L * P) {
@@ -512,10 +511,8 @@ hipError_t launch_norm_grad_types(const NormGradArgs& a, void* workspace, hipStr
         else
             go(norm_grad_kernel<XB, WB, 2, 1>, 1);
     } else if (a.num_tokens > 0) {
-        const int L = lanes_per_row(pieces, 8, a.num_tokens);
-        const int rows = L < 256 ? 256 / L : 1;
-        hipLaunchKernelGGL((norm_rows_kernel<XB, WB>), grid_of((a.num_tokens + rows - 1) / rows),
-                           dim3(rows * L), 0, stream, a, L);
+        hipLaunchKernelGGL((norm_rows_kernel<XB, WB>), grid_of(a.num_tokens),
+                           dim3(lanes_per_row(pieces, 8, a.num_tokens)), 0, stream, a);
         if (params) {
             const int run = (a.num_tokens + most - 1) / most;
             n = (a.num_tokens + run - 1) / run;

@@ -152,20 +152,19 @@ __device__ __forceinline__ float wave_sum(float v) {
     return (lane(0) + lane(16)) + (lane(32) + lane(48));
 }
 
-// Sum over the `waves` waves from wave0 on, which call it together with the
-// whole workgroup; parts: one float per wave of the workgroup, not used since the
-// last barrier.
-__device__ __forceinline__ float group_sum(float v, float* parts, int wave0, int waves, int wave) {
+// Sum over the workgroup's waves; parts: one float per wave, not used since the last
+// barrier.
+__device__ __forceinline__ float workgroup_sum(float v, float* parts) {
     v = wave_sum(v);
-    if (waves == 1) return v;
-    if (threadIdx.x % kWave == 0) parts[wave] = v;
+    if (threadIdx.x % kWave == 0) parts[threadIdx.x / kWave] = v;
     __syncthreads();
     float s = 0.0f;
-    for (int i = 0; i < waves; ++i) s += parts[wave0 + i];
+    for (int i = 0; i < static_cast<int>(blockDim.x) / kWave; ++i) s += parts[i];
     return s;
 }
 
-// The same for B values; parts: B floats per wave.
+// Sums of B values over the `waves` waves from wave0 on, which call it together with the
+// whole workgroup; parts: B floats per wave of the workgroup, not used since the last barrier.
 template <int B>
 __device__ __forceinline__ void group_sums(float (&v)[B], float (*parts)[16], int wave0, int waves,
                                            int wave) {
