@@ -188,17 +188,20 @@ __global__ __launch_bounds__(WAVES* kWave, 4) void expert_i8_kernel(Args a) {
 // weights and, at XT = 4, two of rows, 160 KB in all.  Weights, which mostly come
 // from HBM, are loaded two stages ahead, rows, which other workgroups of the XCD
 // read as well, one.  (Loads alone at XT 2, 8192 skewed tokens over 64 experts: 721 us one
-// stage ahead, 515 two.)  ONCE: up to XT 2 an expert mostly has one row tile, so its
-// weights are not kept in the caches (24 rows each: 140 us, kept 151), unless two stages share
-// cache lines (K 3872, no multiple of 128, N 535 gated, 21 rows each of 256 experts: 233,
-// not kept 271).
+// stage ahead, 515 two.)  ONCE: up to XT 2 weights are not kept in the caches, which is
+// faster where an expert has one row tile (64 experts, K 4096, N 1408 gated, 24 rows each: 134 us,
+// kept 145; 64 rows 148 and 152), unless two stages share cache lines (K 3872, no multiple of
+// 128, N 535 gated, 21 rows each of 256 experts: 233, not kept 271).  Where an expert has
+// several, either side is ahead by case: 8 experts of 250 rows, K 4096, N 1408 gated 37.4, kept
+// 39.8, 32 of 250 121 and 125, but 16 of 200, not gated, 41.7 and 38.5, 32 of 237 with as
+// large a capacity, K 7168, N 946, 77.8 and 71.9.
 //
-// That batch, K 4096, N 1408 gated: 559 to 573 us, 2.0 POP/s; 49152 rows of one expert
+// That batch, K 4096, N 1408 gated: 540 to 590 us by box, 1.9 to 2.1 POP/s; 49152 rows of one expert
 // 2.35 POP/s; an 8192^3 int8 library product 2.06.  LDS and the matrix cores bound it
 // together: fragments and stages take LDS as many cycles as the products take them, which
 // are busy for 47 % of the time, at 2.0 to 2.1 GHz (435 us without loads, 449 without
-// products).  4096 tokens over 256 experts, K 7168, N 2048 gated: 1483 us, the
-// weights at 5.3 TB/s.  Slower were matrix instructions of 32 x 32 x 32 (625 where this
+// products).  4096 tokens over 256 experts, K 7168, N 2048 gated: 1463 to 1512 us, 5.2 to 5.4 TB/s
+// with rows and outputs, 5.0 to 5.1 of weights.  Slower were matrix instructions of 32 x 32 x 32 (625 where this
 // took 566), a stage through registers (648 where this took 596) and four waves of
 // 128 x 128 (637 where this took 600).
 constexpr int kTileWaves = 8;

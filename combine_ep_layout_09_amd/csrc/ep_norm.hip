@@ -123,8 +123,9 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a, int L) {
 //
 // Memory bounds it: 4096 x 7168 bf16 with d_skip 49.5 us for both kernels, 4.75 TB/s of what the
 // call has to move and 7 % more in parts (a single group's sums through LDS as well: 52); 86 with
-// the rows read a second time for the sums over tokens.  1999 x 1409 fp32: 12.9 us, of which the
-// host's two launches are 12.
+// the rows read a second time for the sums over tokens.  1999 x 1409 fp32: 12.9 us for both, which by
+// themselves take 10.6 and 3.8: starts and ends, 7.1 of bytes.  More than 8192 bf16 channels leave
+// CUs without a workgroup (norm_parts): 4096 x 12288 98 us, 4.1 TB/s, 4096 x 16384 137, 3.9.
 
 // Sums of B pairs of values over the lanes of a group; parts: B pairs per wave.
 template <int B>
@@ -527,7 +528,8 @@ hipError_t launch_norm_grad_types(const NormGradArgs& a, void* workspace, hipStr
 }  // namespace
 
 // Partial sums of the gradients of weight and bias: at most one per CU, and at
-// most 2^21 channels of them.
+// most 2^21 channels of them (16 MB).  As many workgroups make them at most, with those sums or
+// without: 170 for rows of 12288 channels, 128 for 16384.
 int norm_parts(int num_tokens, int hidden) {
     int n = 256;
     if (n > (1 << 21) / hidden) n = (1 << 21) / hidden;

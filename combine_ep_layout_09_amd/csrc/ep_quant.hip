@@ -102,7 +102,8 @@ hipError_t launch_quant_rows(const ep_problem& p, int K, const void* rows,
     if (entries == 0) return hipSuccess;
     const int nvec = K / 8;
     const int threads = lanes_of(nvec, 2);
-    // enough workgroups for every row of the mean, up to 2^20 / E per expert
+    // a workgroup per row, up to 2^20; with a capacity twice as many per expert as it has rows
+    // in the mean, up to 1024
     dim3 grid;
     if (p.capacity > 0) {
         int64_t per = 2 * (entries / p.num_experts) + 1;

@@ -337,9 +337,10 @@ typedef struct ep_expert_w4_t {
     int32_t in_format;     /* rows: 0 bf16; 1, 2 E4M3FN with the block scales that
                               ep_problem.use_fp8 = 1, 2 names */
     int32_t activation;    /* 0: out = y, weights [E, N, K].
-                              1: out = silu(gate) * up with silu(v) = v / (1 + exp(-v));
-                              weights [E, 2N, K], rows n and N + n of an expert giving gate
-                              and up of output n */
+                              1: out = silu(gate) * up with silu(v) = v / (1 + exp(-v)),
+                              0 where exp(-v) is beyond fp32 (v below -88.7); weights
+                              [E, 2N, K], rows n and N + n of an expert giving gate and
+                              up of output n */
 } ep_expert_w4_t;
 
 /* out[r, n] = sum_k rows[r, k] * weight[e, n, k] for every receive row r that
@@ -461,7 +462,8 @@ int ep_combine_backward(const ep_problem* prob, const void* dy, const void* expe
  * amax = 0 gives scale 0 and codes 0. */
 
 /* Dispatch as ep_dispatch, with 8-bit integer rows and one scale per token.
- *   prob         use_fp8 is not read beyond the common checks.
+ *   prob         use_fp8 is not read beyond the common checks.  H is a multiple of 8, as
+ *                everywhere; rows that ep_expert_i8 is to take need a multiple of 16.
  *   recv_q       int8 [R, H], device.
  *   recv_scales  fp32 [R], device, at its own alignment.
  * Receive rows that no entry fills are not written.  x must be finite.  T at most 2^21.
@@ -475,8 +477,9 @@ typedef struct ep_expert_i8_t {
     int32_t in_format;     /* rows: 0 bf16 (finite), quantised by the call as above;
                               1 int8 with one scale per row */
     int32_t activation;    /* 0: out = y, weights [E, N, K].
-                              1: out = silu(gate) * up, weights [E, 2N, K], as ep_expert_w4_t;
-                              silu is rounded to fp32, its subnormal values among them */
+                              1: out = silu(gate) * up, weights [E, 2N, K], as ep_expert_w4_t,
+                              but silu is rounded to fp32 at every gate, to its subnormal
+                              values too */
 } ep_expert_i8_t;
 
 /* Bytes of device workspace ep_expert_i8 needs (0 for in_format 1), or -1 if the
